@@ -25,7 +25,6 @@ own = False
 _TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
 
 
-
 # ------------------------------------------------------------------ cases
 def listed():
     return [
@@ -425,16 +424,19 @@ def _exact_cache(s, case, name, new, lens, where):
     rows = _rows64(s, name)
     x = s[name].double()
     if case["quant"]:
+        def two_to(e):  # built from its bits: a power function may be off in the last place
+            return ((e.long() + 1023) << 52).view(torch.float64)
+
         # the smallest power of two that keeps the row within +-448, then the nearest value of
         # the 4-bit significand's grid (spacing 2^(exponent - 3), not below 2^-9), ties to even
         top = x.abs().amax(-1, keepdim=True)
         lo, hi = (-15, 8) if case["dtype"] == "fp16" else (-126, 119)
         power = torch.ceil(torch.log2((top / 448.0).clamp(min=2.0 ** -300)))
-        power = power - (top <= 224.0 * 2.0 ** power).double()        # where the logarithm fell just above
-        power = (power + (top > 448.0 * 2.0 ** power).double()).clamp(lo, hi)
-        y = x * 2.0 ** -power
-        spacing = 2.0 ** ((torch.frexp(y).exponent - 1).clamp(min=-6) - 3).double()
-        x = torch.round(y / spacing) * spacing * 2.0 ** power
+        power = power - (top <= 224.0 * two_to(power)).double()       # where the logarithm fell just above
+        power = (power + (top > 448.0 * two_to(power)).double()).clamp(lo, hi)
+        y = x * two_to(-power)
+        spacing = two_to((torch.frexp(y).exponent - 1).clamp(min=-6) - 3)
+        x = torch.round(y / spacing) * spacing * two_to(power)
     at = 0
     out = []
     for b, (n, m) in enumerate(zip(new, lens)):
