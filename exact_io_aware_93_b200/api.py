@@ -23,6 +23,7 @@ _lib = None
 FA_STATUS = {
     0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_ALIGNMENT",
     4: "FA_ERR_DEVICE", 5: "FA_ERR_LAUNCH", 6: "FA_ERR_TIMEOUT", 7: "FA_ERR_WORKSPACE", 8: "FA_ERR_BOUNDS",
+    9: "FA_ERR_PLAN",
 }
 
 
@@ -41,6 +42,23 @@ class FaDecodeProblem(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("H_kv", ctypes.c_int), ("N_q", ctypes.c_int),
                 ("N_kv", ctypes.c_int), ("d", ctypes.c_int), ("scale", ctypes.c_float),
                 ("causal", ctypes.c_int), ("window", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class FaRopeProblem(ctypes.Structure):
+    """The ``fa_rope_problem`` descriptor of include/fa.h."""
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("H", ctypes.c_int), ("H_k", ctypes.c_int),
+                ("d", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("inverse", ctypes.c_int), ("factor", ctypes.c_float), ("dtype", ctypes.c_int),
+                ("pos64", ctypes.c_int), ("q_stride", ctypes.c_longlong * 3), ("k_stride", ctypes.c_longlong * 3),
+                ("q_out_stride", ctypes.c_longlong * 3), ("k_out_stride", ctypes.c_longlong * 3),
+                ("pos_stride", ctypes.c_longlong * 2)]
+
+
+class FaCacheProblem(ctypes.Structure):
+    """The ``fa_cache_problem`` descriptor of include/fa.h."""
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H_kv", ctypes.c_int), ("d", ctypes.c_int),
+                ("P", ctypes.c_int), ("max_pages", ctypes.c_int), ("page", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("quant", ctypes.c_int), ("k_stride", ctypes.c_longlong * 2), ("v_stride", ctypes.c_longlong * 2)]
 
 
 class FAError(RuntimeError):
@@ -97,6 +115,12 @@ def lib() -> ctypes.CDLL:
     L.fa_decode_workspace_size.restype = ctypes.c_size_t
     L.fa_decode.argtypes = [ctypes.POINTER(FaDecodeProblem), vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
     L.fa_decode.restype = i
+    L.fa_rope.argtypes = [ctypes.POINTER(FaRopeProblem), vp, vp, vp, vp, vp, vp, vp]
+    L.fa_rope.restype = i
+    L.fa_cache_append.argtypes = [ctypes.POINTER(FaCacheProblem)] + [vp] * 10
+    L.fa_cache_append.restype = i
+    L.fa_cache_gather.argtypes = [ctypes.POINTER(FaCacheProblem)] + [vp] * 11
+    L.fa_cache_gather.restype = i
     _lib = L
     return L
 
@@ -304,6 +328,217 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if st != 0:
         raise FAError(st, "fa_decode")
     return out, lse
+
+
+def _check_heads(name: str, t: torch.Tensor, like: torch.Tensor | None = None) -> None:
+    """A [.., heads, d] tensor of a 16-bit type on the GPU with contiguous columns (any other
+    strides), of ``like``'s type and device."""
+    if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [tokens, heads, d] or [batch, seq_len, heads, d]")
+    if t.dtype not in (torch.bfloat16, torch.float16) or (like is not None and t.dtype != like.dtype):
+        raise TypeError(f"{name} must be bfloat16 or float16, one type for all, got {t.dtype}")
+    if not t.is_cuda or (like is not None and t.device != like.device):
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path), one device for all")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name} must have contiguous columns")
+
+
+def _span(t: torch.Tensor) -> tuple[int, int]:
+    last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _check_rope_out(name: str, out: torch.Tensor, x: torch.Tensor, *others: torch.Tensor) -> None:
+    """An output of rope: x's shape, no element twice, and either x itself or apart from it (a
+    partial overlap would be read after it is written)."""
+    _check_heads(name, out, x)
+    if out.shape != x.shape:
+        raise ValueError(f"{name} must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
+    reach = 1
+    for st, n in sorted((st, n) for n, st in zip(out.shape, out.stride()) if n > 1):
+        if st < reach:
+            raise ValueError(f"{name} must not overlap itself")
+        reach = st * (n - 1) + reach
+    if out.data_ptr() == x.data_ptr() and out.stride() == x.stride():
+        if any(t.data_ptr() == x.data_ptr() for t in others if t is not None):
+            raise ValueError(f"{name} must not be another input too")
+        return
+    for t in (x, *others):
+        if t is not None and _span(out)[0] < _span(t)[1] and _span(t)[0] < _span(out)[1]:
+            raise ValueError(f"{name} must be its input itself or lie apart from the inputs")
+
+
+def _strides3(t: torch.Tensor):
+    return (t.stride(0) if t.dim() == 4 else 0, t.stride(-3), t.stride(-2))
+
+
+def _rope(q, k, positions, inv_freq, interleaved, factor, q_out, k_out, inverse):
+    _check_heads("q", q)
+    if k is not None:
+        _check_heads("k", k, q)
+        if k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+            raise ValueError(f"k {tuple(k.shape)} does not fit q {tuple(q.shape)}")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    lead = tuple(q.shape[:-2])
+    if (not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64)
+            or positions.device != q.device or tuple(positions.shape) not in (lead, lead[-1:])):
+        raise ValueError(f"positions must be int32 or int64 of shape {lead} or {lead[-1:]} on {q.device}")
+    if (not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1
+            or inv_freq.device != q.device or not inv_freq.is_contiguous()
+            or not 1 <= inv_freq.numel() <= q.shape[-1] // 2):
+        raise ValueError(f"inv_freq must be a contiguous float64 vector of 1 to {q.shape[-1] // 2} entries on {q.device}")
+    given = (q_out, k_out)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    if given[0] is not None:
+        _check_rope_out("q_out", q_out, q, k)
+    if given[1] is not None:
+        _check_rope_out("k_out", k_out, k, q)
+    if q.numel() == 0 and (k is None or k.numel() == 0):
+        return q_out, k_out
+    B, N = (1, q.shape[0]) if q.dim() == 3 else (q.shape[0], q.shape[1])
+    none = (0, 0, 0)
+    p = FaRopeProblem(B, N, q.shape[-2], 0 if k is None else k.shape[-2], q.shape[-1], 2 * inv_freq.numel(),
+                      int(bool(interleaved)), int(inverse), float(factor), FA_DTYPE[q.dtype],
+                      int(positions.dtype == torch.int64), _strides3(q), none if k is None else _strides3(k),
+                      _strides3(q_out), none if k is None else _strides3(k_out),
+                      (positions.stride(0) if positions.dim() == 2 else 0, positions.stride(-1)))
+    with _on(q):
+        st = lib().fa_rope(ctypes.byref(p), q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+                           None if k is None else k_out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
+                           _stream_ptr(q))
+    if st != 0:
+        raise FAError(st, "fa_rope")
+    return q_out, k_out
+
+
+def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,
+         interleaved: bool = False, factor: float = 1.0, q_out: torch.Tensor | None = None,
+         k_out: torch.Tensor | None = None):
+    """(q, k) rotated by their positions via ``fa_rope``: pair j of the first 2 * len(inv_freq)
+    columns of every head turns by position * inv_freq[j] and is scaled by ``factor``; the other
+    columns are copied.  The pair is columns (j, j + len(inv_freq)), or (2j, 2j + 1) when
+    ``interleaved``.
+
+    q is [T, H, d] or [B, N, H, d] and k the same with its own heads (or None), bfloat16 or
+    float16, with any strides but contiguous columns (slices of a fused projection).
+    ``positions`` is int32 or int64 of the leading shape, or [N] for every batch row;
+    ``inv_freq`` is float64 (``rotary.rope_frequencies``).  Outputs may be the inputs themselves."""
+    return _rope(q, k, positions, inv_freq, interleaved, factor, q_out, k_out, False)
+
+
+def rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,
+             interleaved: bool = False, factor: float = 1.0, q_grad: torch.Tensor | None = None,
+             k_grad: torch.Tensor | None = None):
+    """The gradients of ``rope``'s inputs from those of its outputs (the transposed rotation), with
+    the arguments of the forward call."""
+    return _rope(dq, dk, positions, inv_freq, interleaved, factor, q_grad, k_grad, True)
+
+
+_SCALE_TYPES = (torch.float8_e8m0fnu, torch.uint8)
+
+
+def _check_pages(k_pages, v_pages, page_table, seqlens, k_scales, v_scales, dtype) -> bool:
+    """The tensors of a paged cache read or written as ``dtype``; True for an e4m3 pool."""
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4 or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor [pages, kv_heads, page, d]")
+    if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or k_pages.device != v_pages.device:
+        raise ValueError("k_pages and v_pages must have one shape, dtype and device")
+    quant = k_pages.dtype == torch.float8_e4m3fn
+    if not quant and k_pages.dtype != dtype:
+        raise TypeError(f"pages of {k_pages.dtype} do not fit {dtype} (pages are of that type, or float8_e4m3fn)")
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        if not quant and t is not None:
+            raise ValueError(f"{name} given for 16-bit pages")
+        if quant and (not isinstance(t, torch.Tensor) or t.dtype not in _SCALE_TYPES or t.device != k_pages.device
+                      or t.shape != k_pages.shape[:3] or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float8_e8m0fnu tensor of shape {tuple(k_pages.shape[:3])} "
+                             f"on {k_pages.device}")
+    if (not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.dtype != torch.int32
+            or page_table.device != k_pages.device or not page_table.is_contiguous()):
+        raise ValueError(f"page_table must be a contiguous int32 [sequences, pages] tensor on {k_pages.device}")
+    check_buffer("seqlens", seqlens, (page_table.shape[0],), torch.int32, k_pages.device)
+    return quant
+
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                 page_table: torch.Tensor, seqlens: torch.Tensor, cu_q: torch.Tensor,
+                 k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None) -> None:
+    """Write new keys and values [T, H_kv, d] into a paged cache via ``fa_cache_append``.
+
+    Sequence b owns rows cu_q[b] .. cu_q[b + 1] (int32 [B + 1]), the last of its seqlens[b]
+    positions (int32 [B], the new rows included); rows behind cu_q[B] are not written.  Position p
+    lies in page page_table[b, p // page] (int32 [B, max_pages]) at slot p % page of the pools
+    [P, H_kv, page, d].  Pools of float8_e4m3fn take codes with one power-of-two scale per row in
+    ``k_scales`` / ``v_scales`` (float8_e8m0fnu [P, H_kv, page]).  Everything but the shapes is read
+    on the device; bad positions and page numbers skip their row and set the status word."""
+    for name, t in (("k", k), ("v", v)):
+        _check_heads(name, t, k)
+        if t.dim() != 3 or t.shape != k.shape:
+            raise ValueError(f"{name} must be [tokens, kv_heads, d], k and v of one shape")
+    quant = _check_pages(k_pages, v_pages, page_table, seqlens, k_scales, v_scales, k.dtype)
+    P, H_kv, page, d = k_pages.shape
+    B, max_pages = page_table.shape
+    if k.device != k_pages.device or k.shape[1:] != (H_kv, d):
+        raise ValueError(f"k {tuple(k.shape)} does not fit pages {tuple(k_pages.shape)} on {k_pages.device}")
+    check_buffer("cu_q", cu_q, (B + 1,), torch.int32, k.device)
+    if k.shape[0] == 0:
+        return
+    p = FaCacheProblem(B, k.shape[0], H_kv, d, P, max_pages, page, FA_DTYPE[k.dtype], int(quant),
+                       (k.stride(0), k.stride(1)), (v.stride(0), v.stride(1)))
+    with _on(k):
+        st = lib().fa_cache_append(ctypes.byref(p), k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                   _ptr(k_scales), _ptr(v_scales), page_table.data_ptr(), seqlens.data_ptr(),
+                                   cu_q.data_ptr(), _stream_ptr(k))
+    if st != 0:
+        raise FAError(st, "fa_cache_append")
+
+
+def cache_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, seqlens: torch.Tensor,
+                 cu_k: torch.Tensor, total: int, starts: torch.Tensor | None = None,
+                 k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None,
+                 dtype: torch.dtype | None = None, k_out: torch.Tensor | None = None,
+                 v_out: torch.Tensor | None = None):
+    """(k, v) [total, H_kv, d] read back from a paged cache via ``fa_cache_gather``: row cu_k[b] + i is
+    position starts[b] + i of sequence b (``starts`` None: from 0).  Rows whose position is at or past
+    seqlens[b], and rows behind cu_k[B], are left as they were.  ``dtype`` is the type of the values
+    read from e4m3 pages (bfloat16 when not given); 16-bit pages are read as they are."""
+    if dtype is None:
+        is8 = isinstance(k_pages, torch.Tensor) and k_pages.dtype == torch.float8_e4m3fn
+        dtype = torch.bfloat16 if is8 or not isinstance(k_pages, torch.Tensor) else k_pages.dtype
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"dtype must be bfloat16 or float16, got {dtype}")
+    quant = _check_pages(k_pages, v_pages, page_table, seqlens, k_scales, v_scales, dtype)
+    P, H_kv, page, d = k_pages.shape
+    B, max_pages = page_table.shape
+    total = int(total)
+    if total < 0:
+        raise ValueError(f"total must not be negative, got {total}")
+    check_buffer("cu_k", cu_k, (B + 1,), torch.int32, k_pages.device)
+    if starts is not None:
+        check_buffer("starts", starts, (B,), torch.int32, k_pages.device)
+    shape = (total, H_kv, d)
+    k_out = torch.empty(shape, dtype=dtype, device=k_pages.device) if k_out is None else k_out
+    v_out = torch.empty(shape, dtype=dtype, device=k_pages.device) if v_out is None else v_out
+    check_buffer("k_out", k_out, shape, dtype, k_pages.device)
+    check_buffer("v_out", v_out, shape, dtype, k_pages.device)
+    if total == 0:
+        return k_out, v_out
+    p = FaCacheProblem(B, total, H_kv, d, P, max_pages, page, FA_DTYPE[dtype], int(quant), (0, 0), (0, 0))
+    with _on(k_pages):
+        st = lib().fa_cache_gather(ctypes.byref(p), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
+                                   _ptr(v_scales), page_table.data_ptr(), seqlens.data_ptr(), cu_k.data_ptr(),
+                                   _ptr(starts), k_out.data_ptr(), v_out.data_ptr(), _stream_ptr(k_pages))
+    if st != 0:
+        raise FAError(st, "fa_cache_gather")
+    return k_out, v_out
 
 
 def get_status(device: torch.device | None = None) -> int:

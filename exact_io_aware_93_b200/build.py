@@ -9,6 +9,7 @@ only the NVIDIA driver at run time.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import re
 import shutil
@@ -22,7 +23,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 # the same sources compiled with FA_CHECKS: every kernel bounds-checks its TMA coordinates
 # and global indices and reports a violation in the device status word (include/fa.h)
 CHECKS_LIB_PATH = os.path.join(PKG, "libfa_b200_checks.so")
-SOURCES = ["fa_api.cu"]
+SOURCES = ["fa_api.cu", "fa_cache.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -95,34 +96,56 @@ def check_register_contract(log: str) -> None:
         raise RuntimeError("register contract broken:\n  " + "\n  ".join(bad))
 
 
-def _build_one(path: str, defines, log_name: str, verbose: bool) -> None:
-    tmp = f"{path}.{os.getpid()}.tmp"
-    cmd = [_nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "-shared", "-Xcompiler", "-fPIC",
-           "-Xptxas", "-v", "-cudart", "static", *defines,
-           *[os.path.join(CSRC, s) for s in SOURCES], "-o", tmp]
+def _compile(src: str, obj: str, defines):
+    """One source to one object; (command, ptxas report) or a RuntimeError with nvcc's output."""
+    cmd = [_nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v", *defines,
+           "-c", os.path.join(CSRC, src), "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
+    return cmd, res.returncode, res.stdout + res.stderr
+
+
+def _build_one(path: str, defines, log_name: str, verbose: bool) -> None:
+    """Compile every source (at the same time, one nvcc each) and link the library."""
+    tmp = f"{path}.{os.getpid()}.tmp"
+    objs = [f"{tmp}.{s}.o" for s in SOURCES]
+    try:
+        with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
+            done = list(pool.map(lambda a: _compile(a[0], a[1], defines), zip(SOURCES, objs)))
+        if all(rc == 0 for _, rc, _ in done):
+            cmd = [_nvcc(), *ARCH, "-shared", "-cudart", "static", *objs, "-o", tmp]
+            res = subprocess.run(cmd, capture_output=True, text=True)
+            done.append((cmd, res.returncode, res.stdout + res.stderr))
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.unlink(o)
+    report = "".join(" ".join(cmd) + "\n" + text for cmd, _, text in done)
     log = os.path.join(PKG, log_name)
     with open(log, "w") as f:
-        f.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
-    if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed (see {log}):\n{res.stderr[-4000:]}")
+        f.write(report)
+    bad = [text for _, rc, text in done if rc != 0]
+    if bad:
+        raise RuntimeError(f"nvcc failed (see {log}):\n{bad[0][-4000:]}")
     try:
-        check_register_contract(res.stdout + res.stderr)
+        check_register_contract(report)
     except RuntimeError:
         os.unlink(tmp)
         raise
     os.replace(tmp, path)
     if verbose:
-        print(res.stderr)
+        print(report)
 
 
 def build(force: bool = False, verbose: bool = False, checks: bool = True) -> str:
     """Build the release library and (checks=True) the checking build; returns the release
     library's path."""
-    if force or not up_to_date(LIB_PATH):
-        _build_one(LIB_PATH, [], "build.log", verbose)
-    if checks and (force or not up_to_date(CHECKS_LIB_PATH)):
-        _build_one(CHECKS_LIB_PATH, ["-DFA_CHECKS"], "build_checks.log", verbose)
+    jobs = [(LIB_PATH, [], "build.log")]
+    if checks:
+        jobs.append((CHECKS_LIB_PATH, ["-DFA_CHECKS"], "build_checks.log"))
+    jobs = [j for j in jobs if force or not up_to_date(j[0])]
+    with concurrent.futures.ThreadPoolExecutor(max_workers=2) as pool:
+        for f in [pool.submit(_build_one, *j, verbose) for j in jobs]:
+            f.result()
     return LIB_PATH
 
 

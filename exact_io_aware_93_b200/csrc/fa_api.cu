@@ -12,60 +12,18 @@
 #include "fa_bwd_kernel.cuh"
 #include "fa_decode_kernel.cuh"
 #include "fa_fwd_kernel.cuh"
+#include "fa_host.h"
 #include "tma_host.h"
 
 // Device status word: [0] = first error code a kernel recorded, [1] = wait site.
 __device__ int g_fa_status[2];
 
-namespace {
+namespace fa {
 
-constexpr int kMaxDevices = 64;
+static DeviceInfo g_dev[kMaxDevices];
+static std::mutex g_dev_mutex;
 
-// Per-device set-up.  The first call on a device fills `ok`, `sm_count` and `status` under
-// g_dev_mutex and only then publishes `probed` (release); later calls read `probed`
-// (acquire) without the lock.  The kernel-attribute flags are set under the same mutex, so
-// first calls from several host threads at once are safe.
-struct DeviceInfo {
-  std::atomic<bool> probed{false};
-  bool ok = false;
-  int sm_count = 0;
-  int* status = nullptr;
-  bool fwd_attr[3][2][2] = {};  // [element type][d==128][causal]
-  bool bwd_attr[2][2][2] = {};
-  bool dec_attr[2][2][4] = {};  // [fp16][d==128][M = 128; M = 64 with 1, 2, 4 row copies]
-};
-DeviceInfo g_dev[kMaxDevices];
-std::mutex g_dev_mutex;
-
-// Runs `setup` (which returns true on success) once per flag, under g_dev_mutex.
-template <typename F>
-bool once_per_device(bool& flag, F setup) {
-  std::lock_guard<std::mutex> lock(g_dev_mutex);
-  if (!flag) {
-    if (!setup()) {
-      cudaGetLastError();
-      return false;
-    }
-    flag = true;
-  }
-  return true;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// The warp-specialised kernels move registers between warpgroups with setmaxnreg; the
-// split is computed for a launch at exactly fa::kLaunchRegs registers per thread.  The
-// build script fails when ptxas reports another count; this check refuses to launch a
-// library that was built some other way with a different count.
-template <typename K>
-bool launch_regs_ok(K kern, uint32_t expected) {
-  cudaFuncAttributes a;
-  if (cudaFuncGetAttributes(&a, kern) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  return a.numRegs == static_cast<int>(expected);
-}
+std::mutex& device_mutex() { return g_dev_mutex; }
 
 fa_status current_device(DeviceInfo** out) {
   int dev = -1;
@@ -93,6 +51,17 @@ fa_status current_device(DeviceInfo** out) {
   *out = &di;
   return FA_OK;
 }
+
+}  // namespace fa
+
+namespace {
+
+using fa::aligned;
+using fa::current_device;
+using fa::DeviceInfo;
+using fa::kMaxDevices;
+using fa::launch_regs_ok;
+using fa::once_per_device;
 
 fa_status check_problem(const fa_problem& p) {
   if (p.dtype != FA_DTYPE_BF16 && p.dtype != FA_DTYPE_F16 && p.dtype != FA_DTYPE_E4M3) return FA_ERR_UNSUPPORTED;
@@ -415,6 +384,7 @@ const char* fa_status_string(int s) {
     case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT";
     case FA_ERR_WORKSPACE: return "FA_ERR_WORKSPACE";
     case FA_ERR_BOUNDS: return "FA_ERR_BOUNDS";
+    case FA_ERR_PLAN: return "FA_ERR_PLAN";
     default: return "FA_ERR_UNKNOWN";
   }
 }

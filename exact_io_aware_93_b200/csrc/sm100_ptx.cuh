@@ -99,7 +99,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
 // skipped: a skipped TMA load leaves its barrier short of bytes, so the waiting role's bounded
 // wait runs out and the kernel unwinds.  Without FA_CHECKS the checks compile to nothing.
 #ifdef FA_CHECKS
-__device__ __noinline__ void bounds_fail(int* status, int site) {
+__device__ __noinline__ inline void bounds_fail(int* status, int site) {
   atomicCAS(status, 0, 8 /* FA_ERR_BOUNDS */);
   atomicCAS(status + 1, 0, site);
 }

@@ -54,7 +54,9 @@ typedef enum {
   FA_ERR_LAUNCH = 5,      /* kernel attribute setup or launch failed */
   FA_ERR_TIMEOUT = 6,     /* a kernel abandoned a bounded wait (reported by fa_get_status) */
   FA_ERR_WORKSPACE = 7,   /* workspace pointer NULL or smaller than the required size */
-  FA_ERR_BOUNDS = 8       /* checking build only: a kernel's index left its tensor (fa_get_status) */
+  FA_ERR_BOUNDS = 8,      /* checking build only: a kernel's index left its tensor (fa_get_status) */
+  FA_ERR_PLAN = 9         /* a device-side length, offset or page number of a paged call was out of
+                             range; the access was skipped (reported by fa_get_status) */
 } fa_status;
 
 /* Library ABI version (this header: 6; 6 added fa_get_status_site). */
@@ -277,6 +279,113 @@ size_t fa_decode_workspace_size(const fa_decode_problem* problem);
 fa_status fa_decode(const fa_decode_problem* problem, const void* q, const void* k_cache, const void* v_cache,
                     const int* seqlens, void* o, float* lse, void* workspace, size_t workspace_bytes,
                     void* stream);
+
+/*
+ * ---------------------------------------------------------------- rotary positions
+ * Rotates the first rotary_dim columns of every head of q and k by the token's position:
+ * pair j at position p, with angle t = p * inv_freq[j] (radians), becomes
+ *   (x0, x1) -> factor * (x0 cos t - x1 sin t, x1 cos t + x0 sin t);
+ * the other columns are copied.  The pair is columns (j, j + rotary_dim / 2), or, with
+ * interleaved = 1, columns (2j, 2j + 1).  inverse = 1 applies the transpose (t negated): the
+ * gradient of the forward call, and with factor 1 its inverse.  Angles are reduced in 64
+ * bits, so far positions keep their precision; products are fp32, rounded once.
+ *   B, N       : tokens, N for each of B batch rows (B = 1 for a flat list of N tokens)
+ *   H, H_k     : heads of q and of k; H_k = 0 with k = k_out = NULL rotates q alone
+ *   d          : columns per head, 2 .. 1024;  rotary_dim: even, 2 .. d
+ *   factor     : amplitude, finite (1 for none; long-context scalings set it)
+ *   dtype      : FA_DTYPE_BF16 or FA_DTYPE_F16
+ *   pos64      : 0: positions are int32, 1: int64
+ *   *_stride   : element strides of batch row, token and head (columns are contiguous)
+ *   pos_stride : element strides of the positions: batch row (0: shared) and token
+ */
+typedef struct fa_rope_problem {
+  int B;
+  int N;
+  int H;
+  int H_k;
+  int d;
+  int rotary_dim;
+  int interleaved;
+  int inverse;
+  float factor;
+  int dtype;
+  int pos64;
+  long long q_stride[3];
+  long long k_stride[3];
+  long long q_out_stride[3];
+  long long k_out_stride[3];
+  long long pos_stride[2];
+} fa_rope_problem;
+
+/*
+ *   q, k         : in,  [B, N, H, d] and [B, N, H_k, d] with the given strides
+ *   q_out, k_out : out, the same shapes; each may be its input (same pointer and strides),
+ *                  any other overlap is not supported
+ *   positions    : in,  DEVICE int32 / int64, any sign
+ *   inv_freq     : in,  DEVICE fp64 [rotary_dim / 2], radians per position
+ * Pointers need the alignment of their element; rows that are 16-byte aligned with d and
+ * rotary_dim multiples of 16 take the fast path.  Errors: FA_ERR_INVALID_ARG,
+ * FA_ERR_UNSUPPORTED (dtype), FA_ERR_ALIGNMENT, FA_ERR_DEVICE, FA_ERR_LAUNCH.
+ */
+fa_status fa_rope(const fa_rope_problem* problem, const void* q, const void* k, void* q_out, void* k_out,
+                  const void* positions, const double* inv_freq, void* stream);
+
+/*
+ * ---------------------------------------------------------------- paged key/value cache
+ * A pool of P pages for keys and one for values, each [P, H_kv, page, d] contiguous.
+ * Position p of sequence b lies in page page_table[b, p / page], slot p % page, of both.
+ *   16-bit pool (quant = 0): elements of `dtype`.
+ *   e4m3 pool   (quant = 1): e4m3 codes, with a power-of-two scale per (page, head, slot),
+ *               k_scales / v_scales [P, H_kv, page], one byte e + 127 each (the e8m0 code of
+ *               2^e); the value is code * 2^e.  fa_cache_append picks the smallest 2^e with
+ *               max|row| <= 448 * 2^e (kept within 2^-15 .. 2^8 for fp16, 2^-126 .. 2^119 for
+ *               bf16), so code * 2^e is exact in the 16-bit type; what lies past its largest
+ *               code takes that code (fp16 above 61440, bf16 above 448 * 2^119); infinities
+ *               and NaN become NaN and do not enter the maximum.
+ *   B          : sequences;  T: rows of k and v (or of the gathered output)
+ *   P          : pages in the pool;  max_pages: row length of page_table
+ *   page       : slots per page: 16, 32, 64, 128 or 256;  d: 64 or 128
+ *   k_stride, v_stride : element strides (token, head) of the new keys and values
+ */
+typedef struct fa_cache_problem {
+  int B;
+  int T;
+  int H_kv;
+  int d;
+  int P;
+  int max_pages;
+  int page;
+  int dtype;
+  int quant;
+  long long k_stride[2];
+  long long v_stride[2];
+} fa_cache_problem;
+
+/*
+ * Writes new keys and values into the cache.
+ *   k, v       : in,  [T, H_kv, d] with the given strides (16-byte aligned rows)
+ *   page_table : in,  DEVICE int32 [B, max_pages]
+ *   seqlens    : in,  DEVICE int32 [B]: cached length of each sequence, the new rows included
+ *   cu         : in,  DEVICE int32 [B + 1]: sequence b owns rows cu[b] .. cu[b + 1] - 1, its
+ *                     last positions: row cu[b] + i goes to position seqlens[b] - n_b + i
+ * Rows at or past cu[B] are not written.  A position outside [0, max_pages * page) or a page
+ * number outside [0, P) skips its row and records FA_ERR_PLAN.  Two rows with the same page
+ * and slot leave one of them.
+ */
+fa_status fa_cache_append(const fa_cache_problem* problem, const void* k, const void* v, void* k_pages, void* v_pages,
+                          void* k_scales, void* v_scales, const int* page_table, const int* seqlens, const int* cu,
+                          void* stream);
+
+/*
+ * Reads positions back as contiguous 16-bit rows.
+ *   k_out, v_out : out, [T, H_kv, d] of `dtype`: row cu[b] + i is position starts[b] + i of
+ *                  sequence b (starts NULL: from 0)
+ * Rows whose position is at or past seqlens[b], and rows at or past cu[B], are left as they
+ * were; bad positions and page numbers as in fa_cache_append.
+ */
+fa_status fa_cache_gather(const fa_cache_problem* problem, const void* k_pages, const void* v_pages,
+                          const void* k_scales, const void* v_scales, const int* page_table, const int* seqlens,
+                          const int* cu, const int* starts, void* k_out, void* v_out, void* stream);
 
 /*
  * Failure-detection self-test: launches one warp that waits on a barrier nothing will

@@ -1,0 +1,98 @@
+"""Rotary frequencies (host side): closed forms, limits of the scalings, refusals; and the
+binding's refusals, which come before any device work."""
+import math
+
+import pytest
+import torch
+
+from exact_io_aware_93_b200 import api
+from exact_io_aware_93_b200.rotary import rope_frequencies
+
+
+def f(*a, **kw):
+    return rope_frequencies(*a, device="cpu", **kw)
+
+
+def test_plain_frequencies():
+    freq, factor = f(64, base=10000.0)
+    assert freq.dtype == torch.float64 and factor == 1.0
+    for j in range(32):
+        assert freq[j].item() == pytest.approx(10000.0 ** (-2.0 * j / 64), rel=1e-14)
+
+
+def test_linear_divides_every_frequency():
+    assert torch.equal(f(32, scaling="linear", scale=4.0)[0], f(32)[0] / 4.0)
+
+
+def test_ntk_keeps_the_fastest_and_divides_the_slowest():
+    plain, ntk = f(128)[0], f(128, scaling="ntk", scale=8.0)[0]
+    assert ntk[0].item() == 1.0
+    assert (plain[-1] / ntk[-1]).item() == pytest.approx(8.0, rel=1e-12)
+    assert torch.all(ntk <= plain)
+
+
+def test_bands_keep_fast_pairs_and_divide_slow_ones():
+    plain = f(128, base=500000.0)[0]
+    freq, factor = f(128, base=500000.0, scaling="bands", scale=8.0, trained=8192)
+    turns = 8192 * plain / (2 * math.pi)
+    assert factor == 1.0
+    assert torch.equal(freq[turns >= 4.0], plain[turns >= 4.0])
+    assert torch.allclose(freq[turns <= 1.0], plain[turns <= 1.0] / 8.0, rtol=1e-14)
+    mid = (turns > 1.0) & (turns < 4.0)
+    assert mid.any() and torch.all(freq[mid] < plain[mid]) and torch.all(freq[mid] > plain[mid] / 8.0)
+
+
+def test_yarn_ends_and_factor():
+    plain = f(128)[0]
+    freq, factor = f(128, scaling="yarn", scale=16.0, trained=4096)
+    assert factor == pytest.approx(0.1 * math.log(16.0) + 1.0)
+    assert torch.equal(freq[:10], plain[:10])                   # more than 32 turns over 4096 positions
+    assert torch.allclose(freq[-10:], plain[-10:] / 16.0, rtol=1e-14)
+    assert torch.all(freq[1:] < freq[:-1])
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rotary_dim=63), dict(rotary_dim=0), dict(rotary_dim=64, base=1.0), dict(rotary_dim=64, scale=0.5),
+    dict(rotary_dim=64, scaling="other"), dict(rotary_dim=64, scaling="yarn", scale=2.0),
+    dict(rotary_dim=64, scaling="bands", scale=2.0, trained=100, low=4.0, high=1.0),
+    dict(rotary_dim=2, scaling="ntk", scale=2.0),
+])
+def test_frequencies_refuse(kw):
+    with pytest.raises(ValueError):
+        f(**kw)
+
+
+def test_binding_refuses_before_device_work():
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    pos, freq = torch.arange(4), f(64)[0]
+    with pytest.raises(ValueError):
+        api.rope(q, None, pos, freq)                            # no CPU path
+    with pytest.raises(TypeError):
+        api.rope(q.float(), None, pos, freq)
+    with pytest.raises(ValueError):
+        api.rope(q[0], None, pos, freq)                         # two dimensions
+    with pytest.raises(ValueError):
+        api.cache_append(q, q, q, q, pos, pos, pos)
+
+
+@pytest.mark.parametrize("make", [
+    lambda x: x.expand(3, 4, 2, 64)[:, :, :, :],                # a batch stride of 0
+    lambda x: torch.as_strided(x, (3, 4, 2, 64), (512, 128, 32, 1)),   # heads overlap
+])
+def test_rope_outputs_may_not_overlap_themselves(make, monkeypatch):
+    monkeypatch.setattr(api, "_check_heads", lambda *a: None)
+    x = torch.zeros(3, 4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="overlap itself"):
+        api._check_rope_out("q_out", make(torch.zeros(4096, dtype=torch.bfloat16)[:512].view(1, 4, 2, 64)), x)
+
+
+def test_rope_output_apart_from_its_inputs(monkeypatch):
+    monkeypatch.setattr(api, "_check_heads", lambda *a: None)
+    buf = torch.zeros(10, 6, 64, dtype=torch.bfloat16)
+    q, k = buf[:8, :4], buf[:8, 4:]
+    api._check_rope_out("q_out", q, q, k)                       # in place, beside k
+    api._check_rope_out("q_out", torch.zeros(8, 4, 64, dtype=torch.bfloat16), q, k)
+    with pytest.raises(ValueError):
+        api._check_rope_out("q_out", buf[1:9, :4], q, k)        # shifted by a token
+    with pytest.raises(ValueError):
+        api._check_rope_out("k_out", q, q[:, :4], q)            # another input too
