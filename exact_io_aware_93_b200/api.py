@@ -61,6 +61,14 @@ class FaCacheProblem(ctypes.Structure):
                 ("quant", ctypes.c_int), ("k_stride", ctypes.c_longlong * 2), ("v_stride", ctypes.c_longlong * 2)]
 
 
+class FaPagedProblem(ctypes.Structure):
+    """The ``fa_paged_problem`` descriptor of include/fa.h."""
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int), ("H_kv", ctypes.c_int),
+                ("max_q", ctypes.c_int), ("P", ctypes.c_int), ("max_pages", ctypes.c_int), ("page", ctypes.c_int),
+                ("d", ctypes.c_int), ("scale", ctypes.c_float), ("causal", ctypes.c_int), ("window", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("quant", ctypes.c_int), ("q_stride", ctypes.c_longlong * 2)]
+
+
 class FAError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = int(status)
@@ -121,6 +129,10 @@ def lib() -> ctypes.CDLL:
     L.fa_cache_append.restype = i
     L.fa_cache_gather.argtypes = [ctypes.POINTER(FaCacheProblem)] + [vp] * 11
     L.fa_cache_gather.restype = i
+    L.fa_paged_workspace_size.argtypes = [ctypes.POINTER(FaPagedProblem)]
+    L.fa_paged_workspace_size.restype = ctypes.c_size_t
+    L.fa_paged.argtypes = [ctypes.POINTER(FaPagedProblem)] + [vp] * 11 + [ctypes.c_size_t, vp]
+    L.fa_paged.restype = i
     _lib = L
     return L
 
@@ -539,6 +551,67 @@ def cache_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch
     if st != 0:
         raise FAError(st, "fa_cache_gather")
     return k_out, v_out
+
+
+def _paged_problem(q, k_pages, page_table, max_q, causal, scale, window, quant) -> FaPagedProblem:
+    T, H, d = q.shape
+    P, H_kv, page, _ = k_pages.shape
+    B, max_pages = page_table.shape
+    return FaPagedProblem(B, T, H, H_kv, int(max_q), P, max_pages, page, d,
+                          1.0 / math.sqrt(d) if scale is None else float(scale), int(bool(causal)),
+                          -1 if window is None else int(window), FA_DTYPE[q.dtype], int(quant),
+                          (q.stride(0), q.stride(1)))
+
+
+def paged_workspace_size(q: torch.Tensor, k_pages: torch.Tensor, page_table: torch.Tensor, max_q: int) -> int:
+    """Bytes of device workspace ``fa_paged`` needs for these shapes on q's device."""
+    quant = k_pages.dtype == torch.float8_e4m3fn
+    p = _paged_problem(q, k_pages, page_table, max_q, True, None, None, quant)
+    with _on(q):
+        return int(lib().fa_paged_workspace_size(ctypes.byref(p)))
+
+
+def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                    seqlens: torch.Tensor, cu_q: torch.Tensor, max_q: int, causal: bool = True,
+                    scale: float | None = None, window: int | None = None, k_scales: torch.Tensor | None = None,
+                    v_scales: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """(O [T, H, d] in q's dtype, LSE [H, T] fp32) of the new tokens of a ragged batch against their
+    paged caches (``cache_append``'s layout), via ``fa_paged``.
+
+    Sequence b owns tokens cu_q[b] .. cu_q[b + 1] of q [T, H, d] (at most ``max_q``, any strides but
+    contiguous columns): one token (decoding), a few (drafted tokens) or a chunk of a prompt, mixed
+    freely.  With ``causal`` its token i stands at position seqlens[b] - n_b + i and sees the keys at
+    or before it, with ``window`` no more than that many back; without, all seqlens[b] keys.  A token
+    that sees no key gets O = 0 and LSE = -inf; rows behind cu_q[B] are left as they were."""
+    _check_heads("q", q)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, d]")
+    quant = _check_pages(k_pages, v_pages, page_table, seqlens, k_scales, v_scales, q.dtype)
+    T, H, d = q.shape
+    if q.device != k_pages.device or d != k_pages.shape[3] or H % k_pages.shape[1] != 0:
+        raise ValueError(f"q {tuple(q.shape)} does not fit pages {tuple(k_pages.shape)} on {k_pages.device} "
+                         "(key/value heads must divide the query heads)")
+    check_buffer("cu_q", cu_q, (page_table.shape[0] + 1,), torch.int32, q.device)
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    lse = torch.empty((H, T), dtype=torch.float32, device=q.device) if lse is None else lse
+    check_buffer("out", out, q.shape, q.dtype, q.device)
+    check_buffer("lse", lse, (H, T), torch.float32, q.device)
+    if T == 0:
+        return out, lse
+    p = _paged_problem(q, k_pages, page_table, max_q, causal, scale, window, quant)
+    with _on(q):
+        if workspace is None:
+            need = int(lib().fa_paged_workspace_size(ctypes.byref(p)))
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        check_scratch("workspace", workspace, q.device)
+        st = lib().fa_paged(ctypes.byref(p), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
+                            _ptr(v_scales), page_table.data_ptr(), seqlens.data_ptr(), cu_q.data_ptr(),
+                            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                            workspace.numel() * workspace.element_size(), _stream_ptr(q))
+    if st != 0:
+        raise FAError(st, "fa_paged")
+    return out, lse
 
 
 def get_status(device: torch.device | None = None) -> int:

@@ -1,0 +1,1180 @@
+// fa_paged_kernel.cuh -- exact attention of the new tokens of every sequence of a ragged batch
+// against that sequence's pages, for sm_100a.  One token (decoding), a few (drafted tokens) or
+// a chunk of a prompt, mixed in one call.
+//
+// Rows.  The G = H / H_kv query heads of a key/value head and the new tokens form the rows
+// r = i * G + g, so the cache is read once for all of them.  A TILE holds TQ = floor(128 / G)
+// tokens (one TMA box of G heads x TQ tokens; rows past G * TQ are zero).  A UNIT is a pair of
+// consecutive tiles of one (sequence, key/value head), or one tile when a sequence has no more.
+//
+// Work list.  A unit visits T = hi - lo tiles of 128 keys, those that some row of it sees
+// (causal: up to its last token; window: from its first token's first key).  The key tiles of
+// all units are laid end to end (sequence, key/value head, unit) and CTA c of the persistent
+// grid takes [c L, (c+1) L), L = ceil(total / grid): every SM gets the same number of key
+// tiles whatever the mix of chunks, single tokens and lengths.  A CTA's run falls into
+// SEGMENTS, each inside one unit; a segment that is not a whole unit leaves a partial result
+// (O normalised, log-sums) that fa_paged_merge_kernel joins.  The lengths are read on the
+// device, so a captured graph replays as they grow.
+//
+// Two ways through a segment, chosen per unit:
+//   pair    two tiles: softmax group g owns tile g and both share one stream of K/V tiles, in
+//           the order PV_0(j), S_0(j+1), PV_1(j), S_1(j+1) of the forward kernel.
+//   split   one tile: group g takes the segment's key tiles g, g + 2, ..: two independent
+//           online softmaxes over disjoint keys, joined through shared memory at its end.
+// Few rows (G * max_q <= 32, every unit split) use M = 64 MMAs and COPIES of the rows: copy c
+// of R takes keys [c 128/R, (c+1) 128/R) of every tile, so a softmax warp handles 32 or 64 keys
+// of a tile instead of 128 (see fa_decode_kernel.cuh).
+//
+// Pages.  A key tile is 128 / page boxes (or a part of one page), each fetched by its own lane
+// of the producer warp; page numbers are read 32 at a time, one window ahead.  Pages that no row
+// of the unit sees are not fetched, and value rows outside the unit's keys are zeroed in shared
+// memory: stale slots, and pages a sliding window has left behind, may hold anything.
+//
+// e4m3 pages.  Codes land in a ring of their own and a fourth warpgroup turns them into 16-bit
+// tiles, code * 2^e, which is exact (the scale is a power of two): from there on the kernel is
+// the same.  The conversion is 5 integer and 16-bit instructions per pair of codes, about 800
+// issue slots per SM and tile pair, against 1400 cycles for fetching 32 KB of codes.
+//
+// Warp roles (384 threads, 512 with e4m3 pages): warps 0-3 and 4-7 the softmax groups, warp 8
+// the TMA producer, warp 9 the MMA issuer, warps 10-11 idle, warps 12-15 the conversion.
+// Tensor memory: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [256+D,256+2D).
+#pragma once
+
+#include "fa_cache_kernels.cuh"
+#include "fa_fwd_kernel.cuh"
+
+namespace fa {
+
+constexpr uint32_t kPagedLaunchRegs = 168;    // 16-bit pages, tiles of 128 rows
+constexpr uint32_t kPagedLaunchRegsQ8 = 128;  // e4m3 pages, tiles of 128 rows
+
+// R = 0: tiles of 128 rows, both ways; R = 2, 4: one tile of 64 rows holding R copies of up to
+// 32 or 16 rows.
+template <int D, bool Q8, int R>
+struct PgCfg {
+  static constexpr bool kGeneral = R == 0;
+  static constexpr int kCopies = kGeneral ? 1 : R;
+  static constexpr int kM = kGeneral ? 128 : 64;
+  static constexpr int kRows = kM / kCopies;          // rows of a partial result
+  static constexpr int kSubs = kGeneral ? 2 : 1;      // partial results per segment
+  static constexpr int kStageBytes = 128 * 16 * 4;    // 16 columns of every copy's rows, or of group 1's
+  static constexpr int kThreads = Q8 ? 512 : 384;
+  // setmaxnreg, general kernels only: 2 x 128 x 200 + 128 x 104 of 384 x 168, and with the
+  // conversion warps 128 x (2 x 184 + 72 + 72) of 512 x 128
+  static constexpr uint32_t kLaunch = Q8 ? kPagedLaunchRegsQ8 : kPagedLaunchRegs;
+  static constexpr uint32_t kRegsSoftmax = Q8 ? 184 : 200;
+  static constexpr uint32_t kRegsOther = Q8 ? 72 : 104;
+  static constexpr int kChunks = D / 64;
+  static constexpr int kChunkBytes = 128 * 128;
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kQChunkBytes = kM * 128;
+  static constexpr int kQBytes = kChunks * kQChunkBytes;
+  static constexpr int kRawBytes = 128 * D;
+  static constexpr int kScale = 128 / D;              // slots scale with the tile
+  static constexpr int kStages = (kGeneral ? (Q8 ? 3 : 4) : (Q8 ? 3 : 5)) * kScale;
+  static constexpr int kRaw = Q8 ? (kGeneral ? 3 : 5) * kScale : 1;
+  static constexpr int kPArrive = kGeneral ? 128 : 4;
+  static constexpr uint32_t kOCol = 256;
+  static constexpr uint32_t kTmemCols = 512;
+  static_assert(2 * kRegsSoftmax + kRegsOther * (Q8 ? 2 : 1) <= kLaunch * (kThreads / 128), "register split");
+};
+
+struct PgArgs {
+  const int* cu;          // [B + 1]
+  const int* seqlens;     // [B]
+  const int* table;       // [B, max_pages]
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  void* out;              // [T, H, D]
+  float* lse;             // [H, T]
+  int* meta;              // total, L, unit prefix [B + 1], key-tile prefix [B + 1]
+  float* part_lse;        // [slots * kSubs, kRows, 2]
+  float* part_o;          // [slots * kSubs, kRows, D]
+  int B, T, H, H_kv, max_q, TQ, max_pages, page, page_shift, P, window, causal;
+  float scale_log2;
+  long long slots;        // 2 per CTA
+  int* status;
+};
+
+// ---------------------------------------------------------------- the work list
+struct PgSeq {
+  int q0, n, len, units;
+};
+__device__ __forceinline__ PgSeq pg_seq(const PgArgs& a, int b) {
+  const long long c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
+  PgSeq s;
+  const bool in = c0 >= 0 && c0 <= a.T && c1 > c0;
+  s.q0 = in ? static_cast<int>(c0) : 0;
+  s.n = in ? static_cast<int>(min(min(c1 - c0, static_cast<long long>(a.max_q)), a.T - c0)) : 0;
+  const long long cap = static_cast<long long>(a.max_pages) * a.page;
+  s.len = static_cast<int>(min(max(static_cast<long long>(__ldg(a.seqlens + b)), 0ll), cap));
+  s.units = ((s.n + a.TQ - 1) / a.TQ + 1) / 2;
+  return s;
+}
+__device__ __forceinline__ bool pg_seq_ok(const PgArgs& a, int b) {
+  const long long c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
+  const long long len = __ldg(a.seqlens + b);
+  return c0 >= 0 && c1 >= c0 && c1 <= a.T && c1 - c0 <= a.max_q && len >= 0 &&
+         len <= static_cast<long long>(a.max_pages) * a.page;
+}
+
+// Keys [lo, hi) that the tokens at positions p0 .. p1 of a sequence of `len` keys see, and the
+// key tiles that hold them.
+struct PgKeys {
+  int lo, hi, t0, t1;
+};
+__device__ __forceinline__ PgKeys pg_keys(const PgArgs& a, int len, int p0, int p1) {
+  PgKeys k;
+  k.hi = a.causal ? min(p1 + 1, len) : len;
+  k.lo = a.window >= 0 ? max(0, p0 - a.window) : 0;
+  if (k.hi <= k.lo) k.hi = k.lo = 0;
+  k.t0 = k.lo >> 7;
+  k.t1 = (k.hi + 127) >> 7;
+  return k;
+}
+
+__device__ __forceinline__ PgKeys pg_unit_keys(const PgArgs& a, const PgSeq& s, int u) {
+  const int tok0 = u * 2 * a.TQ;
+  const int ntok = min(2 * a.TQ, s.n - tok0);
+  const int p0 = s.len - s.n + tok0;
+  return pg_keys(a, s.len, p0, p0 + ntok - 1);
+}
+
+__device__ __forceinline__ int pg_seq_tiles(const PgArgs& a, const PgSeq& s) {
+  int w = 0;
+  for (int u = 0; u < s.units; ++u) {
+    const PgKeys k = pg_unit_keys(a, s, u);
+    w += k.t1 - k.t0;
+  }
+  return w;
+}
+
+// This CTA's slice [t0, t1) of the key tiles and the unit it starts in, whose first key tile
+// has index start.
+struct PgPlan {
+  int t0, t1, b, kvh, u, start;
+};
+
+// One warp.  With `write` it also stores the prefixes for the merge kernel and checks the
+// lengths and offsets.
+__device__ __forceinline__ void pg_plan(const PgArgs& a, int lane, PgPlan* out, bool write) {
+  constexpr unsigned kFull = 0xffffffffu;
+  int total = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int v = b < a.B ? pg_seq_tiles(a, pg_seq(a, b)) * a.H_kv : 0;
+    total += static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(v)));
+  }
+  const int grid = static_cast<int>(gridDim.x);
+  const int per = total > 0 ? (total + grid - 1) / grid : 1;
+  const int t0 = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(blockIdx.x) * per));
+  const int t1 = min(total, t0 + per);
+  bool found = t0 >= t1;
+  if (found && lane == 0) *out = PgPlan{t0, t0, 0, 0, 0, 0};
+  int acc = 0, uacc = 0;
+  for (int b0 = 0; b0 < a.B && (!found || write); b0 += 32) {
+    const int b = b0 + lane;
+    PgSeq s{0, 0, 0, 0};
+    if (b < a.B) {
+      s = pg_seq(a, b);
+      if (write && !pg_seq_ok(a, b)) plan_fail(a.status, 43);
+    }
+    const int w = b < a.B ? pg_seq_tiles(a, s) : 0;
+    int incl = w * a.H_kv, uincl = s.units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, incl, o), y = __shfl_up_sync(kFull, uincl, o);
+      if (lane >= o) {
+        incl += x;
+        uincl += y;
+      }
+    }
+    incl += acc;
+    uincl += uacc;
+    const int excl = incl - w * a.H_kv;
+    if (write && b < a.B) {
+      a.meta[2 + b + 1] = uincl;
+      a.meta[2 + a.B + 1 + b + 1] = incl;
+    }
+    if (!found && b < a.B && excl <= t0 && t0 < incl) {  // one lane
+      const int kvh = (t0 - excl) / w;
+      int start = excl + kvh * w, u = 0;
+      while (true) {
+        const PgKeys k = pg_unit_keys(a, s, u);
+        if (t0 < start + k.t1 - k.t0) break;
+        start += k.t1 - k.t0;
+        ++u;
+      }
+      *out = PgPlan{t0, t1, b, kvh, u, start};
+    }
+    found = found || (t0 < __shfl_sync(kFull, incl, 31));
+    acc = __shfl_sync(kFull, incl, 31);
+    uacc = __shfl_sync(kFull, uincl, 31);
+  }
+  if (write && lane == 0) {
+    a.meta[0] = total;
+    a.meta[1] = per;
+    a.meta[2] = 0;
+    a.meta[2 + a.B + 1] = 0;
+  }
+}
+
+// A run of nt key tiles from tile kt0 of one unit.
+struct PgSeg {
+  int b, kvh;
+  int q0;        // the unit's first token
+  int pos0;      // its position
+  int ntok;      // tokens of the unit
+  int len;
+  PgKeys keys;   // what the unit sees
+  int kt0, nt;
+  bool pair;     // two tiles
+  bool whole;    // the run is the whole unit
+  bool first;    // the CTA's first segment
+};
+
+// Walks this CTA's slice segment by segment; every role walks it the same way.
+struct PgWalk {
+  int t, t1, b, kvh, u, start;
+  bool fresh;
+  PgSeq s;
+  __device__ __forceinline__ PgWalk(const PgArgs& a, const PgPlan& p)
+      : t(p.t0), t1(p.t1), b(p.b), kvh(p.kvh), u(p.u), start(p.start), fresh(true), s(pg_seq(a, p.b)) {}
+  __device__ __forceinline__ bool next(const PgArgs& a, PgSeg& g) {
+    if (t >= t1) return false;
+    PgKeys k{0, 0, 0, 0};
+    while (true) {
+      if (u < s.units) {
+        k = pg_unit_keys(a, s, u);
+        if (t < start + k.t1 - k.t0) break;
+        start += k.t1 - k.t0;
+        ++u;
+      } else {
+        u = 0;
+        if (s.units == 0 || ++kvh >= a.H_kv) {
+          kvh = 0;
+          if (++b >= a.B) return false;
+          s = pg_seq(a, b);
+        }
+      }
+    }
+    const int end = start + k.t1 - k.t0;
+    const int stop = min(end, t1);
+    const int tok0 = u * 2 * a.TQ;
+    g.b = b;
+    g.kvh = kvh;
+    g.q0 = s.q0 + tok0;
+    g.pos0 = s.len - s.n + tok0;
+    g.ntok = min(2 * a.TQ, s.n - tok0);
+    g.len = s.len;
+    g.keys = k;
+    g.kt0 = k.t0 + (t - start);
+    g.nt = stop - t;
+    g.pair = g.ntok > a.TQ;
+    g.whole = t == start && stop == end;
+    g.first = fresh;
+    fresh = false;
+    t = stop;
+    return true;
+  }
+};
+
+// Key tiles [lo, hi) of the segment that tile i of a pair visits.
+struct PgRange {
+  int lo, hi;
+};
+__device__ __forceinline__ PgRange pg_range(const PgArgs& a, const PgSeg& g, int i) {
+  const int tok = i * a.TQ;
+  const int n = min(a.TQ, g.ntok - tok);
+  const PgKeys k = pg_keys(a, g.len, g.pos0 + tok, g.pos0 + tok + n - 1);
+  PgRange r{max(k.t0, g.kt0), min(k.t1, g.kt0 + g.nt)};
+  if (r.hi < r.lo) r.hi = r.lo;
+  return r;
+}
+
+// The key tiles of a segment in the order the MMA warp consumes them.  pair: K_j, V_j; split:
+// K_0, K_1, V_0, K_2, V_1, ..  f(is_value, tile) returns false to stop.
+template <typename F>
+__device__ __forceinline__ bool pg_loads(const PgSeg& g, F f) {
+  if (g.pair) {
+    for (int t = 0; t < g.nt; ++t)
+      if (!f(false, g.kt0 + t) || !f(true, g.kt0 + t)) return false;
+    return true;
+  }
+  if (!f(false, g.kt0) || (g.nt > 1 && !f(false, g.kt0 + 1))) return false;
+  for (int t = 0; t < g.nt; ++t)
+    if (!f(true, g.kt0 + t) || (t + 2 < g.nt && !f(false, g.kt0 + t + 2))) return false;
+  return true;
+}
+
+// ---------------------------------------------------------------- e4m3 codes to 16 bits
+// Sixteen codes times the scale of exponent byte eb, in order.
+template <Elem E>
+__device__ __forceinline__ void pg_convert16(const uint4& c, uint32_t eb, uint32_t (&o)[8]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  if constexpr (E == Elem::kF16) {
+    // fp16 holds every code; 2^e is one fp16 factor for -14 <= e <= 15
+    if (eb - 113u <= 29u) {
+      const uint32_t f = ((eb - 112u) << 10) * 0x10001u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 x, y;\n\tmov.b32 {lo, hi}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 x, lo;\n\tcvt.rn.f16x2.e4m3x2 y, hi;\n\t"
+            "mul.rn.f16x2 %0, x, %3;\n\tmul.rn.f16x2 %1, y, %3;\n\t}"
+            : "=r"(o[2 * i]), "=r"(o[2 * i + 1])
+            : "r"(w[i]), "r"(f));
+      return;
+    }
+  } else {
+    // Code s eeee mmm as bf16 bits s 0000eeee mmm0000 is the value times 2^-120 (subnormals
+    // included), so one multiplication by 2^(e + 120) gives it, for -126 <= e <= 7 and codes
+    // that are not NaN (0x7F).
+    uint32_t nan = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
+    if (eb - 1u <= 133u && !(nan & 0x80808080u)) {
+      const uint32_t f = ((eb + 120u) << 7) * 0x10001u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t p = __byte_perm(w[i], 0u, 0x1404), q = __byte_perm(w[i], 0u, 0x3424);
+        const uint32_t x = (p & 0x80008000u) | ((p >> 4) & 0x07f007f0u);
+        const uint32_t y = (q & 0x80008000u) | ((q >> 4) & 0x07f007f0u);
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[2 * i]) : "r"(x), "r"(f));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[2 * i + 1]) : "r"(y), "r"(f));
+      }
+      return;
+    }
+  }
+  const float f = e8m0_to_float(eb);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = e4m3x2_to_float2(w[i]), q = e4m3x2_to_float2(w[i] >> 16);
+    o[2 * i] = ElemOps<E>::pack(p.x * f, p.y * f);
+    o[2 * i + 1] = ElemOps<E>::pack(q.x * f, q.y * f);
+  }
+}
+
+// ---------------------------------------------------------------- the kernel
+template <int D, bool Q8, int R>
+struct __align__(1024) PgSmem {
+  using Cfg = PgCfg<D, Q8, R>;
+  uint8_t q[2][Cfg::kQBytes];
+  uint8_t kv[Cfg::kStages][Cfg::kTileBytes];
+  uint8_t raw[Cfg::kRaw][Q8 ? Cfg::kRawBytes : 16];
+  uint8_t scale[Cfg::kRaw][128];
+  uint8_t stage[Cfg::kStageBytes];
+  float3 stat[2 * Cfg::kCopies][Cfg::kRows];  // m, l, lr of a split segment's copies
+  uint64_t q_full[2];
+  uint64_t q_empty[2];
+  uint64_t kv_full[Cfg::kStages];
+  uint64_t kv_empty[Cfg::kStages];
+  uint64_t raw_full[Cfg::kRaw];
+  uint64_t raw_empty[Cfg::kRaw];
+  uint64_t s_full[2];
+  uint64_t p_full[2];
+  uint64_t o_done[2];
+  uint64_t groups;  // both softmax groups, at the end of a split segment
+  uint64_t mma_drain;
+  PgPlan plan;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Sets value rows [z0, z1) of a 16-bit tile to zero (one warp).
+template <int D>
+__device__ __forceinline__ void pg_zero_rows(uint8_t* tile, int z0, int z1, int lane) {
+  constexpr int kUnits = D / 8;  // 16-byte units per row
+  for (int u = lane; u < (z1 - z0) * kUnits; u += 32) {
+    const int row = z0 + u / kUnits;
+    const int c = u % kUnits;
+    *reinterpret_cast<uint4*>(tile + (c / 8) * 128 * 128 + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+template <int D, Elem E, bool Q8, int R>
+__global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
+    fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const PgArgs a) {
+  using Cfg = PgCfg<D, Q8, R>;
+  constexpr int NS = Cfg::kStages;
+  constexpr int NR = Cfg::kRaw;
+  constexpr unsigned kFull = 0xffffffffu;
+  extern __shared__ uint8_t smem_raw[];
+  PgSmem<D, Q8, R>& sm = *reinterpret_cast<PgSmem<D, Q8, R>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                              ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int G = a.H / a.H_kv;
+  int* status = a.status;
+
+  if (threadIdx.x == 0) {
+    sm.abort_flag = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_empty[i], 1);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], Cfg::kPArrive);
+      mbar_init(&sm.o_done[i], 1);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&sm.kv_full[s], Q8 ? 4 : 1);
+      mbar_init(&sm.kv_empty[s], 1);
+    }
+    for (int s = 0; s < NR; ++s) {
+      mbar_init(&sm.raw_full[s], 1);
+      mbar_init(&sm.raw_empty[s], 4);
+    }
+    mbar_init(&sm.groups, 8);
+    mbar_init(&sm.mma_drain, 1);
+    fence_mbar_init();
+  }
+  // rows past G * TQ of a query tile are never loaded
+  for (uint32_t i = threadIdx.x; i < 2u * Cfg::kQBytes / 16; i += Cfg::kThreads)
+    reinterpret_cast<uint4*>(sm.q[0])[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  if (warp == 9) {
+    tmem_alloc(&sm.tmem_base, Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 8) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    pg_plan(a, lane, &sm.plan, blockIdx.x == 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = sm.tmem_base;
+  const PgPlan plan = sm.plan;
+
+  // Each warpgroup's setmaxnreg sits at the top of the branch holding all of its code.
+  if (warp >= 8 && warp < 12) {
+    if constexpr (Cfg::kGeneral) regs_set<Cfg::kLaunch, Cfg::kRegsOther>();
+    if (warp == 8) {
+      // ---------------------------------------------------------- TMA producer (whole warp)
+      const WaitCtx wc{&sm.abort_flag, status, 31};
+      PgWalk w(a, plan);
+      PgSeg g;
+      uint32_t it = 0, qcnt[2] = {0, 0}, nseg = 0;
+      bool ok = true;
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, wc)); };
+      auto load_q = [&](int slot, int tok, int copies) -> bool {
+        if (!wait_all(&sm.q_empty[slot], (qcnt[slot] & 1) ^ 1)) return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.q_full[slot], static_cast<uint32_t>(copies * Cfg::kChunks * 128 * G * a.TQ));
+          for (int cp = 0; cp < copies; ++cp)
+            for (int c = 0; c < Cfg::kChunks; ++c)
+              if (FA_IN_BOUNDS(tok >= 0 && tok < a.T && g.kvh < a.H_kv && G * a.TQ <= Cfg::kRows, status, 501))
+                tma_load_4d(sm.q[slot] + c * Cfg::kQChunkBytes + cp * Cfg::kRows * 128, &tm_q, &sm.q_full[slot],
+                            c * 64, 0, g.kvh, tok);
+        }
+        __syncwarp();
+        ++qcnt[slot];
+        return true;
+      };
+      const int box = min(128, a.page);  // keys per box
+      // page numbers of windows of 32 table entries: the even and the odd one held, one ahead
+      int id_even = -1, id_odd = -1, ahead = -1, window_at = -1;
+      auto entry = [&](int win) {
+        const long long i = static_cast<long long>(win) * 32 + lane;
+        return i < a.max_pages ? __ldg(a.table + static_cast<long long>(g.b) * a.max_pages + i) : -1;
+      };
+      while (ok && w.next(a, g)) {
+        if (Cfg::kGeneral && g.pair) {
+          for (int i = 0; i < 2 && ok; ++i) {
+            const PgRange r = pg_range(a, g, i);
+            if (r.hi > r.lo) ok = load_q(i, g.q0 + i * a.TQ, 1);
+          }
+        } else {
+          ok = load_q(Cfg::kGeneral ? 0 : (nseg & 1), g.q0, Cfg::kCopies);
+        }
+        ++nseg;
+        if (!ok) break;
+        window_at = ((g.kt0 << 7) >> a.page_shift) >> 5;
+        ahead = entry(window_at);
+        --window_at;
+        ok = pg_loads(g, [&](bool isv, int j) -> bool {
+          const int p0 = (j << 7) >> a.page_shift;  // the tile's first page
+          if ((p0 >> 5) > window_at) {              // keys run at most two tiles ahead of values
+            window_at = p0 >> 5;
+            if (window_at & 1) id_odd = ahead; else id_even = ahead;
+            ahead = entry(window_at + 1);
+          }
+          // the boxes that hold a key of the unit
+          const int k0 = max(g.keys.lo - (j << 7), 0) / box;
+          const int k1 = (min(g.keys.hi - (j << 7), 128) + box - 1) / box;
+          const int slot = Q8 ? it % NR : it % NS;
+          uint64_t* full = Q8 ? &sm.raw_full[slot] : &sm.kv_full[slot];
+          if (!wait_all(Q8 ? &sm.raw_empty[slot] : &sm.kv_empty[slot], ((it / (Q8 ? NR : NS)) & 1) ^ 1)) return false;
+          const uint32_t bytes = static_cast<uint32_t>((k1 - k0) * box * (Q8 ? D + 1 : 2 * D));
+          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+          __syncwarp();
+          constexpr int kParts = Q8 ? 1 : Cfg::kChunks;
+          const int k = k0 + lane / kParts, c = lane % kParts;
+          const int held = (p0 >> 5) & 1 ? id_odd : id_even;
+          int id = __shfl_sync(kFull, held, (p0 + k) & 31);
+          if (k < k1) {
+            const int row = (j << 7) & (a.page - 1) & ~(box - 1);  // inside a page of 256
+            const bool good = id >= 0 && id < a.P;
+            if (!good) plan_fail(status, 44);
+            // a bad page number reads as zeros: a coordinate past the pool
+            const int pl = good ? id * a.H_kv + g.kvh : a.P * a.H_kv;
+            if (FA_IN_BOUNDS(row + box <= a.page && p0 + k < a.max_pages && k * box < 128, status, 502)) {
+              if constexpr (Q8) {
+                tma_load_3d(sm.raw[slot] + k * box * D, isv ? &tm_v : &tm_k, full, 0, row, pl);
+                const uint8_t* sc = (isv ? a.v_scales : a.k_scales) +
+                                    (static_cast<int64_t>(good ? pl : g.kvh) * a.page + row);
+                bulk_load(sm.scale[slot] + k * box, sc, box, full);
+              } else {
+                tma_load_3d(sm.kv[slot] + c * Cfg::kChunkBytes + k * box * 128, isv ? &tm_v : &tm_k, full, c * 64, row,
+                            pl);
+              }
+            }
+          }
+          __syncwarp();
+          ++it;
+          return true;
+        });
+      }
+      if (!ok && lane == 0) {
+        // Unwinding: wait (bounded) for the copies still in flight before the CTA exits.
+        constexpr uint32_t N = Q8 ? NR : NS;
+        for (uint32_t idx = (it > N ? it - N : 0); idx < it; ++idx)
+          mbar_wait_drain(Q8 ? &sm.raw_full[idx % N] : &sm.kv_full[idx % N], (idx / N) & 1, status);
+        for (int i = 0; i < 2; ++i)
+          if (qcnt[i] > 0) mbar_wait_drain(&sm.q_full[i], (qcnt[i] - 1) & 1, status);
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      // ---------------------------------------------------------- MMA issuer (whole warp)
+      const WaitCtx wc{&sm.abort_flag, status, 32};
+      constexpr uint32_t idesc_s = idesc_kind_f16(Cfg::kM, kBN, 0, 0, ElemOps<E>::kMmaType);
+      constexpr uint32_t idesc_o = idesc_kind_f16(Cfg::kM, D, 0, 1, ElemOps<E>::kMmaType);
+      const uint64_t dq[2] = {sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), sdesc_sw128(smem_u32(sm.q[1]), 16, 1024)};
+      const uint64_t dk0 = sdesc_sw128(smem_u32(sm.kv[0]), 16, 1024);
+      const uint64_t dv0 = sdesc_sw128(smem_u32(sm.kv[0]), Cfg::kChunkBytes, 1024);
+      auto issue_s = [&](int i, int qs, int slot) {
+        const uint64_t dk = dk0 + static_cast<uint64_t>((slot * Cfg::kTileBytes) >> 4);
+        const uint64_t dqi = qs ? dq[1] : dq[0];
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss_w(tbase + i * 128, dqi + (((kk / 4) * Cfg::kQChunkBytes + (kk % 4) * 32) >> 4),
+                    dk + (((kk / 4) * Cfg::kChunkBytes + (kk % 4) * 32) >> 4), idesc_s, kk > 0);
+      };
+      auto issue_pv = [&](int i, int slot, uint32_t acc) {
+        const uint64_t dv = dv0 + static_cast<uint64_t>((slot * Cfg::kTileBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk)
+          umma_ts_w(tbase + Cfg::kOCol + i * D, tbase + i * 128 + kk * 8, dv + ((kk * 16 * 128) >> 4), idesc_o,
+                    (kk > 0) || acc);
+      };
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, wc)); };
+      PgWalk w(a, plan);
+      PgSeg g;
+      uint32_t it = 0, qcnt[2] = {0, 0}, pcnt[2] = {0, 0}, nseg = 0;
+      bool ok = true;
+      int slot = 0;
+      auto take = [&]() -> bool {
+        slot = it % NS;
+        const bool r = wait_all(&sm.kv_full[slot], (it / NS) & 1);
+        ++it;
+        return r;
+      };
+      // value rows of tile j that the unit does not see are zeroed: zero weights times stale
+      // infinities would not be zero (the conversion warps do it for e4m3 pages)
+      auto clean = [&](int sv, int j) {
+        if constexpr (!Q8) {
+          const int z0 = max(g.keys.lo - (j << 7), 0), z1 = min(g.keys.hi - (j << 7), 128);
+          if (z0 > 0 || z1 < 128) {
+            pg_zero_rows<D>(sm.kv[sv], 0, z0, lane);
+            pg_zero_rows<D>(sm.kv[sv], z1, 128, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+      };
+      while (ok && w.next(a, g)) {
+        if (Cfg::kGeneral && g.pair) {
+          const PgRange rg[2] = {pg_range(a, g, 0), pg_range(a, g, 1)};
+          const int jlo = g.kt0, jhi = g.kt0 + g.nt;
+          auto in = [&](int i, int j) { return j >= rg[i].lo && j < rg[i].hi; };
+          for (int i = 0; i < 2 && ok; ++i)
+            if (rg[i].hi > rg[i].lo) ok = wait_all(&sm.q_full[i], qcnt[i] & 1);
+          if (!ok) break;
+          ok = take();
+          if (!ok) break;
+          tc_fence_after();
+          for (int i = 0; i < 2; ++i) {
+            if (!in(i, jlo)) continue;
+            issue_s(i, i, slot);
+            umma_commit_w(&sm.s_full[i]);
+            if (rg[i].hi == jlo + 1) umma_commit_w(&sm.q_empty[i]);
+          }
+          umma_commit_w(&sm.kv_empty[slot]);
+          for (int j = jlo; j < jhi && ok; ++j) {
+            ok = take();
+            if (!ok) break;
+            const int sv = slot;
+            clean(sv, j);
+            int skn = -1;
+            if (j + 1 < jhi) {
+              ok = take();
+              if (!ok) break;
+              skn = slot;
+            }
+            for (int i = 0; i < 2 && ok; ++i) {
+              if (in(i, j)) {
+                ok = wait_all(&sm.p_full[i], pcnt[i] & 1);
+                if (!ok) break;
+                ++pcnt[i];
+                tc_fence_after();
+                issue_pv(i, sv, j > rg[i].lo);
+                if (j + 1 == rg[i].hi) umma_commit_w(&sm.o_done[i]);
+              }
+              if (in(i, j + 1)) {
+                issue_s(i, i, skn);
+                umma_commit_w(&sm.s_full[i]);
+                if (j + 2 == rg[i].hi) umma_commit_w(&sm.q_empty[i]);
+              }
+            }
+            if (!ok) break;
+            umma_commit_w(&sm.kv_empty[sv]);
+            if (skn >= 0) umma_commit_w(&sm.kv_empty[skn]);
+          }
+          for (int i = 0; i < 2; ++i)
+            if (rg[i].hi > rg[i].lo) ++qcnt[i];
+        } else {
+          const int qs = Cfg::kGeneral ? 0 : (nseg & 1);
+          ok = wait_all(&sm.q_full[qs], qcnt[qs] & 1);
+          if (!ok) break;
+          ++qcnt[qs];
+          tc_fence_after();
+          for (int t = 0; t < 2 && t < g.nt && ok; ++t) {
+            ok = take();
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(t, qs, slot);
+            umma_commit_w(&sm.s_full[t]);
+            umma_commit_w(&sm.kv_empty[slot]);
+            if (t == g.nt - 1) umma_commit_w(&sm.q_empty[qs]);
+          }
+          for (int t = 0; t < g.nt && ok; ++t) {
+            const int i = t & 1;
+            ok = take();  // V_t
+            if (!ok) break;
+            clean(slot, g.kt0 + t);
+            ok = wait_all(&sm.p_full[i], (i ? pcnt[1] : pcnt[0]) & 1);
+            if (!ok) break;
+            if (i) ++pcnt[1]; else ++pcnt[0];
+            tc_fence_after();
+            issue_pv(i, slot, t >= 2);
+            umma_commit_w(&sm.kv_empty[slot]);
+            if (t + 2 >= g.nt) umma_commit_w(&sm.o_done[i]);
+            if (t + 2 < g.nt) {
+              ok = take();  // K_{t+2}
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(i, qs, slot);
+              umma_commit_w(&sm.s_full[i]);
+              umma_commit_w(&sm.kv_empty[slot]);
+              if (t + 2 == g.nt - 1) umma_commit_w(&sm.q_empty[qs]);
+            }
+          }
+        }
+        ++nseg;
+      }
+      // Wait for every MMA issued to finish before the columns are freed.
+      umma_commit_w(&sm.mma_drain);
+      mbar_wait_drain(&sm.mma_drain, 0, status);
+      __syncwarp();
+    }
+  } else if (Q8 && warp >= 12) {
+    // ------------------------------------------------------------ e4m3 codes to 16-bit tiles
+    if constexpr (Cfg::kGeneral) regs_set<Cfg::kLaunch, Cfg::kRegsOther>();
+    const WaitCtx wc{&sm.abort_flag, status, 35};
+    constexpr int L = D / 16;          // threads per row
+    constexpr int kStep = 128 / L;     // rows per pass
+    constexpr int U = 4;
+    const int tid = threadIdx.x - 384;
+    const int item = tid % L, r0 = tid / L;
+    PgWalk w(a, plan);
+    PgSeg g;
+    uint32_t it = 0;
+    bool ok = true;
+    while (ok && w.next(a, g)) {
+      ok = pg_loads(g, [&](bool isv, int j) -> bool {
+        const int rs = it % NR, ks = it % NS;
+        if (!__all_sync(kFull, mbar_wait(&sm.raw_full[rs], (it / NR) & 1, wc))) return false;
+        if (!__all_sync(kFull, mbar_wait(&sm.kv_empty[ks], ((it / NS) & 1) ^ 1, wc))) return false;
+        ++it;
+        const int z0 = max(g.keys.lo - (j << 7), 0), z1 = min(g.keys.hi - (j << 7), 128);
+        uint8_t* dst = sm.kv[ks] + (item / 4) * Cfg::kChunkBytes;
+#pragma unroll 1
+        for (int base = r0; base < 128; base += U * kStep) {
+          uint4 c[U];
+          uint32_t eb[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int row = base + u * kStep;
+            c[u] = *reinterpret_cast<const uint4*>(sm.raw[rs] + row * D + item * 16);
+            eb[u] = sm.scale[rs][row];
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int row = base + u * kStep;
+            uint32_t o[8];
+            if (row >= z0 && row < z1) {
+              pg_convert16<E>(c[u], eb[u], o);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) o[x] = 0u;
+            }
+            // 16-byte units 2 (item % 4) and the next of the row's 128-byte swizzled chunk; the
+            // upper chunk's threads store the odd unit first, so that a row's eight threads
+            // cover all banks
+            const int u0 = (item % 4) * 2;
+            const int odd = (item / 4) & 1;
+            uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+            uint8_t* p = dst + row * 128;
+            *reinterpret_cast<uint4*>(p + (((u0 + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
+            *reinterpret_cast<uint4*>(p + (((u0 + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.kv_full[ks]);
+          mbar_arrive(&sm.raw_empty[rs]);
+        }
+        return true;
+      });
+    }
+  } else {
+    // ------------------------------------------------------------ softmax groups
+    if constexpr (Cfg::kGeneral) regs_set<Cfg::kLaunch, Cfg::kRegsSoftmax>();
+    constexpr int NC = 128 / Cfg::kCopies;         // keys of a tile this warp handles
+    constexpr int kQuarter = Cfg::kM / 4;          // accumulator rows per 32-lane quarter
+    constexpr int kWarpsPerCopy = 4 / Cfg::kCopies;
+    const int grp = warp >> 2;
+    const int wq = warp & 3;
+    const int cp = wq / kWarpsPerCopy;
+    const int col0 = cp * NC;
+    // row within the copy; with M = 64, lanes 16-31 of a quarter hold no rows
+    const int rc = lane < kQuarter ? (wq % kWarpsPerCopy) * kQuarter + lane : 1 << 20;
+    const int wrow0 = (wq % kWarpsPerCopy) * kQuarter;  // the warp's first row
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tbase + grp * 128 + lane_off;
+    const uint32_t tO = tbase + Cfg::kOCol + grp * D + lane_off;
+    const WaitCtx wc{&sm.abort_flag, status, 33 + grp};
+    PgWalk w(a, plan);
+    PgSeg g;
+    uint32_t scnt = 0, ocnt = 0, gcnt = 0;
+    bool ok = true;
+    while (ok && w.next(a, g)) {
+      // this group's tile and its key tiles j0, j0 + dj, .. below j1
+      const bool pair = Cfg::kGeneral && g.pair;
+      const int tok = pair ? grp * a.TQ : 0;
+      const int ntok = min(a.TQ, g.ntok - tok);
+      const int M = G * ntok;
+      int j0 = g.kt0 + grp, j1 = g.kt0 + g.nt, dj = 2;
+      if (pair) {
+        const PgRange r = pg_range(a, g, grp);
+        j0 = r.lo;
+        j1 = r.hi;
+        dj = 1;
+      }
+      const bool any = j0 < j1;
+      const int iq = rc < M ? rc / G : 0;
+      const int qpos = g.pos0 + tok + iq;
+      const int vis_hi = rc < M ? (a.causal ? min(qpos, g.len - 1) : g.len - 1) : -1;
+      const int vis_lo = a.window >= 0 ? qpos - a.window : 0;
+      // every row of the tile sees the keys from all_lo to all_hi
+      const int all_hi = a.causal ? g.pos0 + tok : g.len - 1;
+      const int all_lo = a.window >= 0 ? g.pos0 + tok + ntok - 1 - a.window : 0;
+      const bool rows_here = wrow0 < M;  // a warp without rows only keeps the barriers
+      float m_ref = -INFINITY, l = 0.f, lr = 0.f;
+      for (int j = j0; j < j1; j += dj) {
+        ok = __all_sync(kFull, mbar_wait(&sm.s_full[grp], scnt & 1, wc));
+        if (!ok) break;
+        ++scnt;
+        tc_fence_after();
+        if (rows_here) {
+          const int k0 = (j << 7) + col0;
+          uint32_t s[NC];
+#pragma unroll
+          for (int c = 0; c < NC; c += 32) tmem_ld32(tS + col0 + c, s + c);
+          tmem_wait_ld();
+          if (k0 + NC - 1 > all_hi || k0 < all_lo) {
+            const int lim = vis_hi - k0, first = vis_lo - k0;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (c > lim || c < first) s[c] = __float_as_uint(-INFINITY);
+          }
+          float mx8[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) mx8[x] = fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 8]));
+#pragma unroll
+          for (int c = 16; c < NC; c += 16)
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              mx8[x] = fmax3(mx8[x], __uint_as_float(s[c + x]), __uint_as_float(s[c + 8 + x]));
+          const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+                                 fmaxf(mx8[6], mx8[7]));
+          const float m_new = mx * a.scale_log2;
+          const bool raise = m_new > m_ref + kTau;
+          if (__any_sync(kFull, raise)) {
+            const float alpha = raise ? ex2_approx(m_ref - m_new) : 1.0f;
+            if (raise) {
+              l *= alpha;
+              lr *= alpha;
+              m_ref = m_new;
+            }
+            if (j > j0) {
+              // the commit that signalled this S covers the group's previous P.V
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tO + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                tmem_st32(tO + c, o);
+              }
+              tmem_wait_st();
+            }
+          }
+          uint32_t p[NC / 2];
+          const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+          softmax_row<E, NC>(s, p, a.scale_log2, m_use, l, lr);
+          // P for all 128 keys: this copy's columns, zeros for the other copies' keys
+#pragma unroll
+          for (int x = 0; x < NC / 2; x += 16) tmem_st16(tS + col0 / 2 + x, p + x);
+          if constexpr (Cfg::kCopies > 1) {
+            uint32_t zero[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) zero[x] = 0u;
+#pragma unroll
+            for (int c = 0; c < 64; c += 16)
+              if (c < col0 / 2 || c >= col0 / 2 + NC / 2) tmem_st16(tS + c, zero);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        if constexpr (Cfg::kPArrive == 4) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_full[grp]);
+        } else {
+          mbar_arrive(&sm.p_full[grp]);
+        }
+      }
+      if (!ok) break;
+      if (any) {
+        ok = __all_sync(kFull, mbar_wait(&sm.o_done[grp], ocnt & 1, wc));
+        if (!ok) break;
+        ++ocnt;
+        tc_fence_after();
+      }
+      const bool real = rc < M;
+      // a segment that is not a whole unit leaves a partial result
+      const int64_t part0 = ((static_cast<int64_t>(blockIdx.x) * 2 + (g.first ? 0 : 1)) * Cfg::kSubs +
+                             (pair ? grp : 0)) * Cfg::kRows;
+      const int64_t token0 = static_cast<int64_t>(g.q0) + tok;
+      auto put = [&](int row, int c, const auto& v) {  // columns c .. of a row of the tile
+        constexpr int n = sizeof(v) / sizeof(float);
+        const int i = row / G;
+        const int64_t token = token0 + i;
+        const int h = g.kvh * G + row - i * G;
+        if (g.whole) {
+          if (FA_IN_BOUNDS(token >= 0 && token < a.T && h < a.H && c + n <= D, status, 503)) {
+            typename ElemOps<E>::T* dst =
+                static_cast<typename ElemOps<E>::T*>(a.out) + (token * a.H + h) * D + c;
+            if constexpr (n % 8 == 0) {
+#pragma unroll
+              for (int x = 0; x < n / 8; ++x)
+                reinterpret_cast<uint4*>(dst)[x] = make_uint4(
+                    ElemOps<E>::pack(v[8 * x], v[8 * x + 1]), ElemOps<E>::pack(v[8 * x + 2], v[8 * x + 3]),
+                    ElemOps<E>::pack(v[8 * x + 4], v[8 * x + 5]), ElemOps<E>::pack(v[8 * x + 6], v[8 * x + 7]));
+            } else {
+#pragma unroll
+              for (int x = 0; x < n / 2; ++x)
+                reinterpret_cast<uint32_t*>(dst)[x] = ElemOps<E>::pack(v[2 * x], v[2 * x + 1]);
+            }
+          }
+        } else if (FA_IN_BOUNDS(part0 + row < a.slots * Cfg::kSubs * Cfg::kRows && row < Cfg::kRows && c + n <= D, status,
+                                504)) {
+          float* dst = a.part_o + (part0 + row) * D + c;
+          if constexpr (n % 4 == 0) {
+#pragma unroll
+            for (int x = 0; x < n / 4; ++x)
+              reinterpret_cast<float4*>(dst)[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+          } else {
+            *reinterpret_cast<float2*>(dst) = make_float2(v[0], v[1]);
+          }
+        }
+      };
+      auto put_lse = [&](float m, float ls, float lrs) {
+        const float lse_l = ls == 0.f ? -INFINITY : (m + lg2_approx(ls)) * kLn2;
+        const float lse_r = lrs == 0.f ? -INFINITY : (m + lg2_approx(lrs)) * kLn2;
+        const int64_t token = token0 + iq;
+        const int h = g.kvh * G + rc - iq * G;
+        if (g.whole) {
+          if (FA_IN_BOUNDS(token >= 0 && token < a.T && h < a.H, status, 505))
+            a.lse[static_cast<int64_t>(h) * a.T + token] = lse_l;
+        } else if (FA_IN_BOUNDS(part0 + rc < a.slots * Cfg::kSubs * Cfg::kRows, status, 506)) {
+          *reinterpret_cast<float2*>(a.part_lse + (part0 + rc) * 2) = make_float2(lse_l, lse_r);
+        }
+      };
+      if (pair) {
+        // O normalised by the sum of the rounded weights, and the log-sums of both
+        const float inv = lr == 0.f ? 0.f : 1.0f / lr;
+        if (rows_here) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            if (any) {
+              tmem_ld32(tO + c, o);
+              tmem_wait_ld();
+            }
+            float v[32];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[x] = lr == 0.f ? 0.f : __uint_as_float(o[x]) * inv;
+            if (real) put(rc, c, v);
+          }
+          if (real) put_lse(m_ref, l, lr);
+        }
+      } else {
+        // Join the copies: weights 2^(m_k - max m) / sum of lr, the rows summed through shared
+        // memory 32 columns at a time
+        auto sync_groups = [&]() -> bool {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.groups);
+          const bool r = __all_sync(kFull, mbar_wait(&sm.groups, gcnt & 1, wc));
+          ++gcnt;
+          return r;
+        };
+        const int me = grp * Cfg::kCopies + cp;
+        if (real) sm.stat[me][rc] = make_float3(m_ref, l, lr);
+        ok = sync_groups();
+        if (!ok) break;
+        float mm = -INFINITY, ls = 0.f, lrs = 0.f, wgt = 0.f;
+        if (real) {
+#pragma unroll
+          for (int k = 0; k < 2 * Cfg::kCopies; ++k) mm = fmaxf(mm, sm.stat[k][rc].x);
+          const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+          for (int k = 0; k < 2 * Cfg::kCopies; ++k) {
+            const float3 st = sm.stat[k][rc];
+            const float e = ex2_approx(st.x - ref);
+            ls += e * st.y;
+            lrs += e * st.z;
+          }
+          wgt = (lr == 0.f || lrs == 0.f) ? 0.f : ex2_approx(m_ref - ref) / lrs;
+          if (me == 0) put_lse(ref, ls, lrs);
+        }
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16];
+          float v[16];
+          if (any && rows_here) {
+            tmem_ld16(tO + c, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int x = 0; x < 16; ++x) v[x] = lr == 0.f ? 0.f : __uint_as_float(o[x]) * wgt;
+          // 16-byte unit u of staged row r sits at u ^ (r / 2 mod 4): two rows fill the banks
+          const int srow = Cfg::kGeneral ? rc : me * Cfg::kRows + rc;
+          if (real && (!Cfg::kGeneral || grp == 1)) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              *reinterpret_cast<float4*>(sm.stage + srow * 64 + ((x ^ ((srow >> 1) & 3)) << 4)) =
+                  make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+          }
+          ok = sync_groups();
+          if (!ok) break;
+          if constexpr (Cfg::kGeneral) {
+            if (grp == 0 && real) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float4 y = *reinterpret_cast<const float4*>(sm.stage + rc * 64 + ((x ^ ((rc >> 1) & 3)) << 4));
+                v[4 * x] += y.x;
+                v[4 * x + 1] += y.y;
+                v[4 * x + 2] += y.z;
+                v[4 * x + 3] += y.w;
+              }
+              put(rc, c, v);
+            }
+          } else {
+            // two columns of a row per thread
+            const int row = threadIdx.x >> 3, col = (threadIdx.x & 7) * 2;  // warps 0-7
+            if (row < M) {
+              float sum[2] = {0.f, 0.f};
+#pragma unroll
+              for (int k = 0; k < 2 * Cfg::kCopies; ++k) {
+                const int sr = k * Cfg::kRows + row;
+                const float2 y = *reinterpret_cast<const float2*>(
+                    sm.stage + sr * 64 + (((col >> 2) ^ ((sr >> 1) & 3)) << 4) + (col & 3) * 4);
+                sum[0] += y.x;
+                sum[1] += y.y;
+              }
+              put(row, c + col, sum);
+            }
+          }
+          ok = sync_groups();
+          if (!ok) break;
+        }
+        if (!ok) break;
+      }
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tbase, Cfg::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- joining the partial results
+// Per row: LSE = log sum_s exp(lse_s) and O = sum_s exp(lr_s - LR) O_s with LR = log sum_s
+// exp(lr_s), the convex combination one CTA would have formed.  Units that one CTA computed
+// were written by it; rows of units without keys get O = 0, LSE = -inf.  Block (unit,
+// key/value head, part) of four warps; W warps share a row's partial results.
+template <int D, Elem E, int R, int W>
+__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PgArgs a) {
+  using T = typename ElemOps<E>::T;
+  using Cfg = PgCfg<D, false, R>;
+  constexpr unsigned kFull = 0xffffffffu;
+  constexpr int V = D / 32;  // columns per lane
+  __shared__ float acc_sh[W > 1 ? W : 1][D];
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int G = a.H / a.H_kv;
+  const int kvh = blockIdx.y;
+  const int unit = blockIdx.x;
+  const int b = find_seq(a.meta + 2, a.B, unit, lane);
+  if (b >= a.B) return;
+  const PgSeq s = pg_seq(a, b);
+  const int u = unit - a.meta[2 + b];
+  const int tok0 = u * 2 * a.TQ;
+  const int ntok = min(2 * a.TQ, s.n - tok0);
+  const PgKeys k = pg_unit_keys(a, s, u);
+  const int T_u = k.t1 - k.t0;
+  const int* steps = a.meta + 2 + a.B + 1;
+  int start = steps[b] + kvh * ((steps[b + 1] - steps[b]) / a.H_kv);
+  int before = 0;
+  for (int x = lane; x < u; x += 32) {
+    const PgKeys kx = pg_unit_keys(a, s, x);
+    before += kx.t1 - kx.t0;
+  }
+  start += static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(before)));
+  const int per = a.meta[1];
+  const int cf = start / per;
+  const int cl = T_u > 0 ? (start + T_u - 1) / per : cf;
+  if (T_u > 0 && cf == cl) return;  // written by its CTA
+  const bool cf_first = start == cf * per;
+  const int parts = T_u > 0 ? cl - cf + 1 : 0;
+  const int rows = G * ntok;
+  for (int row = blockIdx.z * (4 / W) + warp / W; row < rows; row += gridDim.z * (4 / W)) {
+    const int tile = row / (G * a.TQ);
+    const int rc = row - tile * G * a.TQ;
+    const int iq = row / G, h = kvh * G + (row - iq * G);
+    const int64_t token = static_cast<int64_t>(s.q0) + tok0 + iq;
+    // index of partial result i of this row
+    auto at = [&](int i) -> int64_t {
+      const int slot = 2 * (cf + i) + ((i == 0 && !cf_first) ? 1 : 0);
+      return (static_cast<int64_t>(slot) * Cfg::kSubs + tile) * Cfg::kRows + rc;
+    };
+    float mx_l = -INFINITY, mx_r = -INFINITY, s_l = 0.f, s_r = 0.f;
+    for (int i = lane; i < parts; i += 32) {
+      const int64_t x = at(i);
+      if (!FA_IN_BOUNDS(x >= 0 && x < a.slots * Cfg::kSubs * Cfg::kRows, a.status, 507)) continue;
+      const float2 v = *reinterpret_cast<const float2*>(a.part_lse + x * 2);
+      mx_l = fmaxf(mx_l, v.x);
+      mx_r = fmaxf(mx_r, v.y);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      mx_l = fmaxf(mx_l, __shfl_xor_sync(kFull, mx_l, o));
+      mx_r = fmaxf(mx_r, __shfl_xor_sync(kFull, mx_r, o));
+    }
+    if (mx_l == -INFINITY) mx_l = 0.f;  // no key, or NaN only: the sums decide
+    if (mx_r == -INFINITY) mx_r = 0.f;
+    for (int i = lane; i < parts; i += 32) {
+      const int64_t x = at(i);
+      if (!FA_IN_BOUNDS(x >= 0 && x < a.slots * Cfg::kSubs * Cfg::kRows, a.status, 508)) continue;
+      const float2 v = *reinterpret_cast<const float2*>(a.part_lse + x * 2);
+      s_l += expf(v.x - mx_l);
+      s_r += expf(v.y - mx_r);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s_l += __shfl_xor_sync(kFull, s_l, o);
+      s_r += __shfl_xor_sync(kFull, s_r, o);
+    }
+    float acc[V];
+#pragma unroll
+    for (int x = 0; x < V; ++x) acc[x] = 0.f;
+    const float inv = s_r == 0.f ? 0.f : 1.0f / s_r;
+    // 32 partial results at a time: a lane forms one weight, then the warp sums the rows with
+    // the weights broadcast; a partial result without keys was not written and is not read
+    for (int base = (W > 1 ? warp * 32 : 0); base < parts; base += 32 * W) {
+      float wl = 0.f;
+      int64_t x = 0;
+      if (base + lane < parts) {
+        x = at(base + lane);
+        const float v = a.part_lse[x * 2 + 1];
+        wl = v == -INFINITY ? 0.f : expf(v - mx_r) * inv;
+      }
+      const int cnt = min(32, parts - base);
+#pragma unroll 4
+      for (int t = 0; t < cnt; ++t) {
+        const float wgt = __shfl_sync(kFull, wl, t);
+        const int64_t xt = __shfl_sync(kFull, x, t);
+        if (wgt == 0.f) continue;
+        const float* po = a.part_o + xt * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(po);
+          acc[0] = fmaf(wgt, v.x, acc[0]);
+          acc[1] = fmaf(wgt, v.y, acc[1]);
+          acc[2] = fmaf(wgt, v.z, acc[2]);
+          acc[3] = fmaf(wgt, v.w, acc[3]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(po);
+          acc[0] = fmaf(wgt, v.x, acc[0]);
+          acc[1] = fmaf(wgt, v.y, acc[1]);
+        }
+      }
+    }
+    if constexpr (W > 1) {
+#pragma unroll
+      for (int x = 0; x < V; ++x) acc_sh[warp][lane * V + x] = acc[x];
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int x = 0; x < V; ++x) {
+          acc[x] = 0.f;
+#pragma unroll
+          for (int y = 0; y < W; ++y) acc[x] += acc_sh[y][lane * V + x];
+        }
+      }
+      __syncthreads();
+      if (warp != 0) continue;
+    }
+    if (FA_IN_BOUNDS(token >= 0 && token < a.T && h < a.H, a.status, 509)) {
+      T* orow = static_cast<T*>(a.out) + (token * a.H + h) * D + lane * V;
+      if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(orow) =
+            make_uint2(ElemOps<E>::pack(acc[0], acc[1]), ElemOps<E>::pack(acc[2], acc[3]));
+      else
+        *reinterpret_cast<uint32_t*>(orow) = ElemOps<E>::pack(acc[0], acc[1]);
+      if (lane == 0) a.lse[static_cast<int64_t>(h) * a.T + token] = s_l == 0.f ? -INFINITY : mx_l + logf(s_l);
+    }
+  }
+}
+
+}  // namespace fa

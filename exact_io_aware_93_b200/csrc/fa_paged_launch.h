@@ -1,0 +1,70 @@
+// fa_paged_launch.h -- launches of the paged attention kernels.  Each (element type, page type)
+// is instantiated in a source of its own, so that they compile side by side.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/fa.h"
+#include "fa_host.h"
+
+namespace fa {
+
+struct PagedCall {
+  fa_paged_problem p;
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  const void* k_scales;
+  const void* v_scales;
+  const int* page_table;
+  const int* seqlens;
+  const int* cu;
+  void* o;
+  float* lse;
+  void* workspace;
+  cudaStream_t stream;
+};
+
+// Rows one key/value head contributes at most and the copies of them a tile holds: 4 up to 16
+// rows, 2 up to 32, otherwise 0 for tiles of 128 rows.
+inline int paged_copies(const fa_paged_problem& p) {
+  const long long rows = static_cast<long long>(p.H / p.H_kv) * p.max_q;
+  return rows <= 16 ? 4 : (rows <= 32 ? 2 : 0);
+}
+inline int paged_tile_tokens(const fa_paged_problem& p) {
+  return paged_copies(p) ? p.max_q : 128 / (p.H / p.H_kv);
+}
+// At most this many units (pairs of tiles) per key/value head: each sequence's last may be short.
+inline long long paged_units(const fa_paged_problem& p) {
+  const long long tokens = 2ll * paged_tile_tokens(p);
+  const long long each = static_cast<long long>(p.B) * ((p.max_q + tokens - 1) / tokens);
+  const long long all = p.T / tokens + p.B;
+  return each < all ? each : all;
+}
+
+// Workspace regions: the plan (total, tiles per CTA, unit and key-tile prefixes), then the
+// partial log-sums [rows, 2] and the partial outputs [rows, d]; a CTA leaves at most two
+// partial segments of 256 rows (16 or 32 where a tile holds copies).
+struct PagedLayout {
+  size_t meta, part_lse, part_o, total;
+  long long slots;
+};
+inline PagedLayout paged_layout(const fa_paged_problem& p, int grid) {
+  const auto round256 = [](size_t x) { return (x + 255) / 256 * 256; };
+  const int R = paged_copies(p);
+  const size_t rows = 2 * static_cast<size_t>(grid) * (R ? 64 / R : 256);
+  PagedLayout L;
+  L.slots = 2ll * grid;
+  L.meta = 0;
+  L.part_lse = round256((2 + 2 * (static_cast<size_t>(p.B) + 1)) * 4);
+  L.part_o = L.part_lse + round256(rows * 2 * 4);
+  L.total = L.part_o + rows * static_cast<size_t>(p.d) * 4;
+  return L;
+}
+
+fa_status paged_bf16(DeviceInfo& di, const PagedCall& c);
+fa_status paged_bf16_e4m3(DeviceInfo& di, const PagedCall& c);
+fa_status paged_f16(DeviceInfo& di, const PagedCall& c);
+fa_status paged_f16_e4m3(DeviceInfo& di, const PagedCall& c);
+
+}  // namespace fa

@@ -388,6 +388,67 @@ fa_status fa_cache_gather(const fa_cache_problem* problem, const void* k_pages, 
                           const int* cu, const int* starts, void* k_out, void* v_out, void* stream);
 
 /*
+ * Attention of the new tokens of a ragged batch against their paged caches (the layout of
+ * fa_cache_append): decoding, verifying drafted tokens and prompt chunks, mixed in one call.
+ *   B, T       : sequences; rows of q and o (new tokens of all sequences end to end)
+ *   H, H_kv    : query and key/value heads, H % H_kv == 0, H / H_kv <= 128
+ *   max_q      : an upper bound of the new tokens of a sequence
+ *   P, max_pages, page, d, quant : the cache, as in fa_cache_problem
+ *   scale, causal, window : as in fa_decode_problem; token i of sequence b's n_b stands at
+ *                position seqlens[b] - n_b + i; non-causal tokens see all seqlens[b] keys
+ *   dtype      : type of q and o, and of 16-bit pages
+ *   q_stride   : element strides (token, head) of q
+ */
+typedef struct fa_paged_problem {
+  int B;
+  int T;
+  int H;
+  int H_kv;
+  int max_q;
+  int P;
+  int max_pages;
+  int page;
+  int d;
+  float scale;
+  int causal;
+  int window;
+  int dtype;
+  int quant;
+  long long q_stride[2];
+} fa_paged_problem;
+
+/*
+ * Bytes of device workspace fa_paged needs on the CURRENT device: the plan, and two partial
+ * results per SM of 256 rows (32 or 16 when (H / H_kv) * max_q is no more) of 4 * d + 8 bytes.
+ * 0 for an invalid or unsupported problem or without an sm_100 device.
+ */
+size_t fa_paged_workspace_size(const fa_paged_problem* problem);
+
+/*
+ *   q          : in,  [T, H, d] with the given strides (16-byte aligned rows)
+ *   k_pages, v_pages, k_scales, v_scales, page_table : in, the cache
+ *   seqlens    : in,  DEVICE int32 [B]: cached length of each sequence, its new tokens included
+ *   cu_q       : in,  DEVICE int32 [B + 1]: sequence b owns tokens cu_q[b] .. cu_q[b + 1] - 1
+ *   o          : out, [T, H, d] contiguous;  lse: out, fp32 [H, T], natural log
+ *   workspace  : device scratch, 256-byte aligned; its contents on entry do not matter.  Calls
+ *                that share one must not overlap.
+ * A token that sees no key gets O = 0 and LSE = -inf; rows at or past cu_q[B] are left as they
+ * were.  Slots at or past a sequence's length, and positions before the first key that any new
+ * token of the sequence sees through the window, may hold anything, and page_table entries of
+ * pages that hold only such positions too; key and value rows that some new token sees are
+ * expected to be finite (a NaN or infinity there reaches the rows that see it, and may reach
+ * others of the same sequence).  A chunk longer than max_q is cut to it, a length is cut to the
+ * table's capacity, a page number outside [0, P) reads as zeros: each records FA_ERR_PLAN.
+ * Deterministic for fixed inputs and device.  All device-side values are read by the kernels:
+ * a captured graph can be replayed as they change, within B, T and max_q.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_ALIGNMENT, FA_ERR_DEVICE,
+ * FA_ERR_WORKSPACE, FA_ERR_LAUNCH.
+ */
+fa_status fa_paged(const fa_paged_problem* problem, const void* q, const void* k_pages, const void* v_pages,
+                   const void* k_scales, const void* v_scales, const int* page_table, const int* seqlens,
+                   const int* cu_q, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Failure-detection self-test: launches one warp that waits on a barrier nothing will
  * arrive on, through the same bounded wait the attention kernels use, with a bound of
  * timeout_us microseconds (1 .. 1000000).  The wait runs out, the kernel records
@@ -420,8 +481,11 @@ fa_status fa_get_status(void* stream);
  * fa_get_status, and in *site (if not NULL) where the first recorded error arose: for
  * FA_ERR_TIMEOUT the wait that ran out (forward: 1 loads, 2 MMA, 3 and 4 the softmax of the
  * first and second query block; backward: 11 loads, 12 MMA, 13 key rows, 14 dQ drain;
- * decode: 21 loads, 22 MMA, 23 softmax; 98 the final wait for issued MMAs or a wait while
+ * decode: 21 loads, 22 MMA, 23 softmax; paged attention: 31 loads, 32 MMA, 33 and 34 the softmax
+ * groups, 35 the conversion of e4m3 pages; 98 the final wait for issued MMAs or a wait while
  * unwinding after an abort; 99 the self-test),
+ * for FA_ERR_PLAN the reader (41 fa_cache_append, 42 fa_cache_gather, 43 and 44 fa_paged: its
+ * offsets and lengths, its page numbers),
  * for FA_ERR_BOUNDS the check that failed (three-digit sites, 999 the self-test); 0 when
  * none was recorded.  The sources name each site beside its wait or check.
  */
