@@ -30,14 +30,25 @@
 // of the unit sees are not fetched, and value rows outside the unit's keys are zeroed in shared
 // memory: stale slots, and pages a sliding window has left behind, may hold anything.
 //
-// e4m3 pages.  Codes land in a ring of their own and a fourth warpgroup turns them into 16-bit
-// tiles, code * 2^e, which is exact (the scale is a power of two): from there on the kernel is
-// the same.  The conversion is 5 integer and 16-bit instructions per pair of codes, about 800
-// issue slots per SM and tile pair, against 1400 cycles for fetching 32 KB of codes.
+// e4m3 pages.  The tensor core takes the codes as they are (kind::f8f6f4), so nothing is
+// converted and a tile moves half the bytes.  What is not e4m3 is cut into pieces that are, and
+// the products of the pieces are summed by the accumulator:
+//   Q   fa_paged_split_kernel writes q = 2^eq (q1 + q2 [+ q3]), each piece the e4m3 rounding of
+//       what the ones before it left: 4 significant bits each, so two pieces hold a bf16 exactly
+//       and three an fp16 (down to 2^-18 of the row's largest).
+//   P   the weight, an fp16 value rounded to 9 bits, is the sum of three e5m2 pieces (e5m2 is the
+//       upper byte of an fp16): relative error 2^-9 down to 2^-23 of the largest weight.  e5m2
+//       and not e4m3 for its range: a long tail of small weights beside a large one keeps its
+//       mass.
+// The scales: S_j is multiplied by 2^ek_j, and the weight by 2^(ev_j - E), E the segment's largest
+// value exponent so far (O is rescaled when it grows).  Warps 10 and 11 fetch the scale bytes of
+// their softmax group's tiles and expand them into a small ring.  Converting the codes to 16-bit
+// tiles in shared memory instead bounded the kernel: 2116 cycles a tile (bf16) where fetching it
+// takes 700, and 1.6 times the shared-memory traffic.
 //
-// Warp roles (384 threads, 512 with e4m3 pages): warps 0-3 and 4-7 the softmax groups, warp 8
-// the TMA producer, warp 9 the MMA issuer, warps 10-11 idle, warps 12-15 the conversion.
-// Tensor memory: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [256+D,256+2D).
+// Warp roles (384 threads): warps 0-3 and 4-7 the softmax groups, warp 8 the TMA producer, warp 9
+// the MMA issuer, warps 10-11 the scales of e4m3 pages.
+// Tensor memory: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [256+D,256+2D); P overwrites S.
 #pragma once
 
 #include "fa_cache_kernels.cuh"
@@ -45,12 +56,13 @@
 
 namespace fa {
 
-constexpr uint32_t kPagedLaunchRegs = 168;    // 16-bit pages, tiles of 128 rows
-constexpr uint32_t kPagedLaunchRegsQ8 = 128;  // e4m3 pages, tiles of 128 rows
+constexpr uint32_t kPagedLaunchRegs = 168;  // tiles of 128 rows
+constexpr int kPPieces = 3;                 // e5m2 pieces of a weight
+constexpr float kPShift = 7.0f;             // weights are 2^(x - m + 7) <= 2^15 with e4m3 pages
 
 // R = 0: tiles of 128 rows, both ways; R = 2, 4: one tile of 64 rows holding R copies of up to
 // 32 or 16 rows.
-template <int D, bool Q8, int R>
+template <int D, Elem E, bool Q8, int R>
 struct PgCfg {
   static constexpr bool kGeneral = R == 0;
   static constexpr int kCopies = kGeneral ? 1 : R;
@@ -58,25 +70,25 @@ struct PgCfg {
   static constexpr int kRows = kM / kCopies;          // rows of a partial result
   static constexpr int kSubs = kGeneral ? 2 : 1;      // partial results per segment
   static constexpr int kStageBytes = 128 * 16 * 4;    // 16 columns of every copy's rows, or of group 1's
-  static constexpr int kThreads = Q8 ? 512 : 384;
-  // setmaxnreg, general kernels only: 2 x 128 x 200 + 128 x 104 of 384 x 168, and with the
-  // conversion warps 128 x (2 x 184 + 72 + 72) of 512 x 128
-  static constexpr uint32_t kLaunch = Q8 ? kPagedLaunchRegsQ8 : kPagedLaunchRegs;
-  static constexpr uint32_t kRegsSoftmax = Q8 ? 184 : 200;
-  static constexpr uint32_t kRegsOther = Q8 ? 72 : 104;
-  static constexpr int kChunks = D / 64;
-  static constexpr int kChunkBytes = 128 * 128;
-  static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int kQChunkBytes = kM * 128;
-  static constexpr int kQBytes = kChunks * kQChunkBytes;
-  static constexpr int kRawBytes = 128 * D;
-  static constexpr int kScale = 128 / D;              // slots scale with the tile
-  static constexpr int kStages = (kGeneral ? (Q8 ? 3 : 4) : (Q8 ? 3 : 5)) * kScale;
-  static constexpr int kRaw = Q8 ? (kGeneral ? 3 : 5) * kScale : 1;
+  static constexpr int kThreads = 384;
+  // setmaxnreg, tiles of 128 rows only: 2 x 128 x 200 + 128 x 104 of 384 x 168
+  static constexpr uint32_t kRegsSoftmax = 200;
+  static constexpr uint32_t kRegsOther = 104;
+  static_assert(2 * kRegsSoftmax + kRegsOther <= kPagedLaunchRegs * 3, "register split");
+  // a row in shared memory: 128-byte chunks of 64 16-bit elements, or D codes (D = 64 in the
+  // 64-byte swizzle)
+  static constexpr int kRowBytes = Q8 ? D : 128;
+  static constexpr int kChunks = Q8 ? 1 : D / 64;
+  static constexpr int kChunkBytes = 128 * kRowBytes;
+  static constexpr int kTileBytes = kChunks * kChunkBytes;
+  static constexpr int kQParts = Q8 ? (E == Elem::kF16 ? 3 : 2) : D / 64;  // pieces, or chunks
+  static constexpr int kQPartBytes = kM * kRowBytes;
+  static constexpr int kQBytes = kQParts * kQPartBytes;
+  static constexpr int kStages = (Q8 ? (kGeneral ? 6 : 8) : (kGeneral ? 4 : 5)) * (128 / D);
+  static constexpr int kScaleRing = 4;
   static constexpr int kPArrive = kGeneral ? 128 : 4;
   static constexpr uint32_t kOCol = 256;
   static constexpr uint32_t kTmemCols = 512;
-  static_assert(2 * kRegsSoftmax + kRegsOther * (Q8 ? 2 : 1) <= kLaunch * (kThreads / 128), "register split");
 };
 
 struct PgArgs {
@@ -85,6 +97,7 @@ struct PgArgs {
   const int* table;       // [B, max_pages]
   const uint8_t* k_scales;
   const uint8_t* v_scales;
+  const float* q_scale;   // e4m3 pages: [T, H] factors of the query pieces
   void* out;              // [T, H, D]
   float* lse;             // [H, T]
   int* meta;              // total, L, unit prefix [B + 1], key-tile prefix [B + 1]
@@ -307,69 +320,127 @@ __device__ __forceinline__ bool pg_loads(const PgSeg& g, F f) {
   return true;
 }
 
-// ---------------------------------------------------------------- e4m3 codes to 16 bits
-// Sixteen codes times the scale of exponent byte eb, in order.
-template <Elem E>
-__device__ __forceinline__ void pg_convert16(const uint4& c, uint32_t eb, uint32_t (&o)[8]) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  if constexpr (E == Elem::kF16) {
-    // fp16 holds every code; 2^e is one fp16 factor for -14 <= e <= 15
-    if (eb - 113u <= 29u) {
-      const uint32_t f = ((eb - 112u) << 10) * 0x10001u;
+// ---------------------------------------------------------------- e4m3 pages
+// The pieces of every query row: piece i of (token, head) at pieces[((i T + token) H + head) D],
+// factors q_scale[token H + head].  L = D / 16 lanes per row.
+template <int D, Elem E>
+__global__ void __launch_bounds__(256) fa_paged_split_kernel(const void* q, int64_t token_stride, int64_t head_stride,
+                                                             uint8_t* pieces, float* q_scale, int T, int H,
+                                                             int* status) {
+  constexpr int L = D / 16;
+  constexpr int kPieces = PgCfg<D, E, true, 0>::kQParts;
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / L;
+  const int item = threadIdx.x % L;
+  const bool live = row < static_cast<int64_t>(T) * H;
+  const int64_t token = row / H;
+  const int h = static_cast<int>(row - token * H);
+  float f[16];
+  float amax = 0.f;
+  if (live) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const typename ElemOps<E>::T*>(q) +
+                                                      token * token_stride + h * head_stride + item * 16);
+    const uint4 x0 = __ldg(src), x1 = __ldg(src + 1);
+    const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 x, y;\n\tmov.b32 {lo, hi}, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 x, lo;\n\tcvt.rn.f16x2.e4m3x2 y, hi;\n\t"
-            "mul.rn.f16x2 %0, x, %3;\n\tmul.rn.f16x2 %1, y, %3;\n\t}"
-            : "=r"(o[2 * i]), "=r"(o[2 * i + 1])
-            : "r"(w[i]), "r"(f));
-      return;
+    for (int i = 0; i < 8; ++i) {
+      const float2 v = ElemOps<E>::unpack(w[i]);
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
     }
-  } else {
-    // Code s eeee mmm as bf16 bits s 0000eeee mmm0000 is the value times 2^-120 (subnormals
-    // included), so one multiplication by 2^(e + 120) gives it, for -126 <= e <= 7 and codes
-    // that are not NaN (0x7F).
-    uint32_t nan = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
-    if (eb - 1u <= 133u && !(nan & 0x80808080u)) {
-      const uint32_t f = ((eb + 120u) << 7) * 0x10001u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t p = __byte_perm(w[i], 0u, 0x1404), q = __byte_perm(w[i], 0u, 0x3424);
-        const uint32_t x = (p & 0x80008000u) | ((p >> 4) & 0x07f007f0u);
-        const uint32_t y = (q & 0x80008000u) | ((q >> 4) & 0x07f007f0u);
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[2 * i]) : "r"(x), "r"(f));
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[2 * i + 1]) : "r"(y), "r"(f));
-      }
-      return;
+    for (int i = 0; i < 16; ++i) {
+      if (fabsf(f[i]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(f[i]));
+      else f[i] = __uint_as_float(0x7fc00000u);
     }
   }
-  const float f = e8m0_to_float(eb);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = e4m3x2_to_float2(w[i]), q = e4m3x2_to_float2(w[i] >> 16);
-    o[2 * i] = ElemOps<E>::pack(p.x * f, p.y * f);
-    o[2 * i + 1] = ElemOps<E>::pack(q.x * f, q.y * f);
+  for (int o = 1; o < L; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  // the bf16 rule of the cache for both types: e4m3's largest is 448, 2^e <= 2^119
+  const int e = e4m3_exponent<Elem::kBf16>(amax);
+  const float inv = __int_as_float((127 - e) << 23);
+  if (!live || !FA_IN_BOUNDS(token < T && h < H && item * 16 + 16 <= D, status, 510)) return;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] *= inv;
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = pack_e4m3x4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+      const float2 a = e4m3x2_to_float2(c[i]), b = e4m3x2_to_float2(c[i] >> 16);
+      f[4 * i] -= a.x;
+      f[4 * i + 1] -= a.y;
+      f[4 * i + 2] -= b.x;
+      f[4 * i + 3] -= b.y;
+    }
+    *reinterpret_cast<uint4*>(pieces + ((static_cast<int64_t>(p) * T + token) * H + h) * D + item * 16) =
+        make_uint4(c[0], c[1], c[2], c[3]);
   }
+  if (item == 0) q_scale[row] = __int_as_float((127 + e) << 23);
 }
 
+// Four weights (an fp16 pair of pairs) to the three words of their e5m2 pieces.  The fp16 values
+// are rounded to 9 significant bits; the upper byte of an fp16 is its e5m2 truncation, and each
+// remainder is exact in fp16.
+__device__ __forceinline__ void split_e5m2(uint32_t a, uint32_t b, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+  a += 0x00020002u;
+  b += 0x00020002u;
+  p0 = __byte_perm(a, b, 0x7531);
+  uint32_t ra, rb;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(ra) : "r"(a), "r"(a & 0xff00ff00u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rb) : "r"(b), "r"(b & 0xff00ff00u));
+  p1 = __byte_perm(ra, rb, 0x7531);
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(a) : "r"(ra), "r"(ra & 0xff00ff00u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(b) : "r"(rb), "r"(rb & 0xff00ff00u));
+  p2 = __byte_perm(a, b, 0x7531);
+}
+
+// Weights of one score row of NC keys, 2^(s * c - m), times the value factors vs[] (shared
+// memory), as e5m2 pieces, four keys per word; l gets the fp32 sum of the weights.
+template <int NC>
+__device__ __forceinline__ void softmax_row_f8(const uint32_t (&s)[NC], const float* vs, uint32_t (&p0)[NC / 4],
+                                               uint32_t (&p1)[NC / 4], uint32_t (&p2)[NC / 4], float c, float m,
+                                               float& l) {
+  const float2 c2 = make_float2(c, c), nm2 = make_float2(-m, -m);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int i = 0; i < NC / 4; ++i) {
+    const float4 f = reinterpret_cast<const float4*>(vs)[i];
+    const float2 x = ffma2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), c2, nm2);
+    const float2 y = ffma2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), c2, nm2);
+    const float2 e0 = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+    const float2 e1 = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+    sum[0] = fadd2(sum[0], e0);
+    sum[1] = fadd2(sum[1], e1);
+    const float2 w0 = fmul2(e0, make_float2(f.x, f.y)), w1 = fmul2(e1, make_float2(f.z, f.w));
+    split_e5m2(pack_f16x2(w0.x, w0.y), pack_f16x2(w1.x, w1.y), p0[i], p1[i], p2[i]);
+  }
+  l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+
+// Scale factors of one key tile: of the scores, and of the weights relative to 2^e.
+struct PgScales {
+  float ks[128];
+  float vs[128];
+  int e;
+  int pad[3];
+};
+
 // ---------------------------------------------------------------- the kernel
-template <int D, bool Q8, int R>
+template <int D, Elem E, bool Q8, int R>
 struct __align__(1024) PgSmem {
-  using Cfg = PgCfg<D, Q8, R>;
+  using Cfg = PgCfg<D, E, Q8, R>;
   uint8_t q[2][Cfg::kQBytes];
   uint8_t kv[Cfg::kStages][Cfg::kTileBytes];
-  uint8_t raw[Cfg::kRaw][Q8 ? Cfg::kRawBytes : 16];
-  uint8_t scale[Cfg::kRaw][128];
   uint8_t stage[Cfg::kStageBytes];
-  float3 stat[2 * Cfg::kCopies][Cfg::kRows];  // m, l, lr of a split segment's copies
+  PgScales scales[2][Q8 ? Cfg::kScaleRing : 1];  // of each softmax group's tiles
+  float3 stat[2 * Cfg::kCopies][Cfg::kRows];     // m, l, lr of a split segment's copies
   uint64_t q_full[2];
   uint64_t q_empty[2];
   uint64_t kv_full[Cfg::kStages];
   uint64_t kv_empty[Cfg::kStages];
-  uint64_t raw_full[Cfg::kRaw];
-  uint64_t raw_empty[Cfg::kRaw];
+  uint64_t sc_full[2][Cfg::kScaleRing];
+  uint64_t sc_empty[2][Cfg::kScaleRing];
   uint64_t s_full[2];
   uint64_t p_full[2];
   uint64_t o_done[2];
@@ -380,28 +451,27 @@ struct __align__(1024) PgSmem {
   int abort_flag;
 };
 
-// Sets value rows [z0, z1) of a 16-bit tile to zero (one warp).
-template <int D>
+// Sets value rows [z0, z1) of a tile to zero (one warp).  kRowBytes per chunk, kChunks chunks.
+template <int kRowBytes, int kChunks>
 __device__ __forceinline__ void pg_zero_rows(uint8_t* tile, int z0, int z1, int lane) {
-  constexpr int kUnits = D / 8;  // 16-byte units per row
-  for (int u = lane; u < (z1 - z0) * kUnits; u += 32) {
-    const int row = z0 + u / kUnits;
-    const int c = u % kUnits;
-    *reinterpret_cast<uint4*>(tile + (c / 8) * 128 * 128 + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  constexpr int kUnits = kRowBytes / 16;
+  for (int u = lane; u < (z1 - z0) * kUnits * kChunks; u += 32) {
+    const int c = u % kChunks, x = u / kChunks;
+    *reinterpret_cast<uint4*>(tile + c * 128 * kRowBytes + z0 * kRowBytes + x * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
 template <int D, Elem E, bool Q8, int R>
-__global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
+__global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
     fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const PgArgs a) {
-  using Cfg = PgCfg<D, Q8, R>;
+  using Cfg = PgCfg<D, E, Q8, R>;
   constexpr int NS = Cfg::kStages;
-  constexpr int NR = Cfg::kRaw;
+  constexpr int NC8 = Cfg::kScaleRing;
   constexpr unsigned kFull = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
-  PgSmem<D, Q8, R>& sm = *reinterpret_cast<PgSmem<D, Q8, R>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                              ~static_cast<uintptr_t>(1023));
+  PgSmem<D, E, Q8, R>& sm = *reinterpret_cast<PgSmem<D, E, Q8, R>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                                    ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int G = a.H / a.H_kv;
@@ -417,13 +487,14 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
       mbar_init(&sm.o_done[i], 1);
     }
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&sm.kv_full[s], Q8 ? 4 : 1);
+      mbar_init(&sm.kv_full[s], 1);
       mbar_init(&sm.kv_empty[s], 1);
     }
-    for (int s = 0; s < NR; ++s) {
-      mbar_init(&sm.raw_full[s], 1);
-      mbar_init(&sm.raw_empty[s], 4);
-    }
+    for (int i = 0; i < 2; ++i)
+      for (int s = 0; s < NC8; ++s) {
+        mbar_init(&sm.sc_full[i][s], 1);
+        mbar_init(&sm.sc_empty[i][s], 4);
+      }
     mbar_init(&sm.groups, 8);
     mbar_init(&sm.mma_drain, 1);
     fence_mbar_init();
@@ -451,8 +522,8 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
   const PgPlan plan = sm.plan;
 
   // Each warpgroup's setmaxnreg sits at the top of the branch holding all of its code.
-  if (warp >= 8 && warp < 12) {
-    if constexpr (Cfg::kGeneral) regs_set<Cfg::kLaunch, Cfg::kRegsOther>();
+  if (warp >= 8) {
+    if constexpr (Cfg::kGeneral) regs_set<kPagedLaunchRegs, Cfg::kRegsOther>();
     if (warp == 8) {
       // ---------------------------------------------------------- TMA producer (whole warp)
       const WaitCtx wc{&sm.abort_flag, status, 31};
@@ -464,12 +535,13 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
       auto load_q = [&](int slot, int tok, int copies) -> bool {
         if (!wait_all(&sm.q_empty[slot], (qcnt[slot] & 1) ^ 1)) return false;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&sm.q_full[slot], static_cast<uint32_t>(copies * Cfg::kChunks * 128 * G * a.TQ));
+          mbar_arrive_expect_tx(&sm.q_full[slot],
+                                static_cast<uint32_t>(copies * Cfg::kQParts * Cfg::kRowBytes * G * a.TQ));
           for (int cp = 0; cp < copies; ++cp)
-            for (int c = 0; c < Cfg::kChunks; ++c)
+            for (int c = 0; c < Cfg::kQParts; ++c)
               if (FA_IN_BOUNDS(tok >= 0 && tok < a.T && g.kvh < a.H_kv && G * a.TQ <= Cfg::kRows, status, 501))
-                tma_load_4d(sm.q[slot] + c * Cfg::kQChunkBytes + cp * Cfg::kRows * 128, &tm_q, &sm.q_full[slot],
-                            c * 64, 0, g.kvh, tok);
+                tma_load_4d(sm.q[slot] + c * Cfg::kQPartBytes + cp * Cfg::kRows * Cfg::kRowBytes, &tm_q,
+                            &sm.q_full[slot], Q8 ? 0 : c * 64, 0, g.kvh, Q8 ? c * a.T + tok : tok);
         }
         __syncwarp();
         ++qcnt[slot];
@@ -506,33 +578,23 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
           // the boxes that hold a key of the unit
           const int k0 = max(g.keys.lo - (j << 7), 0) / box;
           const int k1 = (min(g.keys.hi - (j << 7), 128) + box - 1) / box;
-          const int slot = Q8 ? it % NR : it % NS;
-          uint64_t* full = Q8 ? &sm.raw_full[slot] : &sm.kv_full[slot];
-          if (!wait_all(Q8 ? &sm.raw_empty[slot] : &sm.kv_empty[slot], ((it / (Q8 ? NR : NS)) & 1) ^ 1)) return false;
-          const uint32_t bytes = static_cast<uint32_t>((k1 - k0) * box * (Q8 ? D + 1 : 2 * D));
-          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+          const int slot = it % NS;
+          if (!wait_all(&sm.kv_empty[slot], ((it / NS) & 1) ^ 1)) return false;
+          if (lane == 0)
+            mbar_arrive_expect_tx(&sm.kv_full[slot],
+                                  static_cast<uint32_t>((k1 - k0) * box * Cfg::kRowBytes * Cfg::kChunks));
           __syncwarp();
-          constexpr int kParts = Q8 ? 1 : Cfg::kChunks;
-          const int k = k0 + lane / kParts, c = lane % kParts;
+          const int k = k0 + lane / Cfg::kChunks, c = lane % Cfg::kChunks;
           const int held = (p0 >> 5) & 1 ? id_odd : id_even;
-          int id = __shfl_sync(kFull, held, (p0 + k) & 31);
+          const int id = __shfl_sync(kFull, held, (p0 + k) & 31);
           if (k < k1) {
             const int row = (j << 7) & (a.page - 1) & ~(box - 1);  // inside a page of 256
             const bool good = id >= 0 && id < a.P;
             if (!good) plan_fail(status, 44);
             // a bad page number reads as zeros: a coordinate past the pool
-            const int pl = good ? id * a.H_kv + g.kvh : a.P * a.H_kv;
-            if (FA_IN_BOUNDS(row + box <= a.page && p0 + k < a.max_pages && k * box < 128, status, 502)) {
-              if constexpr (Q8) {
-                tma_load_3d(sm.raw[slot] + k * box * D, isv ? &tm_v : &tm_k, full, 0, row, pl);
-                const uint8_t* sc = (isv ? a.v_scales : a.k_scales) +
-                                    (static_cast<int64_t>(good ? pl : g.kvh) * a.page + row);
-                bulk_load(sm.scale[slot] + k * box, sc, box, full);
-              } else {
-                tma_load_3d(sm.kv[slot] + c * Cfg::kChunkBytes + k * box * 128, isv ? &tm_v : &tm_k, full, c * 64, row,
-                            pl);
-              }
-            }
+            if (FA_IN_BOUNDS(row + box <= a.page && p0 + k < a.max_pages && k * box < 128, status, 502))
+              tma_load_3d(sm.kv[slot] + c * Cfg::kChunkBytes + k * box * Cfg::kRowBytes, isv ? &tm_v : &tm_k,
+                          &sm.kv_full[slot], c * 64, row, good ? id * a.H_kv + g.kvh : a.P * a.H_kv);
           }
           __syncwarp();
           ++it;
@@ -541,9 +603,8 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
       }
       if (!ok && lane == 0) {
         // Unwinding: wait (bounded) for the copies still in flight before the CTA exits.
-        constexpr uint32_t N = Q8 ? NR : NS;
-        for (uint32_t idx = (it > N ? it - N : 0); idx < it; ++idx)
-          mbar_wait_drain(Q8 ? &sm.raw_full[idx % N] : &sm.kv_full[idx % N], (idx / N) & 1, status);
+        for (uint32_t idx = (it > static_cast<uint32_t>(NS) ? it - NS : 0); idx < it; ++idx)
+          mbar_wait_drain(&sm.kv_full[idx % NS], (idx / NS) & 1, status);
         for (int i = 0; i < 2; ++i)
           if (qcnt[i] > 0) mbar_wait_drain(&sm.q_full[i], (qcnt[i] - 1) & 1, status);
       }
@@ -551,25 +612,50 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
     } else if (warp == 9) {
       // ---------------------------------------------------------- MMA issuer (whole warp)
       const WaitCtx wc{&sm.abort_flag, status, 32};
-      constexpr uint32_t idesc_s = idesc_kind_f16(Cfg::kM, kBN, 0, 0, ElemOps<E>::kMmaType);
-      constexpr uint32_t idesc_o = idesc_kind_f16(Cfg::kM, D, 0, 1, ElemOps<E>::kMmaType);
-      const uint64_t dq[2] = {sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), sdesc_sw128(smem_u32(sm.q[1]), 16, 1024)};
-      const uint64_t dk0 = sdesc_sw128(smem_u32(sm.kv[0]), 16, 1024);
-      const uint64_t dv0 = sdesc_sw128(smem_u32(sm.kv[0]), Cfg::kChunkBytes, 1024);
+      // Q, K K-major; P in TMEM, V MN-major
+      constexpr uint32_t idesc_s =
+          Q8 ? idesc_kind_f8(Cfg::kM, kBN, 0, 0, 0) : idesc_kind_f16(Cfg::kM, kBN, 0, 0, ElemOps<E>::kMmaType);
+      constexpr uint32_t idesc_o =
+          Q8 ? idesc_kind_f8(Cfg::kM, D, 0, 1, 1) : idesc_kind_f16(Cfg::kM, D, 0, 1, ElemOps<E>::kMmaType);
+      constexpr uint32_t kGroup = 8 * Cfg::kRowBytes;  // 8-row groups
+      auto desc = [](const void* p, uint32_t lbo, uint32_t sbo) {
+        return Cfg::kRowBytes == 64 ? sdesc_sw64(smem_u32(p), lbo, sbo) : sdesc_sw128(smem_u32(p), lbo, sbo);
+      };
+      const uint64_t dq[2] = {desc(sm.q[0], 16, kGroup), desc(sm.q[1], 16, kGroup)};
+      const uint64_t dk0 = desc(sm.kv[0], 16, kGroup);
+      const uint64_t dv0 = desc(sm.kv[0], Cfg::kChunkBytes, kGroup);
       auto issue_s = [&](int i, int qs, int slot) {
         const uint64_t dk = dk0 + static_cast<uint64_t>((slot * Cfg::kTileBytes) >> 4);
         const uint64_t dqi = qs ? dq[1] : dq[0];
+        if constexpr (Q8) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss_w(tbase + i * 128, dqi + (((kk / 4) * Cfg::kQChunkBytes + (kk % 4) * 32) >> 4),
-                    dk + (((kk / 4) * Cfg::kChunkBytes + (kk % 4) * 32) >> 4), idesc_s, kk > 0);
+          for (int p = 0; p < Cfg::kQParts; ++p)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              umma_ss_f8_w(tbase + i * 128, dqi + ((p * Cfg::kQPartBytes + kk * 32) >> 4), dk + ((kk * 32) >> 4),
+                           idesc_s, p + kk > 0);
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss_w(tbase + i * 128, dqi + (((kk / 4) * Cfg::kQPartBytes + (kk % 4) * 32) >> 4),
+                      dk + (((kk / 4) * Cfg::kChunkBytes + (kk % 4) * 32) >> 4), idesc_s, kk > 0);
+        }
       };
       auto issue_pv = [&](int i, int slot, uint32_t acc) {
         const uint64_t dv = dv0 + static_cast<uint64_t>((slot * Cfg::kTileBytes) >> 4);
+        const uint32_t tO = tbase + Cfg::kOCol + i * D, tP = tbase + i * 128;
+        if constexpr (Q8) {
 #pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)
-          umma_ts_w(tbase + Cfg::kOCol + i * D, tbase + i * 128 + kk * 8, dv + ((kk * 16 * 128) >> 4), idesc_o,
-                    (kk > 0) || acc);
+          for (int p = 0; p < kPPieces; ++p)
+#pragma unroll
+            for (int kk = 0; kk < kBN / 32; ++kk)
+              umma_ts_f8_w(tO, tP + p * 32 + kk * 8, dv + ((kk * 32 * Cfg::kRowBytes) >> 4), idesc_o,
+                           (p + kk > 0) || acc);
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            umma_ts_w(tO, tP + kk * 8, dv + ((kk * 16 * 128) >> 4), idesc_o, (kk > 0) || acc);
+        }
       };
       auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, wc)); };
       PgWalk w(a, plan);
@@ -584,16 +670,14 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
         return r;
       };
       // value rows of tile j that the unit does not see are zeroed: zero weights times stale
-      // infinities would not be zero (the conversion warps do it for e4m3 pages)
+      // infinities would not be zero
       auto clean = [&](int sv, int j) {
-        if constexpr (!Q8) {
-          const int z0 = max(g.keys.lo - (j << 7), 0), z1 = min(g.keys.hi - (j << 7), 128);
-          if (z0 > 0 || z1 < 128) {
-            pg_zero_rows<D>(sm.kv[sv], 0, z0, lane);
-            pg_zero_rows<D>(sm.kv[sv], z1, 128, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+        const int z0 = max(g.keys.lo - (j << 7), 0), z1 = min(g.keys.hi - (j << 7), 128);
+        if (z0 > 0 || z1 < 128) {
+          pg_zero_rows<Cfg::kRowBytes, Cfg::kChunks>(sm.kv[sv], 0, z0, lane);
+          pg_zero_rows<Cfg::kRowBytes, Cfg::kChunks>(sm.kv[sv], z1, 128, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
         }
       };
       while (ok && w.next(a, g)) {
@@ -690,71 +774,78 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
       umma_commit_w(&sm.mma_drain);
       mbar_wait_drain(&sm.mma_drain, 0, status);
       __syncwarp();
-    }
-  } else if (Q8 && warp >= 12) {
-    // ------------------------------------------------------------ e4m3 codes to 16-bit tiles
-    if constexpr (Cfg::kGeneral) regs_set<Cfg::kLaunch, Cfg::kRegsOther>();
-    const WaitCtx wc{&sm.abort_flag, status, 35};
-    constexpr int L = D / 16;          // threads per row
-    constexpr int kStep = 128 / L;     // rows per pass
-    constexpr int U = 4;
-    const int tid = threadIdx.x - 384;
-    const int item = tid % L, r0 = tid / L;
-    PgWalk w(a, plan);
-    PgSeg g;
-    uint32_t it = 0;
-    bool ok = true;
-    while (ok && w.next(a, g)) {
-      ok = pg_loads(g, [&](bool isv, int j) -> bool {
-        const int rs = it % NR, ks = it % NS;
-        if (!__all_sync(kFull, mbar_wait(&sm.raw_full[rs], (it / NR) & 1, wc))) return false;
-        if (!__all_sync(kFull, mbar_wait(&sm.kv_empty[ks], ((it / NS) & 1) ^ 1, wc))) return false;
-        ++it;
-        const int z0 = max(g.keys.lo - (j << 7), 0), z1 = min(g.keys.hi - (j << 7), 128);
-        uint8_t* dst = sm.kv[ks] + (item / 4) * Cfg::kChunkBytes;
-#pragma unroll 1
-        for (int base = r0; base < 128; base += U * kStep) {
-          uint4 c[U];
-          uint32_t eb[U];
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int row = base + u * kStep;
-            c[u] = *reinterpret_cast<const uint4*>(sm.raw[rs] + row * D + item * 16);
-            eb[u] = sm.scale[rs][row];
-          }
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int row = base + u * kStep;
-            uint32_t o[8];
-            if (row >= z0 && row < z1) {
-              pg_convert16<E>(c[u], eb[u], o);
-            } else {
-#pragma unroll
-              for (int x = 0; x < 8; ++x) o[x] = 0u;
-            }
-            // 16-byte units 2 (item % 4) and the next of the row's 128-byte swizzled chunk; the
-            // upper chunk's threads store the odd unit first, so that a row's eight threads
-            // cover all banks
-            const int u0 = (item % 4) * 2;
-            const int odd = (item / 4) & 1;
-            uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-            uint8_t* p = dst + row * 128;
-            *reinterpret_cast<uint4*>(p + (((u0 + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
-            *reinterpret_cast<uint4*>(p + (((u0 + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
-          }
+    } else if constexpr (Q8) {
+      // ---------------------------------------------------------- scales of group `grp`'s tiles
+      const int grp = warp - 10;
+      const WaitCtx wc{&sm.abort_flag, status, 35};
+      PgWalk w(a, plan);
+      PgSeg g;
+      uint32_t it = 0;
+      bool ok = true;
+      // the scale bytes of the lane's four keys of tile j; 1 for keys the unit does not see
+      auto fetch = [&](int j, uint32_t& kw, uint32_t& vw) {
+        kw = vw = 0x7f7f7f7fu;
+        const int key = (j << 7) + lane * 4;
+        if (key + 3 < g.keys.lo || key >= g.keys.hi) return;
+        const int pg = key >> a.page_shift;
+        const int id = pg < a.max_pages ? __ldg(a.table + static_cast<int64_t>(g.b) * a.max_pages + pg) : -1;
+        if (id < 0 || id >= a.P) return;
+        const int64_t at = (static_cast<int64_t>(id) * a.H_kv + g.kvh) * a.page + (key & (a.page - 1));
+        if (!FA_IN_BOUNDS(at >= 0 && at + 4 <= static_cast<int64_t>(a.P) * a.H_kv * a.page, status, 511)) return;
+        kw = __ldg(reinterpret_cast<const uint32_t*>(a.k_scales + at));
+        vw = __ldg(reinterpret_cast<const uint32_t*>(a.v_scales + at));
+      };
+      while (ok && w.next(a, g)) {
+        int j0 = g.kt0 + grp, j1 = g.kt0 + g.nt, dj = 2;
+        if (Cfg::kGeneral && g.pair) {
+          const PgRange r = pg_range(a, g, grp);
+          j0 = r.lo;
+          j1 = r.hi;
+          dj = 1;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.kv_full[ks]);
-          mbar_arrive(&sm.raw_empty[rs]);
+        int e = -1000;
+        uint32_t kw = 0, vw = 0, kn = 0, vn = 0;
+        if (j0 < j1) fetch(j0, kw, vw);
+        for (int j = j0; j < j1; j += dj) {
+          if (j + dj < j1) fetch(j + dj, kn, vn);  // in flight over this tile
+          const int slot = it % NC8;
+          ok = __all_sync(kFull, mbar_wait(&sm.sc_empty[grp][slot], ((it / NC8) & 1) ^ 1, wc));
+          if (!ok) break;
+          ++it;
+          PgScales& sc = sm.scales[grp][slot];
+          const int key = (j << 7) + lane * 4;
+          int ev[4], top = -1000;
+          bool in[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int b = (vw >> (8 * x)) & 255;
+            in[x] = key + x >= g.keys.lo && key + x < g.keys.hi;
+            ev[x] = b - 127;
+            if (in[x] && b != 255) top = max(top, ev[x]);
+          }
+          e = max(e, __reduce_max_sync(kFull, top));
+          if (e == -1000) e = 0;  // every scale NaN
+          float k4[4], v4[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            k4[x] = in[x] ? e8m0_to_float((kw >> (8 * x)) & 255) : 0.f;
+            const int d = ev[x] - e;  // <= 0; far below the largest is zero
+            v4[x] = !in[x] ? 0.f : (ev[x] == 128 ? __uint_as_float(0x7fc00000u)
+                                                 : (d < -126 ? 0.f : __int_as_float((127 + d) << 23)));
+          }
+          *reinterpret_cast<float4*>(sc.ks + lane * 4) = make_float4(k4[0], k4[1], k4[2], k4[3]);
+          *reinterpret_cast<float4*>(sc.vs + lane * 4) = make_float4(v4[0], v4[1], v4[2], v4[3]);
+          if (lane == 0) sc.e = e;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.sc_full[grp][slot]);
+          kw = kn;
+          vw = vn;
         }
-        return true;
-      });
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax groups
-    if constexpr (Cfg::kGeneral) regs_set<Cfg::kLaunch, Cfg::kRegsSoftmax>();
+    if constexpr (Cfg::kGeneral) regs_set<kPagedLaunchRegs, Cfg::kRegsSoftmax>();
     constexpr int NC = 128 / Cfg::kCopies;         // keys of a tile this warp handles
     constexpr int kQuarter = Cfg::kM / 4;          // accumulator rows per 32-lane quarter
     constexpr int kWarpsPerCopy = 4 / Cfg::kCopies;
@@ -771,7 +862,7 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
     const WaitCtx wc{&sm.abort_flag, status, 33 + grp};
     PgWalk w(a, plan);
     PgSeg g;
-    uint32_t scnt = 0, ocnt = 0, gcnt = 0;
+    uint32_t scnt = 0, ocnt = 0, gcnt = 0;  // scnt also counts the group's scale entries
     bool ok = true;
     while (ok && w.next(a, g)) {
       // this group's tile and its key tiles j0, j0 + dj, .. below j1
@@ -796,9 +887,21 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
       const int all_lo = a.window >= 0 ? g.pos0 + tok + ntok - 1 - a.window : 0;
       const bool rows_here = wrow0 < M;  // a warp without rows only keeps the barriers
       float m_ref = -INFINITY, l = 0.f, lr = 0.f;
+      // log2 units per score; with e4m3 pages the row's query factor, and the exponent of O
+      float c_row = a.scale_log2;
+      int e_ref = 0;
+      if constexpr (Q8) {
+        if (rc < M && FA_IN_BOUNDS(g.q0 + tok + iq < a.T, status, 512))
+          c_row *= __ldg(a.q_scale + (static_cast<int64_t>(g.q0) + tok + iq) * a.H + g.kvh * G + rc - iq * G);
+      }
       for (int j = j0; j < j1; j += dj) {
         ok = __all_sync(kFull, mbar_wait(&sm.s_full[grp], scnt & 1, wc));
         if (!ok) break;
+        const int sslot = scnt % NC8;
+        if constexpr (Q8) {
+          ok = __all_sync(kFull, mbar_wait(&sm.sc_full[grp][sslot], (scnt / NC8) & 1, wc));
+          if (!ok) break;
+        }
         ++scnt;
         tc_fence_after();
         if (rows_here) {
@@ -807,6 +910,21 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < NC; c += 32) tmem_ld32(tS + col0 + c, s + c);
           tmem_wait_ld();
+          if constexpr (Q8) {
+            const float4* ks = reinterpret_cast<const float4*>(sm.scales[grp][sslot].ks + col0);
+#pragma unroll
+            for (int c = 0; c < NC / 4; ++c) {
+              const float4 f = ks[c];
+              const float2 x = fmul2(make_float2(__uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 1])),
+                                     make_float2(f.x, f.y));
+              const float2 y = fmul2(make_float2(__uint_as_float(s[4 * c + 2]), __uint_as_float(s[4 * c + 3])),
+                                     make_float2(f.z, f.w));
+              s[4 * c] = __float_as_uint(x.x);
+              s[4 * c + 1] = __float_as_uint(x.y);
+              s[4 * c + 2] = __float_as_uint(y.x);
+              s[4 * c + 3] = __float_as_uint(y.y);
+            }
+          }
           if (k0 + NC - 1 > all_hi || k0 < all_lo) {
             const int lim = vis_hi - k0, first = vis_lo - k0;
 #pragma unroll
@@ -823,15 +941,22 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
               mx8[x] = fmax3(mx8[x], __uint_as_float(s[c + x]), __uint_as_float(s[c + 8 + x]));
           const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                                  fmaxf(mx8[6], mx8[7]));
-          const float m_new = mx * a.scale_log2;
+          const float m_new = mx * c_row;
           const bool raise = m_new > m_ref + kTau;
-          if (__any_sync(kFull, raise)) {
-            const float alpha = raise ? ex2_approx(m_ref - m_new) : 1.0f;
-            if (raise) {
-              l *= alpha;
-              lr *= alpha;
-              m_ref = m_new;
-            }
+          bool grown = false;  // the value exponent grew: O is held in units of 2^e_ref
+          float alpha = raise ? ex2_approx(m_ref - m_new) : 1.0f;
+          if constexpr (Q8) {
+            const int e = sm.scales[grp][sslot].e;
+            grown = j > j0 && e > e_ref;
+            if (raise) l *= alpha;
+            if (grown) alpha = e - e_ref > 126 ? 0.f : alpha * __int_as_float((127 + e_ref - e) << 23);
+            e_ref = e;
+          } else if (raise) {
+            l *= alpha;
+            lr *= alpha;
+          }
+          if (raise) m_ref = m_new;
+          if (__any_sync(kFull, raise) || grown) {
             if (j > j0) {
               // the commit that signalled this S covers the group's previous P.V
 #pragma unroll 1
@@ -846,21 +971,41 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
               tmem_wait_st();
             }
           }
-          uint32_t p[NC / 2];
           const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-          softmax_row<E, NC>(s, p, a.scale_log2, m_use, l, lr);
           // P for all 128 keys: this copy's columns, zeros for the other copies' keys
+          uint32_t zero[16];
 #pragma unroll
-          for (int x = 0; x < NC / 2; x += 16) tmem_st16(tS + col0 / 2 + x, p + x);
-          if constexpr (Cfg::kCopies > 1) {
-            uint32_t zero[16];
+          for (int x = 0; x < 16; ++x) zero[x] = 0u;
+          if constexpr (Q8) {
+            uint32_t p0[NC / 4], p1[NC / 4], p2[NC / 4];
+            softmax_row_f8<NC>(s, sm.scales[grp][sslot].vs + col0, p0, p1, p2, c_row, m_use - kPShift, l);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) zero[x] = 0u;
+            for (int x = 0; x < NC / 4; x += 8) {
+              tmem_st8(tS + col0 / 4 + x, p0 + x);
+              tmem_st8(tS + 32 + col0 / 4 + x, p1 + x);
+              tmem_st8(tS + 64 + col0 / 4 + x, p2 + x);
+            }
+            if constexpr (Cfg::kCopies > 1) {
 #pragma unroll
-            for (int c = 0; c < 64; c += 16)
-              if (c < col0 / 2 || c >= col0 / 2 + NC / 2) tmem_st16(tS + c, zero);
+              for (int c = 0; c < 96; c += 8)
+                if ((c & 31) < col0 / 4 || (c & 31) >= col0 / 4 + NC / 4) tmem_st8(tS + c, zero);
+            }
+          } else {
+            uint32_t p[NC / 2];
+            softmax_row<E, NC>(s, p, a.scale_log2, m_use, l, lr);
+#pragma unroll
+            for (int x = 0; x < NC / 2; x += 16) tmem_st16(tS + col0 / 2 + x, p + x);
+            if constexpr (Cfg::kCopies > 1) {
+#pragma unroll
+              for (int c = 0; c < 64; c += 16)
+                if (c < col0 / 2 || c >= col0 / 2 + NC / 2) tmem_st16(tS + c, zero);
+            }
           }
           tmem_wait_st();
+        }
+        if constexpr (Q8) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.sc_empty[grp][sslot]);
         }
         tc_fence_before();
         if constexpr (Cfg::kPArrive == 4) {
@@ -871,6 +1016,13 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
         }
       }
       if (!ok) break;
+      float unit = 1.0f;  // of O
+      if constexpr (Q8) {
+        // weights carry 2^7, and fp32 sums normalise them
+        m_ref -= kPShift;
+        lr = l;
+        unit = e8m0_to_float(static_cast<uint32_t>(e_ref + 127));
+      }
       if (any) {
         ok = __all_sync(kFull, mbar_wait(&sm.o_done[grp], ocnt & 1, wc));
         if (!ok) break;
@@ -929,7 +1081,7 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
       };
       if (pair) {
         // O normalised by the sum of the rounded weights, and the log-sums of both
-        const float inv = lr == 0.f ? 0.f : 1.0f / lr;
+        const float inv = lr == 0.f ? 0.f : unit / lr;
         if (rows_here) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
@@ -971,7 +1123,7 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
             ls += e * st.y;
             lrs += e * st.z;
           }
-          wgt = (lr == 0.f || lrs == 0.f) ? 0.f : ex2_approx(m_ref - ref) / lrs;
+          wgt = (lr == 0.f || lrs == 0.f) ? 0.f : ex2_approx(m_ref - ref) * unit / lrs;
           if (me == 0) put_lse(ref, ls, lrs);
         }
 #pragma unroll 1
@@ -1047,7 +1199,7 @@ __global__ void __launch_bounds__(PgCfg<D, Q8, R>::kThreads, 1)
 template <int D, Elem E, int R, int W>
 __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PgArgs a) {
   using T = typename ElemOps<E>::T;
-  using Cfg = PgCfg<D, false, R>;
+  using Cfg = PgCfg<D, E, false, R>;
   constexpr unsigned kFull = 0xffffffffu;
   constexpr int V = D / 32;  // columns per lane
   __shared__ float acc_sh[W > 1 ? W : 1][D];

@@ -9,13 +9,13 @@ namespace fa {
 
 template <int D, Elem E, bool Q8, int R>
 fa_status launch_paged(DeviceInfo& di, const PagedCall& c) {
-  using Cfg = PgCfg<D, Q8, R>;
+  using Cfg = PgCfg<D, E, Q8, R>;
   const fa_paged_problem& p = c.p;
   auto kern = fa_paged_kernel<D, E, Q8, R>;
-  const int smem = static_cast<int>(sizeof(PgSmem<D, Q8, R>)) + 1024;
-  static_assert(sizeof(PgSmem<D, Q8, R>) + 1024 <= 232448, "shared memory of one CTA");
+  const int smem = static_cast<int>(sizeof(PgSmem<D, E, Q8, R>)) + 1024;
+  static_assert(sizeof(PgSmem<D, E, Q8, R>) + 1024 <= 232448, "shared memory of one CTA");
   if (!once_per_device(di.paged_attr[E == Elem::kF16][Q8][D == 128][R / 2], [&] {
-        return (!Cfg::kGeneral || launch_regs_ok(kern, Cfg::kLaunch)) &&
+        return (!Cfg::kGeneral || launch_regs_ok(kern, kPagedLaunchRegs)) &&
                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
       }))
     return FA_ERR_LAUNCH;
@@ -25,20 +25,24 @@ fa_status launch_paged(DeviceInfo& di, const PagedCall& c) {
   const MapElem pe = Q8 ? MapElem::kE4M3 : me;
   const long long planes = static_cast<long long>(p.P) * p.H_kv;
   const int box = p.page < 128 ? p.page : 128;
-  CUtensorMap mq, mk, mv;
-  if (!make_ragged_q_map(&mq, c.q, p.T, p.H_kv, G, D, p.q_stride[0], p.q_stride[1], TQ, me) ||
-      !make_pages_map(&mk, c.k_pages, planes, p.page, D, box, pe) ||
-      !make_pages_map(&mv, c.v_pages, planes, p.page, D, box, pe))
-    return FA_ERR_LAUNCH;
   const int grid = di.sm_count;
   const PagedLayout L = paged_layout(p, grid);
   uint8_t* w = static_cast<uint8_t*>(c.workspace);
+  CUtensorMap mq, mk, mv;
+  // e4m3 pages: the query pieces, one batch of tokens after the other
+  if (!(Q8 ? make_ragged_q_map(&mq, w + L.pieces, Cfg::kQParts * static_cast<long long>(p.T), p.H_kv, G, D,
+                               static_cast<long long>(p.H) * D, D, TQ, MapElem::kE4M3)
+           : make_ragged_q_map(&mq, c.q, p.T, p.H_kv, G, D, p.q_stride[0], p.q_stride[1], TQ, me)) ||
+      !make_pages_map(&mk, c.k_pages, planes, p.page, D, box, pe) ||
+      !make_pages_map(&mv, c.v_pages, planes, p.page, D, box, pe))
+    return FA_ERR_LAUNCH;
   PgArgs a{};
   a.cu = c.cu;
   a.seqlens = c.seqlens;
   a.table = c.page_table;
   a.k_scales = static_cast<const uint8_t*>(c.k_scales);
   a.v_scales = static_cast<const uint8_t*>(c.v_scales);
+  a.q_scale = reinterpret_cast<const float*>(w + L.q_scale);
   a.out = c.o;
   a.lse = c.lse;
   a.meta = reinterpret_cast<int*>(w + L.meta);
@@ -59,6 +63,12 @@ fa_status launch_paged(DeviceInfo& di, const PagedCall& c) {
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.slots = L.slots;
   a.status = di.status;
+  if constexpr (Q8) {
+    const long long threads = static_cast<long long>(p.T) * p.H * (D / 16);
+    fa_paged_split_kernel<D, E><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, c.stream>>>(
+        c.q, p.q_stride[0], p.q_stride[1], w + L.pieces, reinterpret_cast<float*>(w + L.q_scale), p.T, p.H, di.status);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
+  }
   kern<<<grid, Cfg::kThreads, smem, c.stream>>>(mq, mk, mv, a);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
   // few rows: a block per row, its four warps sharing the partial results; otherwise a warp per

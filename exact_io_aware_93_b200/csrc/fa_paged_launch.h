@@ -44,9 +44,10 @@ inline long long paged_units(const fa_paged_problem& p) {
 
 // Workspace regions: the plan (total, tiles per CTA, unit and key-tile prefixes), then the
 // partial log-sums [rows, 2] and the partial outputs [rows, d]; a CTA leaves at most two
-// partial segments of 256 rows (16 or 32 where a tile holds copies).
+// partial segments of 256 rows (16 or 32 where a tile holds copies).  With e4m3 pages also the
+// query pieces (2 or 3 bytes per element) and a factor per query row.
 struct PagedLayout {
-  size_t meta, part_lse, part_o, total;
+  size_t meta, part_lse, part_o, pieces, q_scale, total;
   long long slots;
 };
 inline PagedLayout paged_layout(const fa_paged_problem& p, int grid) {
@@ -58,7 +59,10 @@ inline PagedLayout paged_layout(const fa_paged_problem& p, int grid) {
   L.meta = 0;
   L.part_lse = round256((2 + 2 * (static_cast<size_t>(p.B) + 1)) * 4);
   L.part_o = L.part_lse + round256(rows * 2 * 4);
-  L.total = L.part_o + rows * static_cast<size_t>(p.d) * 4;
+  L.pieces = L.part_o + round256(rows * static_cast<size_t>(p.d) * 4);
+  const size_t q_rows = p.quant ? static_cast<size_t>(p.T) * p.H : 0;
+  L.q_scale = L.pieces + round256(q_rows * p.d * (p.dtype == FA_DTYPE_F16 ? 3 : 2));
+  L.total = L.q_scale + q_rows * 4;
   return L;
 }
 

@@ -215,6 +215,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -243,6 +249,11 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
   return d;
 }
 
+// The same for the 64-byte swizzle (rows of 64 B, 8-row groups of 512 B).
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (sdesc_sw128(saddr, lbo, sbo) & ~(static_cast<uint64_t>(7) << 61)) | (static_cast<uint64_t>(4) << 61);
+}
+
 // Instruction descriptor, kind::f16 with fp32 accumulator; A and B both of `type`
 // (1 = bf16, 0 = f16).
 __host__ __device__ constexpr uint32_t idesc_kind_f16(int M, int N, int a_mn_major, int b_mn_major, uint32_t type = 1) {
@@ -252,6 +263,11 @@ __host__ __device__ constexpr uint32_t idesc_kind_f16(int M, int N, int a_mn_maj
          | (static_cast<uint32_t>(a_mn_major) << 15)  // A major
          | (static_cast<uint32_t>(b_mn_major) << 16)  // B major
          | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// kind::f8f6f4 with fp32 accumulator; A of format `a_type` (0 = e4m3, 1 = e5m2), B e4m3.
+__host__ __device__ constexpr uint32_t idesc_kind_f8(int M, int N, int a_mn_major, int b_mn_major, uint32_t a_type) {
+  return idesc_kind_f16(M, N, a_mn_major, b_mn_major, 0) | (a_type << 7);
 }
 
 // MMA issue.  Every lane of the calling warp executes these with the same operands and one

@@ -72,25 +72,30 @@ inline bool make_decode_q_map(CUtensorMap* map, const void* base, int B, int N_q
 }
 
 // Queries of a ragged batch [T, H, d] with element strides (token, head): one box holds the G
-// consecutive heads of a key/value head for `tokens` tokens, 64 columns wide; in shared memory
-// rows r = i * G + g of 128 bytes (128-byte swizzle).  Tokens past T read as zero.
-inline bool make_ragged_q_map(CUtensorMap* map, const void* base, int T, int H_kv, int G, int d, long long token_stride,
+// consecutive heads of a key/value head for `tokens` tokens: 64 columns of 16-bit elements, or
+// all d of 8-bit ones; in shared memory rows r = i * G + g of 128 bytes (128-byte swizzle), or of
+// d codes.  Tokens past T read as zero.
+inline CUtensorMapSwizzle codes_swizzle(int d) { return d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B; }
+inline bool make_ragged_q_map(CUtensorMap* map, const void* base, long long T, int H_kv, int G, int d, long long token_stride,
                               long long head_stride, int tokens, MapElem e) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return false;
+  const cuuint64_t eb = map_bytes(e);
+  const bool codes = e == MapElem::kE4M3;
   cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)G, (cuuint64_t)H_kv, (cuuint64_t)T};
-  cuuint64_t strides[3] = {(cuuint64_t)head_stride * 2, (cuuint64_t)head_stride * G * 2, (cuuint64_t)token_stride * 2};
-  cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)tokens};
+  cuuint64_t strides[3] = {(cuuint64_t)head_stride * eb, (cuuint64_t)head_stride * G * eb,
+                           (cuuint64_t)token_stride * eb};
+  cuuint32_t box[4] = {(cuuint32_t)(codes ? d : 64), (cuuint32_t)G, 1, (cuuint32_t)tokens};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(map, map_type(e), 4, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? codes_swizzle(d) : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
 // A pool of pages [planes, page, d] (plane = page number * H_kv + head) with boxes of `rows`
-// slots: 64 columns in the 128-byte swizzle for 16-bit elements, whole rows without a swizzle
-// for e4m3 codes.  A plane past the pool reads as zeros.
+// slots: 64 columns of 16-bit elements, or whole rows of e4m3 codes.  A plane past the pool reads as zeros.
 inline bool make_pages_map(CUtensorMap* map, const void* base, long long planes, int page, int d, int rows, MapElem e) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return false;
@@ -101,7 +106,7 @@ inline bool make_pages_map(CUtensorMap* map, const void* base, long long planes,
   cuuint32_t box[3] = {(cuuint32_t)(codes ? d : 64), (cuuint32_t)rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(map, map_type(e), 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? codes_swizzle(d) : CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
