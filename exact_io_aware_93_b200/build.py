@@ -58,7 +58,8 @@ def up_to_date(path: str = LIB_PATH) -> bool:
 REG_CONTRACT = {
     "fa_fwd_kernel": ("fa_fwd_kernel.cuh", "kLaunchRegs"),
     "fa_bwd_main_kernel": ("fa_bwd_kernel.cuh", "kBwdLaunchRegs"),
-    "fa_paged_kernel.*ELi0E": ("fa_paged_kernel.cuh", "kPagedLaunchRegs"),
+    "fa_paged_kernel.*ELb0ELi0E": ("fa_paged_kernel.cuh", "kPagedLaunchRegs"),
+    "fa_paged_kernel.*ELb1ELi0E": ("fa_paged_kernel.cuh", "kPagedLaunchRegsConv"),
 }
 
 

@@ -27,7 +27,7 @@ fa_status check_paged(const fa_paged_problem& p) {
   const long long planes = static_cast<long long>(p.P) * p.H_kv;
   if (cap > INT_MAX - 1024 || planes >= INT_MAX || p.H_kv > 65535 || p.T > INT_MAX / 4) return FA_ERR_INVALID_ARG;
   const long double tiles = static_cast<long double>(fa::paged_units(p)) * p.H_kv * ((cap + 127) / 128);
-  if (tiles > static_cast<long double>(1ll << 30)) return FA_ERR_INVALID_ARG;
+  if (tiles > static_cast<long double>(1ll << 28)) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
 

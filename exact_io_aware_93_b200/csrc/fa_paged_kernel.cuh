@@ -9,45 +9,54 @@
 //
 // Work list.  A unit visits T = hi - lo tiles of 128 keys, those that some row of it sees
 // (causal: up to its last token; window: from its first token's first key).  The key tiles of
-// all units are laid end to end (sequence, key/value head, unit) and CTA c of the persistent
-// grid takes [c L, (c+1) L), L = ceil(total / grid): every SM gets the same number of key
-// tiles whatever the mix of chunks, single tokens and lengths.  A CTA's run falls into
-// SEGMENTS, each inside one unit; a segment that is not a whole unit leaves a partial result
-// (O normalised, log-sums) that fa_paged_merge_kernel joins.  The lengths are read on the
-// device, so a captured graph replays as they grow.
+// all units are laid end to end (sequence, key/value head, unit), each as long as it takes
+// (PgCfg::kPairCost, kSplitCost), and CTA c of the persistent grid takes the tiles that start in
+// [c L, (c+1) L), L = total / grid: every SM gets the same work whatever the mix of chunks,
+// single tokens and lengths.  A CTA's run falls into SEGMENTS, each inside one unit; a segment
+// that is not a whole unit leaves a partial result (O normalised, log-sums) that
+// fa_paged_merge_kernel joins.  The lengths are read on the device, so a captured graph replays
+// as they grow.
 //
 // Two ways through a segment, chosen per unit:
 //   pair    two tiles: softmax group g owns tile g and both share one stream of K/V tiles, in
 //           the order PV_0(j), S_0(j+1), PV_1(j), S_1(j+1) of the forward kernel.
 //   split   one tile: group g takes the segment's key tiles g, g + 2, ..: two independent
 //           online softmaxes over disjoint keys, joined through shared memory at its end.
-// Few rows (G * max_q <= 32, every unit split) use M = 64 MMAs and COPIES of the rows: copy c
-// of R takes keys [c 128/R, (c+1) 128/R) of every tile, so a softmax warp handles 32 or 64 keys
-// of a tile instead of 128 (see fa_decode_kernel.cuh).
+// Few rows (G * max_q <= 32, every unit split) use tiles that hold COPIES of the rows: copy c of
+// R takes keys [c 128/R, (c+1) 128/R) of every tile, so a softmax warp handles 32 or 64 keys of a
+// tile instead of 128 (see fa_decode_kernel.cuh).
 //
 // Pages.  A key tile is 128 / page boxes (or a part of one page), each fetched by its own lane
 // of the producer warp; page numbers are read 32 at a time, one window ahead.  Pages that no row
 // of the unit sees are not fetched, and value rows outside the unit's keys are zeroed in shared
 // memory: stale slots, and pages a sliding window has left behind, may hold anything.
 //
-// e4m3 pages.  The tensor core takes the codes as they are (kind::f8f6f4), so nothing is
-// converted and a tile moves half the bytes.  What is not e4m3 is cut into pieces that are, and
-// the products of the pieces are summed by the accumulator:
-//   Q   fa_paged_split_kernel writes q = 2^eq (q1 + q2 [+ q3]), each piece the e4m3 rounding of
-//       what the ones before it left: 4 significant bits each, so two pieces hold a bf16 exactly
-//       and three an fp16 (down to 2^-18 of the row's largest).
-//   P   the weight, an fp16 value rounded to 9 bits, is the sum of three e5m2 pieces (e5m2 is the
-//       upper byte of an fp16): relative error 2^-9 down to 2^-23 of the largest weight.  e5m2
-//       and not e4m3 for its range: a long tail of small weights beside a large one keeps its
-//       mass.
-// The scales: S_j is multiplied by 2^ek_j, and the weight by 2^(ev_j - E), E the segment's largest
-// value exponent so far (O is rescaled when it grows).  Warps 10 and 11 fetch the scale bytes of
-// their softmax group's tiles and expand them into a small ring.  Converting the codes to 16-bit
-// tiles in shared memory instead bounded the kernel: 2116 cycles a tile (bf16) where fetching it
-// takes 700, and 1.6 times the shared-memory traffic.
+// e4m3 pages.  The tensor core takes the codes as they are (kind::f8f6f4): a tile moves half the
+// bytes and K is never converted.  What is not e4m3 is cut into pieces that are, and the products
+// of the pieces are summed:
+//   Q   fa_paged_split_kernel writes q = 2^eq (q1 + q2), q1 the e4m3 rounding of q / 2^eq and q2
+//       that of the rest: exact for bf16, 8 significant bits of an fp16's 11 (down to 2^-18 of
+//       the row's largest).  A third piece would cost half as many products again for bits that
+//       the cache's own 4-bit significands bury.
+//   P   with few rows: the weight, an fp16 value rounded to 9 bits, is the sum of three e5m2
+//       pieces (e5m2 is the upper byte of an fp16): relative error 2^-9 down to 2^-23 of the
+//       largest weight.  e5m2 and not e4m3 for its range: a long tail of small weights beside a
+//       large one keeps its mass.
+//   V   with tiles of 128 rows the pieces would cost the softmax warps more than its exponentials,
+//       so there a fourth warpgroup turns V's codes into fp16 tiles, code * 2^(ev - E) (exact),
+//       and P is one fp16 operand for both element types.
+// The scales: S_j is multiplied by 2^ek_j, and P or V by 2^(ev_j - E), E the segment's largest
+// value exponent so far (O is rescaled when it grows).  Warps 10 and 11 fetch the scale bytes and
+// expand them into small rings.  (Converting K and V of every tile to 16 bits bounded the kernel:
+// 2116 cycles a tile and a bf16 result, where fetching one takes 700.)
+//   Up to 8 rows  each row takes 4 of a warp's lanes, 8 apart: the rows of the pieces q1 and q2
+//       give partial scores that a shuffle adds, and each lane stores one piece of P: 4 + 4
+//       products of 64 cycles per tile instead of 8 + 12.
 //
-// Warp roles (384 threads): warps 0-3 and 4-7 the softmax groups, warp 8 the TMA producer, warp 9
-// the MMA issuer, warps 10-11 the scales of e4m3 pages.
+// Warp roles (384 threads, 512 with e4m3 pages and tiles of 128 rows): warps 0-3 and 4-7 the
+// softmax groups, warp 8 the schedule and the TMA loads, warp 9 the MMA issuer, warps 10-11 the
+// scales, warps 12-15 the conversion of V.  Warp 8 writes each segment into a small ring that all
+// others follow.
 // Tensor memory: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [256+D,256+2D); P overwrites S.
 #pragma once
 
@@ -56,36 +65,52 @@
 
 namespace fa {
 
-constexpr uint32_t kPagedLaunchRegs = 168;  // tiles of 128 rows
-constexpr int kPPieces = 3;                 // e5m2 pieces of a weight
-constexpr float kPShift = 7.0f;             // weights are 2^(x - m + 7) <= 2^15 with e4m3 pages
+constexpr uint32_t kPagedLaunchRegs = 168;      // 16-bit pages, tiles of 128 rows
+constexpr uint32_t kPagedLaunchRegsConv = 128;  // e4m3 pages, tiles of 128 rows
+constexpr int kPPieces = 3;                     // e5m2 pieces of a weight
+constexpr float kPShift = 7.0f;                 // weights cut into pieces are 2^(x - m + 7) <= 2^15
 
-// R = 0: tiles of 128 rows, both ways; R = 2, 4: one tile of 64 rows holding R copies of up to
-// 32 or 16 rows.
+// R = 0: tiles of 128 rows, both ways; R = 2, 4: one tile of 64 rows holding R copies of up to 32
+// or 16 rows; R = 8 (e4m3 pages): 128 rows holding 4 copies of up to 8 rows, 4 lanes each.
 template <int D, Elem E, bool Q8, int R>
 struct PgCfg {
   static constexpr bool kGeneral = R == 0;
-  static constexpr int kCopies = kGeneral ? 1 : R;
-  static constexpr int kM = kGeneral ? 128 : 64;
-  static constexpr int kRows = kM / kCopies;          // rows of a partial result
+  static constexpr bool kConv = Q8 && kGeneral;       // V as fp16 tiles
+  static constexpr int kSlots = R == 8 ? 4 : 1;       // lanes of a row
+  static constexpr int kCopies = kGeneral ? 1 : (R == 8 ? 4 : R);
+  static constexpr int kM = (kGeneral || R == 8) ? 128 : 64;
+  static constexpr int kRows = kM / kCopies / kSlots; // rows of a partial result
   static constexpr int kSubs = kGeneral ? 2 : 1;      // partial results per segment
-  static constexpr int kStageBytes = 128 * 16 * 4;    // 16 columns of every copy's rows, or of group 1's
-  static constexpr int kThreads = 384;
-  // setmaxnreg, tiles of 128 rows only: 2 x 128 x 200 + 128 x 104 of 384 x 168
-  static constexpr uint32_t kRegsSoftmax = 200;
-  static constexpr uint32_t kRegsOther = 104;
-  static_assert(2 * kRegsSoftmax + kRegsOther <= kPagedLaunchRegs * 3, "register split");
+  static constexpr int kStageCols = kGeneral ? 16 : 32;  // columns joined at a time
+  static constexpr int kStageRows = kGeneral ? 128 : 2 * kCopies * kRows;
+  static constexpr int kThreads = kConv ? 512 : 384;
+  // setmaxnreg, tiles of 128 rows only: 2 x 128 x 200 + 128 x 104 of 384 x 168, and with the
+  // conversion warps 128 x (2 x 184 + 72 + 72) of 512 x 128
+  static constexpr uint32_t kLaunch = kConv ? kPagedLaunchRegsConv : kPagedLaunchRegs;
+  static constexpr uint32_t kRegsSoftmax = kConv ? 184 : 200;
+  static constexpr uint32_t kRegsOther = kConv ? 72 : 104;
+  static_assert(2 * kRegsSoftmax + (kConv ? 2 : 1) * kRegsOther <= kLaunch * (kThreads / 128), "register split");
+  // time of a key tile, in the work list's units: of a pair, and of a single tile
+  static constexpr int kPairCost = kConv ? 5 : 3;
+  static constexpr int kSplitCost = 2;
   // a row in shared memory: 128-byte chunks of 64 16-bit elements, or D codes (D = 64 in the
   // 64-byte swizzle)
   static constexpr int kRowBytes = Q8 ? D : 128;
   static constexpr int kChunks = Q8 ? 1 : D / 64;
   static constexpr int kChunkBytes = 128 * kRowBytes;
   static constexpr int kTileBytes = kChunks * kChunkBytes;
-  static constexpr int kQParts = Q8 ? (E == Elem::kF16 ? 3 : 2) : D / 64;  // pieces, or chunks
+  static constexpr int kQParts = Q8 ? (R == 8 ? 1 : 2) : D / 64;  // pieces, or chunks
   static constexpr int kQPartBytes = kM * kRowBytes;
   static constexpr int kQBytes = kQParts * kQPartBytes;
-  static constexpr int kStages = (Q8 ? (kGeneral ? 6 : 8) : (kGeneral ? 4 : 5)) * (128 / D);
+  static constexpr int kScale = 128 / D;              // slots scale with the tile
+  // the ring of K and V tiles, or of K tiles beside V's codes and fp16 tiles
+  static constexpr int kStages = (kConv ? 2 : (Q8 ? 8 : 4)) * kScale;
+  static constexpr int kVRaw = kConv ? 2 * kScale : 1;
+  static constexpr int kV16 = kConv ? 2 * kScale : 1;
+  static constexpr int kV16Bytes = kConv ? 128 * D * 2 : 16;
   static constexpr int kScaleRing = 4;
+  static constexpr int kSegRing = 4;
+  static constexpr int kSegReaders = 9 + (Q8 ? 2 : 0) + (kConv ? 4 : 0);  // warps
   static constexpr int kPArrive = kGeneral ? 128 : 4;
   static constexpr uint32_t kOCol = 256;
   static constexpr uint32_t kTmemCols = 512;
@@ -153,46 +178,57 @@ __device__ __forceinline__ PgKeys pg_unit_keys(const PgArgs& a, const PgSeq& s, 
   return pg_keys(a, s.len, p0, p0 + ntok - 1);
 }
 
-__device__ __forceinline__ int pg_seq_tiles(const PgArgs& a, const PgSeq& s) {
+__device__ __forceinline__ bool pg_is_pair(const PgArgs& a, const PgSeq& s, int u) {
+  return s.n - u * 2 * a.TQ > a.TQ;
+}
+
+// Cost of a sequence's units for one key/value head.
+template <typename Cfg>
+__device__ __forceinline__ int pg_seq_cost(const PgArgs& a, const PgSeq& s) {
   int w = 0;
   for (int u = 0; u < s.units; ++u) {
     const PgKeys k = pg_unit_keys(a, s, u);
-    w += k.t1 - k.t0;
+    w += (k.t1 - k.t0) * (pg_is_pair(a, s, u) ? Cfg::kPairCost : Cfg::kSplitCost);
   }
   return w;
 }
 
-// This CTA's slice [t0, t1) of the key tiles and the unit it starts in, whose first key tile
-// has index start.
+// This CTA's slice [t0, t1) of the work and the unit that t0 falls into, which starts at `start`.
 struct PgPlan {
   int t0, t1, b, kvh, u, start;
 };
 
 // One warp.  With `write` it also stores the prefixes for the merge kernel and checks the
 // lengths and offsets.
+template <typename Cfg>
 __device__ __forceinline__ void pg_plan(const PgArgs& a, int lane, PgPlan* out, bool write) {
   constexpr unsigned kFull = 0xffffffffu;
   int total = 0;
+  PgSeq s{0, 0, 0, 0};
+  int w = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
-    const int v = b < a.B ? pg_seq_tiles(a, pg_seq(a, b)) * a.H_kv : 0;
-    total += static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(v)));
+    s = PgSeq{0, 0, 0, 0};
+    if (b < a.B) s = pg_seq(a, b);
+    w = pg_seq_cost<Cfg>(a, s);
+    total += static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(w * a.H_kv)));
   }
   const int grid = static_cast<int>(gridDim.x);
-  const int per = total > 0 ? (total + grid - 1) / grid : 1;
+  // at least a tile's cost, so that no CTA inside a unit's span is left without one of its tiles
+  const int per = max((total + grid - 1) / grid, Cfg::kPairCost);
   const int t0 = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(blockIdx.x) * per));
-  const int t1 = min(total, t0 + per);
+  const int t1 = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(t0) + per));
   bool found = t0 >= t1;
-  if (found && lane == 0) *out = PgPlan{t0, t0, 0, 0, 0, 0};
+  if (found && lane == 0) *out = PgPlan{t0, t0, 0, 0, 0, t0};
   int acc = 0, uacc = 0;
   for (int b0 = 0; b0 < a.B && (!found || write); b0 += 32) {
     const int b = b0 + lane;
-    PgSeq s{0, 0, 0, 0};
-    if (b < a.B) {
-      s = pg_seq(a, b);
-      if (write && !pg_seq_ok(a, b)) plan_fail(a.status, 43);
+    if (a.B > 32) {  // up to 32 sequences are still at hand
+      s = PgSeq{0, 0, 0, 0};
+      if (b < a.B) s = pg_seq(a, b);
+      w = pg_seq_cost<Cfg>(a, s);
     }
-    const int w = b < a.B ? pg_seq_tiles(a, s) : 0;
+    if (write && b < a.B && !pg_seq_ok(a, b)) plan_fail(a.status, 43);
     int incl = w * a.H_kv, uincl = s.units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -214,8 +250,9 @@ __device__ __forceinline__ void pg_plan(const PgArgs& a, int lane, PgPlan* out, 
       int start = excl + kvh * w, u = 0;
       while (true) {
         const PgKeys k = pg_unit_keys(a, s, u);
-        if (t0 < start + k.t1 - k.t0) break;
-        start += k.t1 - k.t0;
+        const int c = (k.t1 - k.t0) * (pg_is_pair(a, s, u) ? Cfg::kPairCost : Cfg::kSplitCost);
+        if (t0 < start + c) break;
+        start += c;
         ++u;
       }
       *out = PgPlan{t0, t1, b, kvh, u, start};
@@ -232,7 +269,12 @@ __device__ __forceinline__ void pg_plan(const PgArgs& a, int lane, PgPlan* out, 
   }
 }
 
-// A run of nt key tiles from tile kt0 of one unit.
+// Key tiles [lo, hi).
+struct PgRange {
+  int lo, hi;
+};
+
+// A run of nt key tiles from tile kt0 of one unit; nt = 0 ends a CTA's list.
 struct PgSeg {
   int b, kvh;
   int q0;        // the unit's first token
@@ -241,69 +283,69 @@ struct PgSeg {
   int len;
   PgKeys keys;   // what the unit sees
   int kt0, nt;
-  bool pair;     // two tiles
-  bool whole;    // the run is the whole unit
-  bool first;    // the CTA's first segment
+  int pair;      // two tiles
+  int whole;     // the run is the whole unit
+  int slot;      // of a partial result: 0 when the unit started in an earlier CTA, else 1
+  PgRange tile[2];  // pair: the key tiles of the run that each tile visits
 };
 
-// Walks this CTA's slice segment by segment; every role walks it the same way.
+// Walks this CTA's slice segment by segment (the schedule's warp, every lane alike).
+template <typename Cfg>
 struct PgWalk {
-  int t, t1, b, kvh, u, start;
-  bool fresh;
+  int t0, t1, b, kvh, u, start;
   PgSeq s;
   __device__ __forceinline__ PgWalk(const PgArgs& a, const PgPlan& p)
-      : t(p.t0), t1(p.t1), b(p.b), kvh(p.kvh), u(p.u), start(p.start), fresh(true), s(pg_seq(a, p.b)) {}
+      : t0(p.t0), t1(p.t1), b(p.b), kvh(p.kvh), u(p.u), start(p.start), s(pg_seq(a, p.b)) {}
   __device__ __forceinline__ bool next(const PgArgs& a, PgSeg& g) {
-    if (t >= t1) return false;
-    PgKeys k{0, 0, 0, 0};
-    while (true) {
-      if (u < s.units) {
-        k = pg_unit_keys(a, s, u);
-        if (t < start + k.t1 - k.t0) break;
-        start += k.t1 - k.t0;
-        ++u;
-      } else {
+    while (start < t1) {
+      if (u >= s.units) {
         u = 0;
         if (s.units == 0 || ++kvh >= a.H_kv) {
           kvh = 0;
           if (++b >= a.B) return false;
           s = pg_seq(a, b);
         }
+        continue;
       }
+      const PgKeys k = pg_unit_keys(a, s, u);
+      const bool pair = pg_is_pair(a, s, u);
+      const int cost = pair ? Cfg::kPairCost : Cfg::kSplitCost;
+      const int T = k.t1 - k.t0;
+      // the tiles that start in [t0, t1)
+      const int first = t0 > start ? (t0 - start + cost - 1) / cost : 0;
+      const int last = min(T, (t1 - start + cost - 1) / cost);
+      const int tok0 = u * 2 * a.TQ;
+      start += T * cost;
+      ++u;
+      if (first >= last) continue;
+      g.b = b;
+      g.kvh = kvh;
+      g.q0 = s.q0 + tok0;
+      g.pos0 = s.len - s.n + tok0;
+      g.ntok = min(2 * a.TQ, s.n - tok0);
+      g.len = s.len;
+      g.keys = k;
+      g.kt0 = k.t0 + first;
+      g.nt = last - first;
+      g.pair = pair;
+      g.whole = first == 0 && last == T;
+      g.slot = first == 0;
+      for (int i = 0; i < 2; ++i) {
+        const int tok = i * a.TQ;
+        const int n = min(a.TQ, g.ntok - tok);
+        PgRange r{0, 0};
+        if (n > 0) {
+          const PgKeys kt = pg_keys(a, g.len, g.pos0 + tok, g.pos0 + tok + n - 1);
+          r = PgRange{max(kt.t0, g.kt0), min(kt.t1, g.kt0 + g.nt)};
+          if (r.hi < r.lo) r.hi = r.lo;
+        }
+        g.tile[i] = r;
+      }
+      return true;
     }
-    const int end = start + k.t1 - k.t0;
-    const int stop = min(end, t1);
-    const int tok0 = u * 2 * a.TQ;
-    g.b = b;
-    g.kvh = kvh;
-    g.q0 = s.q0 + tok0;
-    g.pos0 = s.len - s.n + tok0;
-    g.ntok = min(2 * a.TQ, s.n - tok0);
-    g.len = s.len;
-    g.keys = k;
-    g.kt0 = k.t0 + (t - start);
-    g.nt = stop - t;
-    g.pair = g.ntok > a.TQ;
-    g.whole = t == start && stop == end;
-    g.first = fresh;
-    fresh = false;
-    t = stop;
-    return true;
+    return false;
   }
 };
-
-// Key tiles [lo, hi) of the segment that tile i of a pair visits.
-struct PgRange {
-  int lo, hi;
-};
-__device__ __forceinline__ PgRange pg_range(const PgArgs& a, const PgSeg& g, int i) {
-  const int tok = i * a.TQ;
-  const int n = min(a.TQ, g.ntok - tok);
-  const PgKeys k = pg_keys(a, g.len, g.pos0 + tok, g.pos0 + tok + n - 1);
-  PgRange r{max(k.t0, g.kt0), min(k.t1, g.kt0 + g.nt)};
-  if (r.hi < r.lo) r.hi = r.lo;
-  return r;
-}
 
 // The key tiles of a segment in the order the MMA warp consumes them.  pair: K_j, V_j; split:
 // K_0, K_1, V_0, K_2, V_1, ..  f(is_value, tile) returns false to stop.
@@ -321,14 +363,14 @@ __device__ __forceinline__ bool pg_loads(const PgSeg& g, F f) {
 }
 
 // ---------------------------------------------------------------- e4m3 pages
-// The pieces of every query row: piece i of (token, head) at pieces[((i T + token) H + head) D],
+// The two pieces of every query row: piece i of (token, head) at pieces[((i T + token) H + head) D],
 // factors q_scale[token H + head].  L = D / 16 lanes per row.
 template <int D, Elem E>
 __global__ void __launch_bounds__(256) fa_paged_split_kernel(const void* q, int64_t token_stride, int64_t head_stride,
                                                              uint8_t* pieces, float* q_scale, int T, int H,
                                                              int* status) {
   constexpr int L = D / 16;
-  constexpr int kPieces = PgCfg<D, E, true, 0>::kQParts;
+  constexpr int kPieces = 2;
   const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / L;
   const int item = threadIdx.x % L;
   const bool live = row < static_cast<int64_t>(T) * H;
@@ -396,11 +438,10 @@ __device__ __forceinline__ void split_e5m2(uint32_t a, uint32_t b, uint32_t& p0,
 }
 
 // Weights of one score row of NC keys, 2^(s * c - m), times the value factors vs[] (shared
-// memory), as e5m2 pieces, four keys per word; l gets the fp32 sum of the weights.
+// memory), as e5m2 pieces p[piece], four keys per word; l gets the fp32 sum of the weights.
 template <int NC>
-__device__ __forceinline__ void softmax_row_f8(const uint32_t (&s)[NC], const float* vs, uint32_t (&p0)[NC / 4],
-                                               uint32_t (&p1)[NC / 4], uint32_t (&p2)[NC / 4], float c, float m,
-                                               float& l) {
+__device__ __forceinline__ void softmax_row_f8(const uint32_t (&s)[NC], const float* vs,
+                                               uint32_t (&p)[kPPieces][NC / 4], float c, float m, float& l) {
   const float2 c2 = make_float2(c, c), nm2 = make_float2(-m, -m);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -413,17 +454,43 @@ __device__ __forceinline__ void softmax_row_f8(const uint32_t (&s)[NC], const fl
     sum[0] = fadd2(sum[0], e0);
     sum[1] = fadd2(sum[1], e1);
     const float2 w0 = fmul2(e0, make_float2(f.x, f.y)), w1 = fmul2(e1, make_float2(f.z, f.w));
-    split_e5m2(pack_f16x2(w0.x, w0.y), pack_f16x2(w1.x, w1.y), p0[i], p1[i], p2[i]);
+    split_e5m2(pack_f16x2(w0.x, w0.y), pack_f16x2(w1.x, w1.y), p[0][i], p[1][i], p[2][i]);
   }
   l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
-// Scale factors of one key tile: of the scores, and of the weights relative to 2^e.
+// The factor 2^(byte - 127 - e) of a value's scale byte as fp32 and as fp16 bits; NaN for 255.
+__device__ __forceinline__ float pg_factor(int byte, int e) {
+  const int d = byte - 127 - e;  // <= 0 unless NaN; far below the largest is zero
+  return byte == 255 ? __uint_as_float(0x7fc00000u) : (d < -126 ? 0.f : __int_as_float((127 + d) << 23));
+}
+__device__ __forceinline__ uint32_t pg_factor16(int byte, int e) {
+  const int d = byte - 127 - e;
+  return byte == 255 ? 0x7e00u : (d >= -14 ? static_cast<uint32_t>(15 + d) << 10 : (d >= -24 ? 1u << (24 + d) : 0u));
+}
+
+// Sixteen codes times an fp16 factor (twice in f), in order.
+__device__ __forceinline__ void pg_convert16(const uint4& c, uint32_t f, uint32_t (&o)[8]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 x, y;\n\tmov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 x, lo;\n\tcvt.rn.f16x2.e4m3x2 y, hi;\n\t"
+        "mul.rn.f16x2 %0, x, %3;\n\tmul.rn.f16x2 %1, y, %3;\n\t}"
+        : "=r"(o[2 * i]), "=r"(o[2 * i + 1])
+        : "r"(w[i]), "r"(f));
+}
+
+// Scale factors of one key tile: of the scores, and of the weights (or, for V's conversion, fp16
+// factors of the rows) relative to 2^e.
 struct PgScales {
   float ks[128];
   float vs[128];
   int e;
   int pad[3];
+};
+struct PgVScales {
+  uint32_t f[128];
 };
 
 // ---------------------------------------------------------------- the kernel
@@ -432,15 +499,27 @@ struct __align__(1024) PgSmem {
   using Cfg = PgCfg<D, E, Q8, R>;
   uint8_t q[2][Cfg::kQBytes];
   uint8_t kv[Cfg::kStages][Cfg::kTileBytes];
-  uint8_t stage[Cfg::kStageBytes];
-  PgScales scales[2][Q8 ? Cfg::kScaleRing : 1];  // of each softmax group's tiles
-  float3 stat[2 * Cfg::kCopies][Cfg::kRows];     // m, l, lr of a split segment's copies
+  uint8_t v16[Cfg::kV16][Cfg::kConv ? Cfg::kV16Bytes : 16];
+  uint8_t vraw[Cfg::kVRaw][Cfg::kConv ? Cfg::kTileBytes : 16];
+  alignas(16) float stage[2][Cfg::kStageRows * Cfg::kStageCols];  // a split segment's columns being joined
+  PgScales scales[2][Q8 ? Cfg::kScaleRing : 1];       // of each softmax group's tiles
+  PgVScales vscales[Cfg::kConv ? Cfg::kScaleRing : 1];
+  float3 stat[2 * Cfg::kCopies][Cfg::kRows];          // m, l, lr of a split segment's copies
+  PgSeg segs[Cfg::kSegRing];
   uint64_t q_full[2];
   uint64_t q_empty[2];
   uint64_t kv_full[Cfg::kStages];
   uint64_t kv_empty[Cfg::kStages];
+  uint64_t vraw_full[Cfg::kVRaw];
+  uint64_t vraw_empty[Cfg::kVRaw];
+  uint64_t v16_full[Cfg::kV16];
+  uint64_t v16_empty[Cfg::kV16];
   uint64_t sc_full[2][Cfg::kScaleRing];
   uint64_t sc_empty[2][Cfg::kScaleRing];
+  uint64_t vsc_full[Cfg::kScaleRing];
+  uint64_t vsc_empty[Cfg::kScaleRing];
+  uint64_t seg_full[Cfg::kSegRing];
+  uint64_t seg_empty[Cfg::kSegRing];
   uint64_t s_full[2];
   uint64_t p_full[2];
   uint64_t o_done[2];
@@ -467,7 +546,8 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
                     const __grid_constant__ CUtensorMap tm_v, const PgArgs a) {
   using Cfg = PgCfg<D, E, Q8, R>;
   constexpr int NS = Cfg::kStages;
-  constexpr int NC8 = Cfg::kScaleRing;
+  constexpr int NSC = Cfg::kScaleRing;
+  constexpr int NSEG = Cfg::kSegRing;
   constexpr unsigned kFull = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
   PgSmem<D, E, Q8, R>& sm = *reinterpret_cast<PgSmem<D, E, Q8, R>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -490,16 +570,35 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
       mbar_init(&sm.kv_full[s], 1);
       mbar_init(&sm.kv_empty[s], 1);
     }
-    for (int i = 0; i < 2; ++i)
-      for (int s = 0; s < NC8; ++s) {
-        mbar_init(&sm.sc_full[i][s], 1);
-        mbar_init(&sm.sc_empty[i][s], 4);
+    if constexpr (Q8) {
+      for (int s = 0; s < NSC; ++s) {
+        for (int i = 0; i < 2; ++i) {
+          mbar_init(&sm.sc_full[i][s], 1);
+          mbar_init(&sm.sc_empty[i][s], 4);
+        }
+        mbar_init(&sm.vsc_full[s], 1);
+        mbar_init(&sm.vsc_empty[s], 4);
       }
+    }
+    if constexpr (Cfg::kConv) {
+      for (int s = 0; s < Cfg::kVRaw; ++s) {
+        mbar_init(&sm.vraw_full[s], 1);
+        mbar_init(&sm.vraw_empty[s], 4);
+      }
+      for (int s = 0; s < Cfg::kV16; ++s) {
+        mbar_init(&sm.v16_full[s], 4);
+        mbar_init(&sm.v16_empty[s], 1);
+      }
+    }
+    for (int s = 0; s < NSEG; ++s) {
+      mbar_init(&sm.seg_full[s], 1);
+      mbar_init(&sm.seg_empty[s], Cfg::kSegReaders);
+    }
     mbar_init(&sm.groups, 8);
     mbar_init(&sm.mma_drain, 1);
     fence_mbar_init();
   }
-  // rows past G * TQ of a query tile are never loaded
+  // rows of a query tile that hold no query are never loaded
   for (uint32_t i = threadIdx.x; i < 2u * Cfg::kQBytes / 16; i += Cfg::kThreads)
     reinterpret_cast<uint4*>(sm.q[0])[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
@@ -513,35 +612,54 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
-    pg_plan(a, lane, &sm.plan, blockIdx.x == 0);
+    pg_plan<Cfg>(a, lane, &sm.plan, blockIdx.x == 0);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
-  const PgPlan plan = sm.plan;
+
+  // Readers of the segment ring: the next segment, or null at the end or after an abort; a
+  // reader gives the one it holds back first.
+  uint32_t nseg = 0;
+  auto next_seg = [&](const WaitCtx& wc) -> const PgSeg* {
+    if (nseg > 0) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.seg_empty[(nseg - 1) % NSEG]);
+    }
+    const int i = nseg % NSEG;
+    if (!__all_sync(kFull, mbar_wait(&sm.seg_full[i], (nseg / NSEG) & 1, wc))) return nullptr;
+    ++nseg;
+    return sm.segs[i].nt > 0 ? &sm.segs[i] : nullptr;
+  };
 
   // Each warpgroup's setmaxnreg sits at the top of the branch holding all of its code.
-  if (warp >= 8) {
-    if constexpr (Cfg::kGeneral) regs_set<kPagedLaunchRegs, Cfg::kRegsOther>();
+  if (warp >= 8 && warp < 12) {
+    if constexpr (Cfg::kGeneral) regs_set<Cfg::kLaunch, Cfg::kRegsOther>();
     if (warp == 8) {
-      // ---------------------------------------------------------- TMA producer (whole warp)
+      // ---------------------------------------------------------- schedule and TMA loads
       const WaitCtx wc{&sm.abort_flag, status, 31};
-      PgWalk w(a, plan);
+      PgWalk<Cfg> w(a, sm.plan);
       PgSeg g;
-      uint32_t it = 0, qcnt[2] = {0, 0}, nseg = 0;
+      uint32_t it = 0, itv = 0, qcnt[2] = {0, 0};
       bool ok = true;
       auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, wc)); };
-      auto load_q = [&](int slot, int tok, int copies) -> bool {
+      auto load_q = [&](int slot, int tok) -> bool {
         if (!wait_all(&sm.q_empty[slot], (qcnt[slot] & 1) ^ 1)) return false;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&sm.q_full[slot],
-                                static_cast<uint32_t>(copies * Cfg::kQParts * Cfg::kRowBytes * G * a.TQ));
-          for (int cp = 0; cp < copies; ++cp)
-            for (int c = 0; c < Cfg::kQParts; ++c)
-              if (FA_IN_BOUNDS(tok >= 0 && tok < a.T && g.kvh < a.H_kv && G * a.TQ <= Cfg::kRows, status, 501))
-                tma_load_4d(sm.q[slot] + c * Cfg::kQPartBytes + cp * Cfg::kRows * Cfg::kRowBytes, &tm_q,
-                            &sm.q_full[slot], Q8 ? 0 : c * 64, 0, g.kvh, Q8 ? c * a.T + tok : tok);
+        // a box per copy and chunk or piece; with four lanes a row, the pieces go to the row
+        // blocks of a copy in turn
+        constexpr int kBoxes = Cfg::kCopies * (Cfg::kSlots > 1 ? Cfg::kSlots : Cfg::kQParts);
+        if (lane == 0)
+          mbar_arrive_expect_tx(&sm.q_full[slot], static_cast<uint32_t>(kBoxes * Cfg::kRowBytes * G * a.TQ));
+        __syncwarp();
+        if (lane < kBoxes) {
+          const int cp = lane % Cfg::kCopies, x = lane / Cfg::kCopies;
+          const int part = Cfg::kSlots > 1 ? 0 : x;
+          const int row = (cp * Cfg::kSlots + (Cfg::kSlots > 1 ? x : 0)) * Cfg::kRows;
+          const int piece = Cfg::kSlots > 1 ? x & 1 : x;
+          if (FA_IN_BOUNDS(tok >= 0 && tok < a.T && g.kvh < a.H_kv && G * a.TQ <= Cfg::kRows, status, 501))
+            tma_load_4d(sm.q[slot] + part * Cfg::kQPartBytes + row * Cfg::kRowBytes, &tm_q, &sm.q_full[slot],
+                        Q8 ? 0 : part * 64, 0, g.kvh, Q8 ? piece * a.T + tok : tok);
         }
         __syncwarp();
         ++qcnt[slot];
@@ -554,20 +672,27 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
         const long long i = static_cast<long long>(win) * 32 + lane;
         return i < a.max_pages ? __ldg(a.table + static_cast<long long>(g.b) * a.max_pages + i) : -1;
       };
-      while (ok && w.next(a, g)) {
-        if (Cfg::kGeneral && g.pair) {
-          for (int i = 0; i < 2 && ok; ++i) {
-            const PgRange r = pg_range(a, g, i);
-            if (r.hi > r.lo) ok = load_q(i, g.q0 + i * a.TQ, 1);
-          }
-        } else {
-          ok = load_q(Cfg::kGeneral ? 0 : (nseg & 1), g.q0, Cfg::kCopies);
+      while (ok) {
+        const int i = nseg % NSEG;
+        const bool more = w.next(a, g);
+        if (more) ahead = entry(((g.kt0 << 7) >> a.page_shift) >> 5);
+        ok = wait_all(&sm.seg_empty[i], ((nseg / NSEG) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
+          if (!more) g.nt = 0;
+          sm.segs[i] = g;
+          mbar_arrive(&sm.seg_full[i]);
         }
         ++nseg;
+        if (!more) break;
+        if (Cfg::kGeneral && g.pair) {
+          for (int x = 0; x < 2 && ok; ++x)
+            if (g.tile[x].hi > g.tile[x].lo) ok = load_q(x, g.q0 + x * a.TQ);
+        } else {
+          ok = load_q(Cfg::kGeneral ? 0 : ((nseg - 1) & 1), g.q0);
+        }
         if (!ok) break;
-        window_at = ((g.kt0 << 7) >> a.page_shift) >> 5;
-        ahead = entry(window_at);
-        --window_at;
+        window_at = (((g.kt0 << 7) >> a.page_shift) >> 5) - 1;
         ok = pg_loads(g, [&](bool isv, int j) -> bool {
           const int p0 = (j << 7) >> a.page_shift;  // the tile's first page
           if ((p0 >> 5) > window_at) {              // keys run at most two tiles ahead of values
@@ -578,11 +703,14 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
           // the boxes that hold a key of the unit
           const int k0 = max(g.keys.lo - (j << 7), 0) / box;
           const int k1 = (min(g.keys.hi - (j << 7), 128) + box - 1) / box;
-          const int slot = it % NS;
-          if (!wait_all(&sm.kv_empty[slot], ((it / NS) & 1) ^ 1)) return false;
+          const bool raw = Cfg::kConv && isv;
+          const int n = raw ? Cfg::kVRaw : NS;
+          uint32_t& cnt = raw ? itv : it;
+          const int slot = cnt % n;
+          uint64_t* full = raw ? &sm.vraw_full[slot] : &sm.kv_full[slot];
+          if (!wait_all(raw ? &sm.vraw_empty[slot] : &sm.kv_empty[slot], ((cnt / n) & 1) ^ 1)) return false;
           if (lane == 0)
-            mbar_arrive_expect_tx(&sm.kv_full[slot],
-                                  static_cast<uint32_t>((k1 - k0) * box * Cfg::kRowBytes * Cfg::kChunks));
+            mbar_arrive_expect_tx(full, static_cast<uint32_t>((k1 - k0) * box * Cfg::kRowBytes * Cfg::kChunks));
           __syncwarp();
           const int k = k0 + lane / Cfg::kChunks, c = lane % Cfg::kChunks;
           const int held = (p0 >> 5) & 1 ? id_odd : id_even;
@@ -591,13 +719,14 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
             const int row = (j << 7) & (a.page - 1) & ~(box - 1);  // inside a page of 256
             const bool good = id >= 0 && id < a.P;
             if (!good) plan_fail(status, 44);
+            uint8_t* dst = raw ? sm.vraw[slot] : sm.kv[slot];
             // a bad page number reads as zeros: a coordinate past the pool
             if (FA_IN_BOUNDS(row + box <= a.page && p0 + k < a.max_pages && k * box < 128, status, 502))
-              tma_load_3d(sm.kv[slot] + c * Cfg::kChunkBytes + k * box * Cfg::kRowBytes, isv ? &tm_v : &tm_k,
-                          &sm.kv_full[slot], c * 64, row, good ? id * a.H_kv + g.kvh : a.P * a.H_kv);
+              tma_load_3d(dst + c * Cfg::kChunkBytes + k * box * Cfg::kRowBytes, isv ? &tm_v : &tm_k, full, c * 64, row,
+                          good ? id * a.H_kv + g.kvh : a.P * a.H_kv);
           }
           __syncwarp();
-          ++it;
+          ++cnt;
           return true;
         });
       }
@@ -605,6 +734,9 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
         // Unwinding: wait (bounded) for the copies still in flight before the CTA exits.
         for (uint32_t idx = (it > static_cast<uint32_t>(NS) ? it - NS : 0); idx < it; ++idx)
           mbar_wait_drain(&sm.kv_full[idx % NS], (idx / NS) & 1, status);
+        constexpr uint32_t NV = Cfg::kVRaw;
+        for (uint32_t idx = (itv > NV ? itv - NV : 0); idx < itv; ++idx)
+          mbar_wait_drain(&sm.vraw_full[idx % NV], (idx / NV) & 1, status);
         for (int i = 0; i < 2; ++i)
           if (qcnt[i] > 0) mbar_wait_drain(&sm.q_full[i], (qcnt[i] - 1) & 1, status);
       }
@@ -615,15 +747,18 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
       // Q, K K-major; P in TMEM, V MN-major
       constexpr uint32_t idesc_s =
           Q8 ? idesc_kind_f8(Cfg::kM, kBN, 0, 0, 0) : idesc_kind_f16(Cfg::kM, kBN, 0, 0, ElemOps<E>::kMmaType);
-      constexpr uint32_t idesc_o =
-          Q8 ? idesc_kind_f8(Cfg::kM, D, 0, 1, 1) : idesc_kind_f16(Cfg::kM, D, 0, 1, ElemOps<E>::kMmaType);
+      constexpr bool kPieces = Q8 && !Cfg::kConv;  // P as e5m2 pieces, V as codes
+      constexpr uint32_t idesc_o = kPieces ? idesc_kind_f8(Cfg::kM, D, 0, 1, 1)
+                                           : idesc_kind_f16(Cfg::kM, D, 0, 1, Cfg::kConv ? 0 : ElemOps<E>::kMmaType);
       constexpr uint32_t kGroup = 8 * Cfg::kRowBytes;  // 8-row groups
       auto desc = [](const void* p, uint32_t lbo, uint32_t sbo) {
         return Cfg::kRowBytes == 64 ? sdesc_sw64(smem_u32(p), lbo, sbo) : sdesc_sw128(smem_u32(p), lbo, sbo);
       };
       const uint64_t dq[2] = {desc(sm.q[0], 16, kGroup), desc(sm.q[1], 16, kGroup)};
       const uint64_t dk0 = desc(sm.kv[0], 16, kGroup);
-      const uint64_t dv0 = desc(sm.kv[0], Cfg::kChunkBytes, kGroup);
+      const uint64_t dv0 = Cfg::kConv ? sdesc_sw128(smem_u32(sm.v16[0]), 128 * 128, 1024)
+                                      : desc(sm.kv[0], Cfg::kChunkBytes, kGroup);
+      constexpr int kVBytes = Cfg::kConv ? Cfg::kV16Bytes : Cfg::kTileBytes;
       auto issue_s = [&](int i, int qs, int slot) {
         const uint64_t dk = dk0 + static_cast<uint64_t>((slot * Cfg::kTileBytes) >> 4);
         const uint64_t dqi = qs ? dq[1] : dq[0];
@@ -642,11 +777,11 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
         }
       };
       auto issue_pv = [&](int i, int slot, uint32_t acc) {
-        const uint64_t dv = dv0 + static_cast<uint64_t>((slot * Cfg::kTileBytes) >> 4);
+        const uint64_t dv = dv0 + static_cast<uint64_t>((slot * kVBytes) >> 4);
         const uint32_t tO = tbase + Cfg::kOCol + i * D, tP = tbase + i * 128;
-        if constexpr (Q8) {
+        if constexpr (kPieces) {
 #pragma unroll
-          for (int p = 0; p < kPPieces; ++p)
+          for (int p = 0; p < (Cfg::kSlots > 1 ? 1 : kPPieces); ++p)
 #pragma unroll
             for (int kk = 0; kk < kBN / 32; ++kk)
               umma_ts_f8_w(tO, tP + p * 32 + kk * 8, dv + ((kk * 32 * Cfg::kRowBytes) >> 4), idesc_o,
@@ -658,54 +793,66 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
         }
       };
       auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, wc)); };
-      PgWalk w(a, plan);
-      PgSeg g;
-      uint32_t it = 0, qcnt[2] = {0, 0}, pcnt[2] = {0, 0}, nseg = 0;
+      uint32_t it = 0, itv = 0, qcnt[2] = {0, 0}, pcnt[2] = {0, 0};
       bool ok = true;
       int slot = 0;
-      auto take = [&]() -> bool {
+      auto take_k = [&]() -> bool {
         slot = it % NS;
         const bool r = wait_all(&sm.kv_full[slot], (it / NS) & 1);
         ++it;
         return r;
       };
-      // value rows of tile j that the unit does not see are zeroed: zero weights times stale
-      // infinities would not be zero
-      auto clean = [&](int sv, int j) {
-        const int z0 = max(g.keys.lo - (j << 7), 0), z1 = min(g.keys.hi - (j << 7), 128);
-        if (z0 > 0 || z1 < 128) {
-          pg_zero_rows<Cfg::kRowBytes, Cfg::kChunks>(sm.kv[sv], 0, z0, lane);
-          pg_zero_rows<Cfg::kRowBytes, Cfg::kChunks>(sm.kv[sv], z1, 128, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
+      auto take_v = [&]() -> bool {
+        if constexpr (!Cfg::kConv) return take_k();
+        slot = itv % Cfg::kV16;
+        const bool r = wait_all(&sm.v16_full[slot], (itv / Cfg::kV16) & 1);
+        ++itv;
+        return r;
       };
-      while (ok && w.next(a, g)) {
+      auto free_v = [&](int sv) { umma_commit_w(Cfg::kConv ? &sm.v16_empty[sv] : &sm.kv_empty[sv]); };
+      while (ok) {
+        const PgSeg* gp = next_seg(wc);
+        if (gp == nullptr) break;
+        const PgSeg& g = *gp;
+        const int kt0 = g.kt0, nt = g.nt;
+        // value rows of tile j that the unit does not see are zeroed: zero weights times stale
+        // infinities would not be zero (the conversion does it for its fp16 tiles)
+        auto clean = [&](int sv, int j) {
+          if constexpr (!Cfg::kConv) {
+            const int z0 = max(g.keys.lo - (j << 7), 0), z1 = min(g.keys.hi - (j << 7), 128);
+            if (z0 > 0 || z1 < 128) {
+              pg_zero_rows<Cfg::kRowBytes, Cfg::kChunks>(sm.kv[sv], 0, z0, lane);
+              pg_zero_rows<Cfg::kRowBytes, Cfg::kChunks>(sm.kv[sv], z1, 128, lane);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
+        };
         if (Cfg::kGeneral && g.pair) {
-          const PgRange rg[2] = {pg_range(a, g, 0), pg_range(a, g, 1)};
-          const int jlo = g.kt0, jhi = g.kt0 + g.nt;
+          const PgRange rg[2] = {g.tile[0], g.tile[1]};
+          const int jhi = kt0 + nt;
           auto in = [&](int i, int j) { return j >= rg[i].lo && j < rg[i].hi; };
           for (int i = 0; i < 2 && ok; ++i)
             if (rg[i].hi > rg[i].lo) ok = wait_all(&sm.q_full[i], qcnt[i] & 1);
           if (!ok) break;
-          ok = take();
+          ok = take_k();
           if (!ok) break;
           tc_fence_after();
           for (int i = 0; i < 2; ++i) {
-            if (!in(i, jlo)) continue;
+            if (!in(i, kt0)) continue;
             issue_s(i, i, slot);
             umma_commit_w(&sm.s_full[i]);
-            if (rg[i].hi == jlo + 1) umma_commit_w(&sm.q_empty[i]);
+            if (rg[i].hi == kt0 + 1) umma_commit_w(&sm.q_empty[i]);
           }
           umma_commit_w(&sm.kv_empty[slot]);
-          for (int j = jlo; j < jhi && ok; ++j) {
-            ok = take();
+          for (int j = kt0; j < jhi && ok; ++j) {
+            ok = take_v();
             if (!ok) break;
             const int sv = slot;
             clean(sv, j);
             int skn = -1;
             if (j + 1 < jhi) {
-              ok = take();
+              ok = take_k();
               if (!ok) break;
               skn = slot;
             }
@@ -725,127 +872,216 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
               }
             }
             if (!ok) break;
-            umma_commit_w(&sm.kv_empty[sv]);
+            free_v(sv);
             if (skn >= 0) umma_commit_w(&sm.kv_empty[skn]);
           }
           for (int i = 0; i < 2; ++i)
             if (rg[i].hi > rg[i].lo) ++qcnt[i];
         } else {
-          const int qs = Cfg::kGeneral ? 0 : (nseg & 1);
+          const int qs = Cfg::kGeneral ? 0 : ((nseg - 1) & 1);
           ok = wait_all(&sm.q_full[qs], qcnt[qs] & 1);
           if (!ok) break;
           ++qcnt[qs];
           tc_fence_after();
-          for (int t = 0; t < 2 && t < g.nt && ok; ++t) {
-            ok = take();
+          for (int t = 0; t < 2 && t < nt && ok; ++t) {
+            ok = take_k();
             if (!ok) break;
             tc_fence_after();
             issue_s(t, qs, slot);
             umma_commit_w(&sm.s_full[t]);
             umma_commit_w(&sm.kv_empty[slot]);
-            if (t == g.nt - 1) umma_commit_w(&sm.q_empty[qs]);
+            if (t == nt - 1) umma_commit_w(&sm.q_empty[qs]);
           }
-          for (int t = 0; t < g.nt && ok; ++t) {
+          for (int t = 0; t < nt && ok; ++t) {
             const int i = t & 1;
-            ok = take();  // V_t
+            ok = take_v();
             if (!ok) break;
-            clean(slot, g.kt0 + t);
+            clean(slot, kt0 + t);
             ok = wait_all(&sm.p_full[i], (i ? pcnt[1] : pcnt[0]) & 1);
             if (!ok) break;
             if (i) ++pcnt[1]; else ++pcnt[0];
             tc_fence_after();
             issue_pv(i, slot, t >= 2);
-            umma_commit_w(&sm.kv_empty[slot]);
-            if (t + 2 >= g.nt) umma_commit_w(&sm.o_done[i]);
-            if (t + 2 < g.nt) {
-              ok = take();  // K_{t+2}
+            free_v(slot);
+            if (t + 2 >= nt) umma_commit_w(&sm.o_done[i]);
+            if (t + 2 < nt) {
+              ok = take_k();
               if (!ok) break;
               tc_fence_after();
               issue_s(i, qs, slot);
               umma_commit_w(&sm.s_full[i]);
               umma_commit_w(&sm.kv_empty[slot]);
-              if (t + 2 == g.nt - 1) umma_commit_w(&sm.q_empty[qs]);
+              if (t + 2 == nt - 1) umma_commit_w(&sm.q_empty[qs]);
             }
           }
         }
-        ++nseg;
       }
       // Wait for every MMA issued to finish before the columns are freed.
       umma_commit_w(&sm.mma_drain);
       mbar_wait_drain(&sm.mma_drain, 0, status);
       __syncwarp();
     } else if constexpr (Q8) {
-      // ---------------------------------------------------------- scales of group `grp`'s tiles
-      const int grp = warp - 10;
+      // ---------------------------------------------------------- scales
+      // Split segments, and pieces: warp 10 + g serves group g.  With V's conversion warp 10
+      // serves both groups and warp 11 the conversion, and both follow every tile, so that they
+      // agree on the exponent.
       const WaitCtx wc{&sm.abort_flag, status, 35};
-      PgWalk w(a, plan);
-      PgSeg g;
-      uint32_t it = 0;
+      const int me = warp - 10;
+      uint32_t cnt[2] = {0, 0};
       bool ok = true;
-      // the scale bytes of the lane's four keys of tile j; 1 for keys the unit does not see
-      auto fetch = [&](int j, uint32_t& kw, uint32_t& vw) {
-        kw = vw = 0x7f7f7f7fu;
-        const int key = (j << 7) + lane * 4;
-        if (key + 3 < g.keys.lo || key >= g.keys.hi) return;
-        const int pg = key >> a.page_shift;
-        const int id = pg < a.max_pages ? __ldg(a.table + static_cast<int64_t>(g.b) * a.max_pages + pg) : -1;
-        if (id < 0 || id >= a.P) return;
-        const int64_t at = (static_cast<int64_t>(id) * a.H_kv + g.kvh) * a.page + (key & (a.page - 1));
-        if (!FA_IN_BOUNDS(at >= 0 && at + 4 <= static_cast<int64_t>(a.P) * a.H_kv * a.page, status, 511)) return;
-        kw = __ldg(reinterpret_cast<const uint32_t*>(a.k_scales + at));
-        vw = __ldg(reinterpret_cast<const uint32_t*>(a.v_scales + at));
-      };
-      while (ok && w.next(a, g)) {
-        int j0 = g.kt0 + grp, j1 = g.kt0 + g.nt, dj = 2;
-        if (Cfg::kGeneral && g.pair) {
-          const PgRange r = pg_range(a, g, grp);
-          j0 = r.lo;
-          j1 = r.hi;
-          dj = 1;
-        }
+      while (ok) {
+        const PgSeg* gp = next_seg(wc);
+        if (gp == nullptr) break;
+        const PgSeg& g = *gp;
+        // the scale bytes of the lane's four keys of tile j; 2^0 for keys the unit does not see
+        auto fetch = [&](int j, uint32_t& kw, uint32_t& vw) {
+          kw = vw = 0x7f7f7f7fu;
+          const int key = (j << 7) + lane * 4;
+          if (key + 3 < g.keys.lo || key >= g.keys.hi) return;
+          const int pg = key >> a.page_shift;
+          const int id = pg < a.max_pages ? __ldg(a.table + static_cast<int64_t>(g.b) * a.max_pages + pg) : -1;
+          if (id < 0 || id >= a.P) return;
+          const int64_t at = (static_cast<int64_t>(id) * a.H_kv + g.kvh) * a.page + (key & (a.page - 1));
+          if (!FA_IN_BOUNDS(at >= 0 && at + 4 <= static_cast<int64_t>(a.P) * a.H_kv * a.page, status, 511)) return;
+          if (!Cfg::kConv || me == 0) kw = __ldg(reinterpret_cast<const uint32_t*>(a.k_scales + at));
+          vw = __ldg(reinterpret_cast<const uint32_t*>(a.v_scales + at));
+        };
+        const int jend = g.kt0 + g.nt;
+        const int dj = Cfg::kConv ? 1 : 2;
         int e = -1000;
         uint32_t kw = 0, vw = 0, kn = 0, vn = 0;
-        if (j0 < j1) fetch(j0, kw, vw);
-        for (int j = j0; j < j1; j += dj) {
-          if (j + dj < j1) fetch(j + dj, kn, vn);  // in flight over this tile
-          const int slot = it % NC8;
-          ok = __all_sync(kFull, mbar_wait(&sm.sc_empty[grp][slot], ((it / NC8) & 1) ^ 1, wc));
-          if (!ok) break;
-          ++it;
-          PgScales& sc = sm.scales[grp][slot];
+        int j = g.kt0 + (Cfg::kConv ? 0 : me);
+        if (j < jend) fetch(j, kw, vw);
+        for (; j < jend && ok; j += dj) {
+          if (j + dj < jend) fetch(j + dj, kn, vn);  // in flight over this tile
           const int key = (j << 7) + lane * 4;
-          int ev[4], top = -1000;
+          int top = -1000;
           bool in[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int b = (vw >> (8 * x)) & 255;
             in[x] = key + x >= g.keys.lo && key + x < g.keys.hi;
-            ev[x] = b - 127;
-            if (in[x] && b != 255) top = max(top, ev[x]);
+            if (in[x] && b != 255) top = max(top, b - 127);
           }
           e = max(e, __reduce_max_sync(kFull, top));
           if (e == -1000) e = 0;  // every scale NaN
-          float k4[4], v4[4];
+          if (Cfg::kConv && me == 1) {
+            const int slot = cnt[0] % NSC;
+            ok = __all_sync(kFull, mbar_wait(&sm.vsc_empty[slot], ((cnt[0] / NSC) & 1) ^ 1, wc));
+            if (!ok) break;
+            ++cnt[0];
+            uint32_t f[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            k4[x] = in[x] ? e8m0_to_float((kw >> (8 * x)) & 255) : 0.f;
-            const int d = ev[x] - e;  // <= 0; far below the largest is zero
-            v4[x] = !in[x] ? 0.f : (ev[x] == 128 ? __uint_as_float(0x7fc00000u)
-                                                 : (d < -126 ? 0.f : __int_as_float((127 + d) << 23)));
+            for (int x = 0; x < 4; ++x) f[x] = pg_factor16((vw >> (8 * x)) & 255, e) * 0x10001u;
+            *reinterpret_cast<uint4*>(sm.vscales[slot].f + lane * 4) = make_uint4(f[0], f[1], f[2], f[3]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.vsc_full[slot]);
+          } else {
+            float k4[4], v4[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              k4[x] = in[x] ? e8m0_to_float((kw >> (8 * x)) & 255) : 0.f;
+              v4[x] = in[x] ? pg_factor((vw >> (8 * x)) & 255, e) : 0.f;
+            }
+#pragma unroll
+            for (int grp = 0; grp < 2; ++grp) {
+              const bool mine = !Cfg::kConv ? grp == me
+                                            : (g.pair ? j >= g.tile[grp].lo && j < g.tile[grp].hi
+                                                      : ((j - g.kt0) & 1) == grp);
+              if (!mine) continue;
+              const int slot = cnt[grp] % NSC;
+              ok = __all_sync(kFull, mbar_wait(&sm.sc_empty[grp][slot], ((cnt[grp] / NSC) & 1) ^ 1, wc));
+              if (!ok) break;
+              ++cnt[grp];
+              PgScales& sc = sm.scales[grp][slot];
+              *reinterpret_cast<float4*>(sc.ks + lane * 4) = make_float4(k4[0], k4[1], k4[2], k4[3]);
+              if constexpr (!Cfg::kConv)
+                *reinterpret_cast<float4*>(sc.vs + lane * 4) = make_float4(v4[0], v4[1], v4[2], v4[3]);
+              if (lane == 0) sc.e = e;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.sc_full[grp][slot]);
+            }
           }
-          *reinterpret_cast<float4*>(sc.ks + lane * 4) = make_float4(k4[0], k4[1], k4[2], k4[3]);
-          *reinterpret_cast<float4*>(sc.vs + lane * 4) = make_float4(v4[0], v4[1], v4[2], v4[3]);
-          if (lane == 0) sc.e = e;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.sc_full[grp][slot]);
           kw = kn;
           vw = vn;
         }
       }
     }
+  } else if (Cfg::kConv && warp >= 12) {
+    // ------------------------------------------------------------ V's codes to fp16 tiles
+    if constexpr (Cfg::kConv) {
+      regs_set<Cfg::kLaunch, Cfg::kRegsOther>();
+      const WaitCtx wc{&sm.abort_flag, status, 36};
+      constexpr int L = D / 16;          // threads per row
+      constexpr int kStep = 128 / L;     // rows per pass
+      constexpr int U = 4;
+      const int tid = threadIdx.x - 384;
+      const int item = tid % L, r0 = tid / L;
+      // codes lie in the swizzle of their row; the thread's two 16-byte units of the fp16 row are
+      // 2 (item % 4) and the next of chunk item / 4, the upper chunk's threads storing the odd one
+      // first, so that a row's threads cover all banks.  Rows a multiple of 8 apart share both
+      // swizzles.
+      static_assert(kStep % 8 == 0, "one swizzle for all of a thread's rows");
+      const int in_unit = D == 128 ? item ^ (r0 & 7) : item ^ ((r0 >> 1) & 3);
+      const int odd = (item >> 2) & 1;
+      const int first = ((item & 3) * 2 + odd) ^ (r0 & 7), second = ((item & 3) * 2 + 1 - odd) ^ (r0 & 7);
+      uint32_t it = 0;
+      bool ok = true;
+      while (ok) {
+        const PgSeg* gp = next_seg(wc);
+        if (gp == nullptr) break;
+        const PgSeg& g = *gp;
+        const int jend = g.kt0 + g.nt;
+        for (int j = g.kt0; j < jend; ++j) {
+          const int rs = it % Cfg::kVRaw, vs = it % Cfg::kV16, ss = it % NSC;
+          ok = __all_sync(kFull, mbar_wait(&sm.vsc_full[ss], (it / NSC) & 1, wc)) &&
+               __all_sync(kFull, mbar_wait(&sm.vraw_full[rs], (it / Cfg::kVRaw) & 1, wc)) &&
+               __all_sync(kFull, mbar_wait(&sm.v16_empty[vs], ((it / Cfg::kV16) & 1) ^ 1, wc));
+          if (!ok) break;
+          ++it;
+          const int z0 = max(g.keys.lo - (j << 7), 0), z1 = min(g.keys.hi - (j << 7), 128);
+          uint8_t* dst = sm.v16[vs] + (item >> 2) * 128 * 128;
+#pragma unroll 1
+          for (int base = r0; base < 128; base += U * kStep) {
+            uint4 c[U];
+            uint32_t f[U], o[U][8];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              c[u] = *reinterpret_cast<const uint4*>(sm.vraw[rs] + (base + u * kStep) * D + in_unit * 16);
+              f[u] = sm.vscales[ss].f[base + u * kStep];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) pg_convert16(c[u], f[u], o[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              uint8_t* p = dst + (base + u * kStep) * 128;
+              const uint4 lo = make_uint4(o[u][0], o[u][1], o[u][2], o[u][3]);
+              const uint4 hi = make_uint4(o[u][4], o[u][5], o[u][6], o[u][7]);
+              *reinterpret_cast<uint4*>(p + (first << 4)) = odd ? hi : lo;
+              *reinterpret_cast<uint4*>(p + (second << 4)) = odd ? lo : hi;
+            }
+          }
+          if (z0 > 0 || z1 < 128) {
+            for (int row = r0; row < 128; row += kStep)
+              if (row < z0 || row >= z1) {
+                *reinterpret_cast<uint4*>(dst + row * 128 + (first << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(dst + row * 128 + (second << 4)) = make_uint4(0u, 0u, 0u, 0u);
+              }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sm.v16_full[vs]);
+            mbar_arrive(&sm.vraw_empty[rs]);
+            mbar_arrive(&sm.vsc_empty[ss]);
+          }
+        }
+      }
+    }
   } else {
     // ------------------------------------------------------------ softmax groups
-    if constexpr (Cfg::kGeneral) regs_set<kPagedLaunchRegs, Cfg::kRegsSoftmax>();
+    if constexpr (Cfg::kGeneral) regs_set<Cfg::kLaunch, Cfg::kRegsSoftmax>();
+    constexpr bool kPieces = Q8 && !Cfg::kConv;
     constexpr int NC = 128 / Cfg::kCopies;         // keys of a tile this warp handles
     constexpr int kQuarter = Cfg::kM / 4;          // accumulator rows per 32-lane quarter
     constexpr int kWarpsPerCopy = 4 / Cfg::kCopies;
@@ -854,54 +1090,54 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
     const int cp = wq / kWarpsPerCopy;
     const int col0 = cp * NC;
     // row within the copy; with M = 64, lanes 16-31 of a quarter hold no rows
-    const int rc = lane < kQuarter ? (wq % kWarpsPerCopy) * kQuarter + lane : 1 << 20;
-    const int wrow0 = (wq % kWarpsPerCopy) * kQuarter;  // the warp's first row
+    const int wrow0 = Cfg::kSlots > 1 ? 0 : (wq % kWarpsPerCopy) * kQuarter;  // the warp's first row
+    const int rc = Cfg::kSlots > 1 ? lane % Cfg::kRows : (lane < kQuarter ? wrow0 + lane : 1 << 20);
+    const bool writer = Cfg::kSlots == 1 || lane < Cfg::kRows;  // of a row's lanes
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tbase + grp * 128 + lane_off;
     const uint32_t tO = tbase + Cfg::kOCol + grp * D + lane_off;
     const WaitCtx wc{&sm.abort_flag, status, 33 + grp};
-    PgWalk w(a, plan);
-    PgSeg g;
     uint32_t scnt = 0, ocnt = 0, gcnt = 0;  // scnt also counts the group's scale entries
     bool ok = true;
-    while (ok && w.next(a, g)) {
+    while (ok) {
+      const PgSeg* gp = next_seg(wc);
+      if (gp == nullptr) break;
+      const PgSeg& g = *gp;
       // this group's tile and its key tiles j0, j0 + dj, .. below j1
       const bool pair = Cfg::kGeneral && g.pair;
       const int tok = pair ? grp * a.TQ : 0;
-      const int ntok = min(a.TQ, g.ntok - tok);
-      const int M = G * ntok;
-      int j0 = g.kt0 + grp, j1 = g.kt0 + g.nt, dj = 2;
-      if (pair) {
-        const PgRange r = pg_range(a, g, grp);
-        j0 = r.lo;
-        j1 = r.hi;
-        dj = 1;
-      }
+      const int M = G * min(a.TQ, g.ntok - tok);
+      const int j0 = pair ? g.tile[grp].lo : g.kt0 + grp;
+      const int j1 = pair ? g.tile[grp].hi : g.kt0 + g.nt;
+      const int dj = pair ? 1 : 2;
       const bool any = j0 < j1;
-      const int iq = rc < M ? rc / G : 0;
-      const int qpos = g.pos0 + tok + iq;
-      const int vis_hi = rc < M ? (a.causal ? min(qpos, g.len - 1) : g.len - 1) : -1;
-      const int vis_lo = a.window >= 0 ? qpos - a.window : 0;
-      // every row of the tile sees the keys from all_lo to all_hi
-      const int all_hi = a.causal ? g.pos0 + tok : g.len - 1;
-      const int all_lo = a.window >= 0 ? g.pos0 + tok + ntok - 1 - a.window : 0;
       const bool rows_here = wrow0 < M;  // a warp without rows only keeps the barriers
-      float m_ref = -INFINITY, l = 0.f, lr = 0.f;
+      int vis_hi, vis_lo, all_hi, all_lo;
       // log2 units per score; with e4m3 pages the row's query factor, and the exponent of O
       float c_row = a.scale_log2;
       int e_ref = 0;
-      if constexpr (Q8) {
-        if (rc < M && FA_IN_BOUNDS(g.q0 + tok + iq < a.T, status, 512))
-          c_row *= __ldg(a.q_scale + (static_cast<int64_t>(g.q0) + tok + iq) * a.H + g.kvh * G + rc - iq * G);
-      }
-      for (int j = j0; j < j1; j += dj) {
-        ok = __all_sync(kFull, mbar_wait(&sm.s_full[grp], scnt & 1, wc));
-        if (!ok) break;
-        const int sslot = scnt % NC8;
+      {
+        const int iq = rc < M ? rc / G : 0;
+        const int qpos = g.pos0 + tok + iq;
+        vis_hi = rc < M ? (a.causal ? min(qpos, g.len - 1) : g.len - 1) : -1;
+        vis_lo = a.window >= 0 ? qpos - a.window : 0;
+        // every row of the tile sees the keys from all_lo to all_hi
+        all_hi = a.causal ? g.pos0 + tok : g.len - 1;
+        all_lo = a.window >= 0 ? g.pos0 + tok + M / G - 1 - a.window : 0;
         if constexpr (Q8) {
-          ok = __all_sync(kFull, mbar_wait(&sm.sc_full[grp][sslot], (scnt / NC8) & 1, wc));
+          if (rc < M && FA_IN_BOUNDS(g.q0 + tok + iq < a.T, status, 512))
+            c_row *= __ldg(a.q_scale + (static_cast<int64_t>(g.q0) + tok + iq) * a.H + g.kvh * G + rc - iq * G);
+        }
+      }
+      float m_ref = -INFINITY, l = 0.f, lr = 0.f;
+      for (int j = j0; j < j1; j += dj) {
+        const int ss = scnt % NSC;
+        if constexpr (Q8) {
+          ok = __all_sync(kFull, mbar_wait(&sm.sc_full[grp][ss], (scnt / NSC) & 1, wc));
           if (!ok) break;
         }
+        ok = __all_sync(kFull, mbar_wait(&sm.s_full[grp], scnt & 1, wc));
+        if (!ok) break;
         ++scnt;
         tc_fence_after();
         if (rows_here) {
@@ -910,8 +1146,15 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < NC; c += 32) tmem_ld32(tS + col0 + c, s + c);
           tmem_wait_ld();
+          if constexpr (Cfg::kSlots > 1) {
+            // the scores of the pieces q1 and q2 lie 8 lanes apart
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              s[c] = __float_as_uint(__uint_as_float(s[c]) +
+                                     __uint_as_float(__shfl_xor_sync(kFull, s[c], Cfg::kRows)));
+          }
           if constexpr (Q8) {
-            const float4* ks = reinterpret_cast<const float4*>(sm.scales[grp][sslot].ks + col0);
+            const float4* ks = reinterpret_cast<const float4*>(sm.scales[grp][ss].ks + col0);
 #pragma unroll
             for (int c = 0; c < NC / 4; ++c) {
               const float4 f = ks[c];
@@ -945,17 +1188,17 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
           const bool raise = m_new > m_ref + kTau;
           bool grown = false;  // the value exponent grew: O is held in units of 2^e_ref
           float alpha = raise ? ex2_approx(m_ref - m_new) : 1.0f;
-          if constexpr (Q8) {
-            const int e = sm.scales[grp][sslot].e;
-            grown = j > j0 && e > e_ref;
-            if (raise) l *= alpha;
-            if (grown) alpha = e - e_ref > 126 ? 0.f : alpha * __int_as_float((127 + e_ref - e) << 23);
-            e_ref = e;
-          } else if (raise) {
+          if (raise) {
             l *= alpha;
             lr *= alpha;
+            m_ref = m_new;
           }
-          if (raise) m_ref = m_new;
+          if constexpr (Q8) {
+            const int e = sm.scales[grp][ss].e;
+            grown = j > j0 && e > e_ref;
+            if (grown) alpha = e - e_ref > 126 ? 0.f : alpha * __int_as_float((127 + e_ref - e) << 23);
+            e_ref = e;
+          }
           if (__any_sync(kFull, raise) || grown) {
             if (j > j0) {
               // the commit that signalled this S covers the group's previous P.V
@@ -976,23 +1219,29 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
           uint32_t zero[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) zero[x] = 0u;
-          if constexpr (Q8) {
-            uint32_t p0[NC / 4], p1[NC / 4], p2[NC / 4];
-            softmax_row_f8<NC>(s, sm.scales[grp][sslot].vs + col0, p0, p1, p2, c_row, m_use - kPShift, l);
+          if constexpr (kPieces) {
+            uint32_t p[kPPieces][NC / 4];
+            softmax_row_f8<NC>(s, sm.scales[grp][ss].vs + col0, p, c_row, m_use - kPShift, l);
+            if constexpr (Cfg::kSlots > 1) {
+              // each of a row's lanes stores one piece, the fourth zeros
+              const int slot = lane / Cfg::kRows;
 #pragma unroll
-            for (int x = 0; x < NC / 4; x += 8) {
-              tmem_st8(tS + col0 / 4 + x, p0 + x);
-              tmem_st8(tS + 32 + col0 / 4 + x, p1 + x);
-              tmem_st8(tS + 64 + col0 / 4 + x, p2 + x);
+              for (int x = 0; x < NC / 4; ++x)
+                p[0][x] = slot == 0 ? p[0][x] : (slot == 1 ? p[1][x] : (slot == 2 ? p[2][x] : 0u));
             }
+            constexpr int n = Cfg::kSlots > 1 ? 1 : kPPieces;
+#pragma unroll
+            for (int y = 0; y < n; ++y)
+#pragma unroll
+              for (int x = 0; x < NC / 4; x += 8) tmem_st8(tS + y * 32 + col0 / 4 + x, p[y] + x);
             if constexpr (Cfg::kCopies > 1) {
 #pragma unroll
-              for (int c = 0; c < 96; c += 8)
+              for (int c = 0; c < n * 32; c += 8)
                 if ((c & 31) < col0 / 4 || (c & 31) >= col0 / 4 + NC / 4) tmem_st8(tS + c, zero);
             }
           } else {
             uint32_t p[NC / 2];
-            softmax_row<E, NC>(s, p, a.scale_log2, m_use, l, lr);
+            softmax_row<Cfg::kConv ? Elem::kF16 : E, NC>(s, p, c_row, m_use, l, lr);
 #pragma unroll
             for (int x = 0; x < NC / 2; x += 16) tmem_st16(tS + col0 / 2 + x, p + x);
             if constexpr (Cfg::kCopies > 1) {
@@ -1003,10 +1252,6 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
           }
           tmem_wait_st();
         }
-        if constexpr (Q8) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.sc_empty[grp][sslot]);
-        }
         tc_fence_before();
         if constexpr (Cfg::kPArrive == 4) {
           __syncwarp();
@@ -1014,14 +1259,18 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
         } else {
           mbar_arrive(&sm.p_full[grp]);
         }
+        if constexpr (Q8) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.sc_empty[grp][ss]);
+        }
       }
       if (!ok) break;
       float unit = 1.0f;  // of O
-      if constexpr (Q8) {
-        // weights carry 2^7, and fp32 sums normalise them
+      if constexpr (Q8) unit = e8m0_to_float(static_cast<uint32_t>(e_ref + 127));
+      if constexpr (kPieces) {
+        // the pieces' weights carry 2^7, and fp32 sums normalise them
         m_ref -= kPShift;
         lr = l;
-        unit = e8m0_to_float(static_cast<uint32_t>(e_ref + 127));
       }
       if (any) {
         ok = __all_sync(kFull, mbar_wait(&sm.o_done[grp], ocnt & 1, wc));
@@ -1029,15 +1278,14 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
         ++ocnt;
         tc_fence_after();
       }
-      const bool real = rc < M;
+      const bool real = rc < M && writer;
       // a segment that is not a whole unit leaves a partial result
-      const int64_t part0 = ((static_cast<int64_t>(blockIdx.x) * 2 + (g.first ? 0 : 1)) * Cfg::kSubs +
-                             (pair ? grp : 0)) * Cfg::kRows;
-      const int64_t token0 = static_cast<int64_t>(g.q0) + tok;
+      const int64_t part0 =
+          ((static_cast<int64_t>(blockIdx.x) * 2 + g.slot) * Cfg::kSubs + (pair ? grp : 0)) * Cfg::kRows;
       auto put = [&](int row, int c, const auto& v) {  // columns c .. of a row of the tile
         constexpr int n = sizeof(v) / sizeof(float);
         const int i = row / G;
-        const int64_t token = token0 + i;
+        const int64_t token = static_cast<int64_t>(g.q0) + tok + i;
         const int h = g.kvh * G + row - i * G;
         if (g.whole) {
           if (FA_IN_BOUNDS(token >= 0 && token < a.T && h < a.H && c + n <= D, status, 503)) {
@@ -1070,7 +1318,8 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
       auto put_lse = [&](float m, float ls, float lrs) {
         const float lse_l = ls == 0.f ? -INFINITY : (m + lg2_approx(ls)) * kLn2;
         const float lse_r = lrs == 0.f ? -INFINITY : (m + lg2_approx(lrs)) * kLn2;
-        const int64_t token = token0 + iq;
+        const int iq = rc / G;
+        const int64_t token = static_cast<int64_t>(g.q0) + tok + iq;
         const int h = g.kvh * G + rc - iq * G;
         if (g.whole) {
           if (FA_IN_BOUNDS(token >= 0 && token < a.T && h < a.H, status, 505))
@@ -1099,7 +1348,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
         }
       } else {
         // Join the copies: weights 2^(m_k - max m) / sum of lr, the rows summed through shared
-        // memory 32 columns at a time
+        // memory a few columns at a time in two buffers, so that one barrier per step suffices
         auto sync_groups = [&]() -> bool {
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.groups);
@@ -1107,12 +1356,15 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
           ++gcnt;
           return r;
         };
+        constexpr int SC = Cfg::kStageCols;
+        constexpr int kUnits = SC / 4;  // 16-byte units of a staged row; unit u sits at u ^ key(row)
+        auto key = [](int r) { return (kUnits == 8 ? r : r >> 1) & (kUnits - 1); };
         const int me = grp * Cfg::kCopies + cp;
         if (real) sm.stat[me][rc] = make_float3(m_ref, l, lr);
         ok = sync_groups();
         if (!ok) break;
         float mm = -INFINITY, ls = 0.f, lrs = 0.f, wgt = 0.f;
-        if (real) {
+        if (rc < M) {
 #pragma unroll
           for (int k = 0; k < 2 * Cfg::kCopies; ++k) mm = fmaxf(mm, sm.stat[k][rc].x);
           const float ref = mm == -INFINITY ? 0.f : mm;
@@ -1124,24 +1376,31 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
             lrs += e * st.z;
           }
           wgt = (lr == 0.f || lrs == 0.f) ? 0.f : ex2_approx(m_ref - ref) * unit / lrs;
-          if (me == 0) put_lse(ref, ls, lrs);
+          if (me == 0 && writer) put_lse(ref, ls, lrs);
         }
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o[16];
-          float v[16];
+        for (int c = 0; c < D; c += SC) {
+          float* stage = sm.stage[(c / SC) & 1];
+          const int srow = Cfg::kGeneral ? rc : me * Cfg::kRows + rc;
+          uint32_t o[SC];
+          float v[SC];
           if (any && rows_here) {
-            tmem_ld16(tO + c, o);
+#pragma unroll
+            for (int x = 0; x < SC; x += 16) tmem_ld16(tO + c + x, o + x);
             tmem_wait_ld();
           }
 #pragma unroll
-          for (int x = 0; x < 16; ++x) v[x] = lr == 0.f ? 0.f : __uint_as_float(o[x]) * wgt;
-          // 16-byte unit u of staged row r sits at u ^ (r / 2 mod 4): two rows fill the banks
-          const int srow = Cfg::kGeneral ? rc : me * Cfg::kRows + rc;
+          for (int x = 0; x < SC; ++x) {
+            v[x] = lr == 0.f ? 0.f : __uint_as_float(o[x]) * wgt;
+            if constexpr (Cfg::kSlots > 1) {  // the products of a row's pieces
+              v[x] += __shfl_xor_sync(kFull, v[x], 8);
+              v[x] += __shfl_xor_sync(kFull, v[x], 16);
+            }
+          }
           if (real && (!Cfg::kGeneral || grp == 1)) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              *reinterpret_cast<float4*>(sm.stage + srow * 64 + ((x ^ ((srow >> 1) & 3)) << 4)) =
+            for (int x = 0; x < kUnits; ++x)
+              *reinterpret_cast<float4*>(stage + srow * SC + ((x ^ key(srow)) << 2)) =
                   make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
           }
           ok = sync_groups();
@@ -1149,8 +1408,8 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
           if constexpr (Cfg::kGeneral) {
             if (grp == 0 && real) {
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const float4 y = *reinterpret_cast<const float4*>(sm.stage + rc * 64 + ((x ^ ((rc >> 1) & 3)) << 4));
+              for (int x = 0; x < kUnits; ++x) {
+                const float4 y = *reinterpret_cast<const float4*>(stage + rc * SC + ((x ^ key(rc)) << 2));
                 v[4 * x] += y.x;
                 v[4 * x + 1] += y.y;
                 v[4 * x + 2] += y.z;
@@ -1160,22 +1419,20 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
             }
           } else {
             // two columns of a row per thread
-            const int row = threadIdx.x >> 3, col = (threadIdx.x & 7) * 2;  // warps 0-7
-            if (row < M) {
+            const int col = (threadIdx.x % (SC / 2)) * 2;  // warps 0-7
+            for (int row = threadIdx.x / (SC / 2); row < M; row += 256 / (SC / 2)) {
               float sum[2] = {0.f, 0.f};
 #pragma unroll
               for (int k = 0; k < 2 * Cfg::kCopies; ++k) {
                 const int sr = k * Cfg::kRows + row;
-                const float2 y = *reinterpret_cast<const float2*>(
-                    sm.stage + sr * 64 + (((col >> 2) ^ ((sr >> 1) & 3)) << 4) + (col & 3) * 4);
+                const float2 y =
+                    *reinterpret_cast<const float2*>(stage + sr * SC + (((col >> 2) ^ key(sr)) << 2) + (col & 3));
                 sum[0] += y.x;
                 sum[1] += y.y;
               }
               put(row, c + col, sum);
             }
           }
-          ok = sync_groups();
-          if (!ok) break;
         }
         if (!ok) break;
       }
@@ -1196,10 +1453,10 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8, R>::kThreads, 1)
 // exp(lr_s), the convex combination one CTA would have formed.  Units that one CTA computed
 // were written by it; rows of units without keys get O = 0, LSE = -inf.  Block (unit,
 // key/value head, part) of four warps; W warps share a row's partial results.
-template <int D, Elem E, int R, int W>
+template <int D, Elem E, bool Q8, int R, int W>
 __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PgArgs a) {
   using T = typename ElemOps<E>::T;
-  using Cfg = PgCfg<D, E, false, R>;
+  using Cfg = PgCfg<D, E, Q8, R>;
   constexpr unsigned kFull = 0xffffffffu;
   constexpr int V = D / 32;  // columns per lane
   __shared__ float acc_sh[W > 1 ? W : 1][D];
@@ -1216,19 +1473,19 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PgArgs a) {
   const int ntok = min(2 * a.TQ, s.n - tok0);
   const PgKeys k = pg_unit_keys(a, s, u);
   const int T_u = k.t1 - k.t0;
-  const int* steps = a.meta + 2 + a.B + 1;
-  int start = steps[b] + kvh * ((steps[b + 1] - steps[b]) / a.H_kv);
-  int before = 0;
+  const int* costs = a.meta + 2 + a.B + 1;
+  int start = costs[b] + kvh * ((costs[b + 1] - costs[b]) / a.H_kv);
+  int before = 0;  // the sequence's units before this one are pairs
   for (int x = lane; x < u; x += 32) {
     const PgKeys kx = pg_unit_keys(a, s, x);
-    before += kx.t1 - kx.t0;
+    before += (kx.t1 - kx.t0) * Cfg::kPairCost;
   }
   start += static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(before)));
   const int per = a.meta[1];
   const int cf = start / per;
-  const int cl = T_u > 0 ? (start + T_u - 1) / per : cf;
+  const int cost = pg_is_pair(a, s, u) ? Cfg::kPairCost : Cfg::kSplitCost;
+  const int cl = T_u > 0 ? (start + (T_u - 1) * cost) / per : cf;
   if (T_u > 0 && cf == cl) return;  // written by its CTA
-  const bool cf_first = start == cf * per;
   const int parts = T_u > 0 ? cl - cf + 1 : 0;
   const int rows = G * ntok;
   for (int row = blockIdx.z * (4 / W) + warp / W; row < rows; row += gridDim.z * (4 / W)) {
@@ -1238,7 +1495,7 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PgArgs a) {
     const int64_t token = static_cast<int64_t>(s.q0) + tok0 + iq;
     // index of partial result i of this row
     auto at = [&](int i) -> int64_t {
-      const int slot = 2 * (cf + i) + ((i == 0 && !cf_first) ? 1 : 0);
+      const int slot = 2 * (cf + i) + (i == 0);
       return (static_cast<int64_t>(slot) * Cfg::kSubs + tile) * Cfg::kRows + rc;
     };
     float mx_l = -INFINITY, mx_r = -INFINITY, s_l = 0.f, s_r = 0.f;

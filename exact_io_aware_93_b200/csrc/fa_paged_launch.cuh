@@ -5,6 +5,8 @@
 #include "fa_paged_launch.h"
 #include "tma_host.h"
 
+#include <type_traits>
+
 namespace fa {
 
 template <int D, Elem E, bool Q8, int R>
@@ -14,8 +16,8 @@ fa_status launch_paged(DeviceInfo& di, const PagedCall& c) {
   auto kern = fa_paged_kernel<D, E, Q8, R>;
   const int smem = static_cast<int>(sizeof(PgSmem<D, E, Q8, R>)) + 1024;
   static_assert(sizeof(PgSmem<D, E, Q8, R>) + 1024 <= 232448, "shared memory of one CTA");
-  if (!once_per_device(di.paged_attr[E == Elem::kF16][Q8][D == 128][R / 2], [&] {
-        return (!Cfg::kGeneral || launch_regs_ok(kern, kPagedLaunchRegs)) &&
+  if (!once_per_device(di.paged_attr[E == Elem::kF16][Q8][D == 128][R == 8 ? 3 : R / 2], [&] {
+        return (!Cfg::kGeneral || launch_regs_ok(kern, Cfg::kLaunch)) &&
                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
       }))
     return FA_ERR_LAUNCH;
@@ -30,7 +32,7 @@ fa_status launch_paged(DeviceInfo& di, const PagedCall& c) {
   uint8_t* w = static_cast<uint8_t*>(c.workspace);
   CUtensorMap mq, mk, mv;
   // e4m3 pages: the query pieces, one batch of tokens after the other
-  if (!(Q8 ? make_ragged_q_map(&mq, w + L.pieces, Cfg::kQParts * static_cast<long long>(p.T), p.H_kv, G, D,
+  if (!(Q8 ? make_ragged_q_map(&mq, w + L.pieces, 2ll * p.T, p.H_kv, G, D,
                                static_cast<long long>(p.H) * D, D, TQ, MapElem::kE4M3)
            : make_ragged_q_map(&mq, c.q, p.T, p.H_kv, G, D, p.q_stride[0], p.q_stride[1], TQ, me)) ||
       !make_pages_map(&mk, c.k_pages, planes, p.page, D, box, pe) ||
@@ -76,20 +78,26 @@ fa_status launch_paged(DeviceInfo& di, const PagedCall& c) {
   const unsigned units = static_cast<unsigned>(paged_units(p));
   const int rows = G * (p.max_q < 2 * TQ ? p.max_q : 2 * TQ);
   if constexpr (Cfg::kGeneral)
-    fa_paged_merge_kernel<D, E, R, 1><<<dim3(units, p.H_kv, (rows + 31) / 32), 128, 0, c.stream>>>(a);
+    fa_paged_merge_kernel<D, E, Q8, R, 1><<<dim3(units, p.H_kv, (rows + 31) / 32), 128, 0, c.stream>>>(a);
   else
-    fa_paged_merge_kernel<D, E, R, 4><<<dim3(units, p.H_kv, rows), 128, 0, c.stream>>>(a);
+    fa_paged_merge_kernel<D, E, Q8, R, 4><<<dim3(units, p.H_kv, rows), 128, 0, c.stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 template <Elem E, bool Q8>
 fa_status paged_call(DeviceInfo& di, const PagedCall& c) {
-  const int R = paged_copies(c.p);
-  if (c.p.d == 128)
-    return R == 4 ? launch_paged<128, E, Q8, 4>(di, c)
-                  : (R == 2 ? launch_paged<128, E, Q8, 2>(di, c) : launch_paged<128, E, Q8, 0>(di, c));
-  return R == 4 ? launch_paged<64, E, Q8, 4>(di, c)
-                : (R == 2 ? launch_paged<64, E, Q8, 2>(di, c) : launch_paged<64, E, Q8, 0>(di, c));
+  const auto go = [&](auto d) -> fa_status {
+    constexpr int D = decltype(d)::value;
+    switch (paged_copies(c.p)) {
+      case 8:
+        if constexpr (Q8) return launch_paged<D, E, Q8, 8>(di, c);
+        return FA_ERR_LAUNCH;
+      case 4: return launch_paged<D, E, Q8, 4>(di, c);
+      case 2: return launch_paged<D, E, Q8, 2>(di, c);
+      default: return launch_paged<D, E, Q8, 0>(di, c);
+    }
+  };
+  return c.p.d == 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 64>{});
 }
 
 }  // namespace fa

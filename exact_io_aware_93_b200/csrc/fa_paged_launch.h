@@ -25,10 +25,12 @@ struct PagedCall {
   cudaStream_t stream;
 };
 
-// Rows one key/value head contributes at most and the copies of them a tile holds: 4 up to 16
-// rows, 2 up to 32, otherwise 0 for tiles of 128 rows.
+// The kernel's variant (PgCfg's R) by the rows that one key/value head contributes at most: 4
+// copies of up to 16 rows in a tile, 2 of up to 32, otherwise 0 for tiles of 128 rows; with e4m3
+// pages 8 for 4 copies of up to 8 rows of four lanes each.
 inline int paged_copies(const fa_paged_problem& p) {
   const long long rows = static_cast<long long>(p.H / p.H_kv) * p.max_q;
+  if (p.quant && rows <= 8) return 8;
   return rows <= 16 ? 4 : (rows <= 32 ? 2 : 0);
 }
 inline int paged_tile_tokens(const fa_paged_problem& p) {
@@ -44,8 +46,8 @@ inline long long paged_units(const fa_paged_problem& p) {
 
 // Workspace regions: the plan (total, tiles per CTA, unit and key-tile prefixes), then the
 // partial log-sums [rows, 2] and the partial outputs [rows, d]; a CTA leaves at most two
-// partial segments of 256 rows (16 or 32 where a tile holds copies).  With e4m3 pages also the
-// query pieces (2 or 3 bytes per element) and a factor per query row.
+// partial segments of 256 rows (8, 16 or 32 where a tile holds copies).  With e4m3 pages also the
+// query pieces (2 bytes per element) and a factor per query row.
 struct PagedLayout {
   size_t meta, part_lse, part_o, pieces, q_scale, total;
   long long slots;
@@ -53,7 +55,7 @@ struct PagedLayout {
 inline PagedLayout paged_layout(const fa_paged_problem& p, int grid) {
   const auto round256 = [](size_t x) { return (x + 255) / 256 * 256; };
   const int R = paged_copies(p);
-  const size_t rows = 2 * static_cast<size_t>(grid) * (R ? 64 / R : 256);
+  const size_t rows = 2 * static_cast<size_t>(grid) * (R == 0 ? 256 : (R == 8 ? 8 : 64 / R));
   PagedLayout L;
   L.slots = 2ll * grid;
   L.meta = 0;
@@ -61,7 +63,7 @@ inline PagedLayout paged_layout(const fa_paged_problem& p, int grid) {
   L.part_o = L.part_lse + round256(rows * 2 * 4);
   L.pieces = L.part_o + round256(rows * static_cast<size_t>(p.d) * 4);
   const size_t q_rows = p.quant ? static_cast<size_t>(p.T) * p.H : 0;
-  L.q_scale = L.pieces + round256(q_rows * p.d * (p.dtype == FA_DTYPE_F16 ? 3 : 2));
+  L.q_scale = L.pieces + round256(q_rows * p.d * 2);
   L.total = L.q_scale + q_rows * 4;
   return L;
 }

@@ -419,7 +419,8 @@ typedef struct fa_paged_problem {
 
 /*
  * Bytes of device workspace fa_paged needs on the CURRENT device: the plan, and two partial
- * results per SM of 256 rows (32 or 16 when (H / H_kv) * max_q is no more) of 4 * d + 8 bytes.
+ * results per SM of 256 rows (32, 16 or 8 when (H / H_kv) * max_q is no more) of 4 * d + 8
+ * bytes; with e4m3 pages also 2 * d + 4 bytes per query row.
  * 0 for an invalid or unsupported problem or without an sm_100 device.
  */
 size_t fa_paged_workspace_size(const fa_paged_problem* problem);
@@ -482,7 +483,7 @@ fa_status fa_get_status(void* stream);
  * FA_ERR_TIMEOUT the wait that ran out (forward: 1 loads, 2 MMA, 3 and 4 the softmax of the
  * first and second query block; backward: 11 loads, 12 MMA, 13 key rows, 14 dQ drain;
  * decode: 21 loads, 22 MMA, 23 softmax; paged attention: 31 loads, 32 MMA, 33 and 34 the softmax
- * groups, 35 the conversion of e4m3 pages; 98 the final wait for issued MMAs or a wait while
+ * groups, 35 the scales and 36 the conversion of e4m3 pages; 98 the final wait for issued MMAs or a wait while
  * unwinding after an abort; 99 the self-test),
  * for FA_ERR_PLAN the reader (41 fa_cache_append, 42 fa_cache_gather, 43 and 44 fa_paged: its
  * offsets and lengths, its page numbers),

@@ -12,7 +12,10 @@ e4m3 pages, both types: a weight is the sum of three e5m2 pieces of its fp16 val
 bits, u = 2^-9 relative, and loses what lies under 2^-16 / 2^7 = 2^-23 of the largest weight
 (times a value of up to 2 max|v|, by the scales' powers of two); the fp32 sum divides.  Query
 pieces end at 2^-10 with a row maximum of at least 224: 2^-17.8 of it per element, which moves a
-score by up to 2^-17.8 scale max|q| sum|k| < 2^-12.5 at these sizes, so eta = 2^-12."""
+score by up to 2^-17.8 scale max|q| sum|k| < 2^-12.5 at these sizes, so eta = 2^-12.  An fp16
+query keeps 8 of its 11 bits: |dq| <= 2^-8 |q| (a second rounding to 4 bits of what the first
+left), so a row's scores move by at most dS = 2^-8 scale max_j sum |q| |k_j|, its normalised
+weights by a factor within exp(+-2 dS) and its LSE by dS."""
 import math
 
 import pytest
@@ -102,6 +105,10 @@ def check(s, o, lse, causal=True, scale=None, q=None):
         w = torch.exp(x - want_l[..., None]).masked_fill(~seen, 0.0).masked_fill(none[:, None], 0.0)
         want = torch.matmul(w, v)
         tol = torch.zeros_like(want)
+        ds = torch.zeros_like(want_l)
+        if m and quant and dtype == torch.float16:
+            far = torch.matmul(q[at:at + n].double().transpose(0, 1).abs(), k.abs().transpose(1, 2)) * scale
+            ds = 2.0 ** -8 * far.masked_fill(~seen, 0.0).amax(-1)
         if m:
             top = v.abs().amax()
             for r in range(0, n, 64):                        # sum_j w_j |v_j - O|, a block of rows at a time
@@ -113,7 +120,7 @@ def check(s, o, lse, causal=True, scale=None, q=None):
                     for c in range(0, d, 16):
                         far = (v[:, None, :, c:c + 16] - want[:, r:r + 64, None, c:c + 16]).abs()
                         tol[:, r:r + 64, c:c + 16] = (wr[..., None] * far).sum(2)
-            tol = (u + eta) * tol / (1 - u - eta) + 2.0 ** -17 * top
+            tol = (u + eta + torch.expm1(2 * ds)[..., None]) * tol / (1 - u - eta) + 2.0 ** -17 * top
         tol = tol + out_u * (want.abs() + tol) + 2.0 ** -25
         got = o[at:at + n].double().transpose(0, 1)
         err = (got - want).abs()
@@ -121,7 +128,7 @@ def check(s, o, lse, causal=True, scale=None, q=None):
         gl = lse[:, at:at + n].double()
         assert torch.equal(torch.isneginf(gl), none.expand_as(gl))
         keep = ~none.expand_as(gl)
-        assert torch.all((gl - want_l)[keep].abs() <= eta + 2.0 ** -20 * want_l[keep].abs()), b
+        assert torch.all((gl - want_l)[keep].abs() <= eta + (ds + 2.0 ** -20 * want_l.abs())[keep]), b
         at += n
 
 
@@ -152,6 +159,13 @@ CASES = [
     ([2] * 70, [30 * i + 2 for i in range(70)], 16, 4, 128, 32, FP, True, True, 200),
     ([40] * 3, [100, 64, 40], 3, 3, 128, 16, FP, False, True, -1),            # 40 rows: one tile
     ([90] * 3, [300, 164, 140], 3, 3, 128, 16, FP, True, True, 30),
+    ([2, 1, 2], [3000, 130, 2], 16, 4, 128, 64, BF, True, True, -1),          # 8 rows of four lanes
+    ([1, 1, 1], [1, 4097, 128], 5, 1, 64, 16, BF, True, True, -1),
+    ([1] * 9, [513 * i + 1 for i in range(9)], 8, 8, 128, 128, FP, True, False, -1),
+    ([1] * 3, [2000] * 3, 24, 2, 128, 32, BF, True, True, -1),                # 12 rows of e4m3
+    ([1] * 3, [2000] * 3, 40, 2, 64, 256, BF, True, True, 900),               # 20 rows of e4m3
+    ([70, 1, 1, 1], [2000, 700, 1500, 3000], 8, 2, 64, 64, BF, True, True, -1),
+    ([70, 65, 1, 64], [4000, 700, 1500, 64], 2, 2, 128, 128, FP, False, True, -1),
 ]
 
 
