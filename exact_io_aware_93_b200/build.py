@@ -53,13 +53,12 @@ def up_to_date(path: str = LIB_PATH) -> bool:
 
 # Kernels whose warpgroups rebalance registers with setmaxnreg: the split assumes that ptxas
 # gives every instantiation exactly the launch allocation named by the constant.
-# (Keys are patterns of mangled names; the paged kernel's instantiations with row copies do not
-# rebalance.)
+# (Keys are patterns of mangled names.)
 REG_CONTRACT = {
     "fa_fwd_kernel": ("fa_fwd_kernel.cuh", "kLaunchRegs"),
     "fa_bwd_main_kernel": ("fa_bwd_kernel.cuh", "kBwdLaunchRegs"),
-    "fa_paged_kernel.*ELb0ELi0E": ("fa_paged_kernel.cuh", "kPagedLaunchRegs"),
-    "fa_paged_kernel.*ELb1ELi0E": ("fa_paged_kernel.cuh", "kPagedLaunchRegsConv"),
+    "fa_paged_kernel.*ELb0E": ("fa_paged_kernel.cuh", "kPagedLaunchRegs"),
+    "fa_paged_kernel.*ELb1E": ("fa_paged_kernel.cuh", "kPagedLaunchRegsConv"),
 }
 
 

@@ -26,7 +26,8 @@ fa_status check_paged(const fa_paged_problem& p) {
   const long long cap = static_cast<long long>(p.max_pages) * p.page;
   const long long planes = static_cast<long long>(p.P) * p.H_kv;
   if (cap > INT_MAX - 1024 || planes >= INT_MAX || p.H_kv > 65535 || p.T > INT_MAX / 4) return FA_ERR_INVALID_ARG;
-  const long double tiles = static_cast<long double>(fa::paged_units(p)) * p.H_kv * ((cap + 127) / 128);
+  // (with one token per tile and pair, the most units there can be)
+  const long double tiles = static_cast<long double>(fa::paged_units(p, p.max_q, 1)) * p.H_kv * ((cap + 127) / 128);
   if (tiles > static_cast<long double>(1ll << 28)) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }

@@ -1,0 +1,596 @@
+// fa_paged_common.cuh -- attention over a paged cache: the work list, page loads, query scaling
+// and the join, shared by the kernels for few rows (fa_paged_few_kernel.cuh) and for tiles of 128
+// rows (fa_paged_kernel.cuh).
+//
+// Rows.  The G = H / H_kv query heads of a key/value head and a sequence's new tokens form the
+// rows r = i * G + g, so the cache is read once for all of them.  A TILE holds TQ tokens (one TMA
+// box of G heads x TQ tokens).  A UNIT is a pair of consecutive tiles of one (sequence, key/value
+// head), or one tile when a sequence has no more.
+//
+// Work list.  A unit visits T = hi - lo tiles of 128 keys, those that some row of it sees
+// (causal: up to its last token; window: from its first token's first key).  The key tiles of
+// all units are laid end to end (sequence, key/value head, unit), each as long as it takes
+// (Cfg::kPairCost, kSplitCost), and CTA c of the persistent grid takes the tiles that start in
+// [c L, (c+1) L), L = total / grid: every SM gets the same work whatever the mix of chunks,
+// single tokens and lengths.  A CTA's run falls into SEGMENTS, each inside one unit; a segment
+// that is not a whole unit leaves a partial result (O normalised, log-sums) that
+// fa_paged_merge_kernel joins.  The lengths are read on the device, so a captured graph replays
+// as they grow.  One warp walks the list and writes each segment into a small ring in shared
+// memory that the CTA's other warps follow.
+//
+// Pages.  A key tile is 128 / page boxes (or a part of one page), each fetched by its own lane
+// of the loading warp; page numbers are read 32 at a time, one window ahead.  Pages that no row
+// of the unit sees are not fetched, and value rows outside the unit's keys are zeroed in shared
+// memory: stale slots, and pages a sliding window has left behind, may hold anything.
+#pragma once
+
+#include "fa_cache_kernels.cuh"
+#include "fa_fwd_kernel.cuh"
+
+namespace fa {
+
+struct PgArgs {
+  const int* cu;          // [B + 1]
+  const int* seqlens;     // [B]
+  const int* table;       // [B, max_pages]
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  const float* q_scale;   // e4m3 pages: [T, H] factors of the scaled queries
+  void* out;              // [T, H, D]
+  float* lse;             // [H, T]
+  int* meta;              // total, L, unit prefix [B + 1], key-tile prefix [B + 1]
+  float* part_lse;        // [slots * kSubs, kRows, 2]
+  float* part_o;          // [slots * kSubs, kRows, D]
+  int n_lo, n_hi;         // sequences with more than n_lo and up to n_hi new tokens are computed
+  int B, T, H, H_kv, max_q, TQ, max_pages, page, page_shift, P, window, causal;
+  float scale_log2;
+  long long slots;        // 2 per CTA
+  int* status;
+};
+
+// ---------------------------------------------------------------- the work list
+struct PgSeq {
+  int q0, n, len, units;
+};
+__device__ __forceinline__ PgSeq pg_seq(const PgArgs& a, int b) {
+  const long long c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
+  PgSeq s;
+  const bool in = c0 >= 0 && c0 <= a.T && c1 > c0;
+  s.q0 = in ? static_cast<int>(c0) : 0;
+  s.n = in ? static_cast<int>(min(min(c1 - c0, static_cast<long long>(a.max_q)), a.T - c0)) : 0;
+  if (s.n <= a.n_lo || s.n > a.n_hi) s.n = 0;
+  const long long cap = static_cast<long long>(a.max_pages) * a.page;
+  s.len = static_cast<int>(min(max(static_cast<long long>(__ldg(a.seqlens + b)), 0ll), cap));
+  s.units = ((s.n + a.TQ - 1) / a.TQ + 1) / 2;
+  return s;
+}
+__device__ __forceinline__ bool pg_seq_ok(const PgArgs& a, int b) {
+  const long long c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
+  const long long len = __ldg(a.seqlens + b);
+  return c0 >= 0 && c1 >= c0 && c1 <= a.T && c1 - c0 <= a.max_q && len >= 0 &&
+         len <= static_cast<long long>(a.max_pages) * a.page;
+}
+
+// Keys [lo, hi) that the tokens at positions p0 .. p1 of a sequence of `len` keys see, and the
+// key tiles that hold them.
+struct PgKeys {
+  int lo, hi, t0, t1;
+};
+__device__ __forceinline__ PgKeys pg_keys(const PgArgs& a, int len, int p0, int p1) {
+  PgKeys k;
+  k.hi = a.causal ? min(p1 + 1, len) : len;
+  k.lo = a.window >= 0 ? max(0, p0 - a.window) : 0;
+  if (k.hi <= k.lo) k.hi = k.lo = 0;
+  k.t0 = k.lo >> 7;
+  k.t1 = (k.hi + 127) >> 7;
+  return k;
+}
+
+__device__ __forceinline__ PgKeys pg_unit_keys(const PgArgs& a, const PgSeq& s, int u) {
+  const int tok0 = u * 2 * a.TQ;
+  const int ntok = min(2 * a.TQ, s.n - tok0);
+  const int p0 = s.len - s.n + tok0;
+  return pg_keys(a, s.len, p0, p0 + ntok - 1);
+}
+
+__device__ __forceinline__ bool pg_is_pair(const PgArgs& a, const PgSeq& s, int u) {
+  return s.n - u * 2 * a.TQ > a.TQ;
+}
+
+// Cost of a sequence's units for one key/value head.
+template <typename Cfg>
+__device__ __forceinline__ int pg_seq_cost(const PgArgs& a, const PgSeq& s) {
+  int w = 0;
+  for (int u = 0; u < s.units; ++u) {
+    const PgKeys k = pg_unit_keys(a, s, u);
+    w += (k.t1 - k.t0) * (pg_is_pair(a, s, u) ? Cfg::kPairCost : Cfg::kSplitCost);
+  }
+  return w;
+}
+
+// This CTA's slice [t0, t1) of the work and the unit that t0 falls into, which starts at `start`.
+struct PgPlan {
+  int t0, t1, b, kvh, u, start;
+};
+
+// One warp.  With `write` it also stores the prefixes for the merge kernel and checks the
+// lengths and offsets.
+template <typename Cfg>
+__device__ __forceinline__ void pg_plan(const PgArgs& a, int lane, PgPlan* out, bool write) {
+  constexpr unsigned kFull = 0xffffffffu;
+  int total = 0;
+  PgSeq s{0, 0, 0, 0};
+  int w = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    s = PgSeq{0, 0, 0, 0};
+    if (b < a.B) s = pg_seq(a, b);
+    w = pg_seq_cost<Cfg>(a, s);
+    total += static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(w * a.H_kv)));
+  }
+  const int grid = static_cast<int>(gridDim.x);
+  // at least a tile's cost, so that no CTA inside a unit's span is left without one of its tiles
+  const int per = max((total + grid - 1) / grid, Cfg::kPairCost);
+  const int t0 = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(blockIdx.x) * per));
+  const int t1 = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(t0) + per));
+  bool found = t0 >= t1;
+  if (found && lane == 0) *out = PgPlan{t0, t0, 0, 0, 0, t0};
+  int acc = 0, uacc = 0;
+  for (int b0 = 0; b0 < a.B && (!found || write); b0 += 32) {
+    const int b = b0 + lane;
+    if (a.B > 32) {  // up to 32 sequences are still at hand
+      s = PgSeq{0, 0, 0, 0};
+      if (b < a.B) s = pg_seq(a, b);
+      w = pg_seq_cost<Cfg>(a, s);
+    }
+    if (write && b < a.B && !pg_seq_ok(a, b)) plan_fail(a.status, 43);
+    int incl = w * a.H_kv, uincl = s.units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, incl, o), y = __shfl_up_sync(kFull, uincl, o);
+      if (lane >= o) {
+        incl += x;
+        uincl += y;
+      }
+    }
+    incl += acc;
+    uincl += uacc;
+    const int excl = incl - w * a.H_kv;
+    if (write && b < a.B) {
+      a.meta[2 + b + 1] = uincl;
+      a.meta[2 + a.B + 1 + b + 1] = incl;
+    }
+    if (!found && b < a.B && excl <= t0 && t0 < incl) {  // one lane
+      const int kvh = (t0 - excl) / w;
+      int start = excl + kvh * w, u = 0;
+      while (true) {
+        const PgKeys k = pg_unit_keys(a, s, u);
+        const int c = (k.t1 - k.t0) * (pg_is_pair(a, s, u) ? Cfg::kPairCost : Cfg::kSplitCost);
+        if (t0 < start + c) break;
+        start += c;
+        ++u;
+      }
+      *out = PgPlan{t0, t1, b, kvh, u, start};
+    }
+    found = found || (t0 < __shfl_sync(kFull, incl, 31));
+    acc = __shfl_sync(kFull, incl, 31);
+    uacc = __shfl_sync(kFull, uincl, 31);
+  }
+  if (write && lane == 0) {
+    a.meta[0] = total;
+    a.meta[1] = per;
+    a.meta[2] = 0;
+    a.meta[2 + a.B + 1] = 0;
+  }
+}
+
+// Key tiles [lo, hi).
+struct PgRange {
+  int lo, hi;
+};
+
+// A run of nt key tiles from tile kt0 of one unit; nt = 0 ends a CTA's list.
+struct PgSeg {
+  int b, kvh;
+  int q0;        // the unit's first token
+  int pos0;      // its position
+  int ntok;      // tokens of the unit
+  int len;
+  PgKeys keys;   // what the unit sees
+  int kt0, nt;
+  int pair;      // two tiles
+  int whole;     // the run is the whole unit
+  int slot;      // of a partial result: 0 when the unit started in an earlier CTA, else 1
+  PgRange tile[2];  // pair: the key tiles of the run that each tile visits
+};
+
+// Walks this CTA's slice segment by segment (the schedule's warp, every lane alike).
+template <typename Cfg>
+struct PgWalk {
+  int t0, t1, b, kvh, u, start;
+  PgSeq s;
+  __device__ __forceinline__ PgWalk(const PgArgs& a, const PgPlan& p)
+      : t0(p.t0), t1(p.t1), b(p.b), kvh(p.kvh), u(p.u), start(p.start), s(pg_seq(a, p.b)) {}
+  __device__ __forceinline__ bool next(const PgArgs& a, PgSeg& g) {
+    while (start < t1) {
+      if (u >= s.units) {
+        u = 0;
+        if (s.units == 0 || ++kvh >= a.H_kv) {
+          kvh = 0;
+          if (++b >= a.B) return false;
+          s = pg_seq(a, b);
+        }
+        continue;
+      }
+      const PgKeys k = pg_unit_keys(a, s, u);
+      const bool pair = pg_is_pair(a, s, u);
+      const int cost = pair ? Cfg::kPairCost : Cfg::kSplitCost;
+      const int T = k.t1 - k.t0;
+      // the tiles that start in [t0, t1)
+      const int first = t0 > start ? (t0 - start + cost - 1) / cost : 0;
+      const int last = min(T, (t1 - start + cost - 1) / cost);
+      const int tok0 = u * 2 * a.TQ;
+      start += T * cost;
+      ++u;
+      if (first >= last) continue;
+      g.b = b;
+      g.kvh = kvh;
+      g.q0 = s.q0 + tok0;
+      g.pos0 = s.len - s.n + tok0;
+      g.ntok = min(2 * a.TQ, s.n - tok0);
+      g.len = s.len;
+      g.keys = k;
+      g.kt0 = k.t0 + first;
+      g.nt = last - first;
+      g.pair = pair;
+      g.whole = first == 0 && last == T;
+      g.slot = first == 0;
+      for (int i = 0; i < 2; ++i) {
+        const int tok = i * a.TQ;
+        const int n = min(a.TQ, g.ntok - tok);
+        PgRange r{0, 0};
+        if (n > 0) {
+          const PgKeys kt = pg_keys(a, g.len, g.pos0 + tok, g.pos0 + tok + n - 1);
+          r = PgRange{max(kt.t0, g.kt0), min(kt.t1, g.kt0 + g.nt)};
+          if (r.hi < r.lo) r.hi = r.lo;
+        }
+        g.tile[i] = r;
+      }
+      return true;
+    }
+    return false;
+  }
+};
+
+// The key tiles of a segment in the order the MMA warp consumes them.  pair: K_j, V_j; split:
+// K_0, .., K_{Ahead-1}, V_0, K_Ahead, V_1, ..  f(is_value, tile) returns false to stop.
+template <int Ahead, typename F>
+__device__ __forceinline__ bool pg_loads(const PgSeg& g, F f) {
+  if (g.pair) {
+    for (int t = 0; t < g.nt; ++t)
+      if (!f(false, g.kt0 + t) || !f(true, g.kt0 + t)) return false;
+    return true;
+  }
+  for (int t = 0; t < Ahead && t < g.nt; ++t)
+    if (!f(false, g.kt0 + t)) return false;
+  for (int t = 0; t < g.nt; ++t)
+    if (!f(true, g.kt0 + t) || (t + Ahead < g.nt && !f(false, g.kt0 + t + Ahead))) return false;
+  return true;
+}
+
+// Page numbers of one sequence as the loading warp needs them: windows of 32 table entries, the
+// even and the odd one held (keys run a few tiles ahead of values), one read ahead.
+struct PgPages {
+  int even, odd, ahead, at;
+  __device__ __forceinline__ int entry(const PgArgs& a, int b, int win, int lane) const {
+    const long long i = static_cast<long long>(win) * 32 + lane;
+    return i < a.max_pages ? __ldg(a.table + static_cast<long long>(b) * a.max_pages + i) : -1;
+  }
+  __device__ __forceinline__ void start(const PgArgs& a, const PgSeg& g, int lane) {
+    at = (((g.kt0 << 7) >> a.page_shift) >> 5) - 1;
+    ahead = entry(a, g.b, at + 1, lane);
+  }
+  // Page number of tile j's page p0 + k (p0 its first), per lane.
+  __device__ __forceinline__ int get(const PgArgs& a, const PgSeg& g, int p0, int k, int lane) {
+    if ((p0 >> 5) > at) {
+      at = p0 >> 5;
+      if (at & 1) odd = ahead; else even = ahead;
+      ahead = entry(a, g.b, at + 1, lane);
+    }
+    return __shfl_sync(0xffffffffu, (p0 >> 5) & 1 ? odd : even, (p0 + k) & 31);
+  }
+};
+
+// Issues the boxes of key tile j that hold a key of the unit (whole warp; the slot is free).
+template <int kRowBytes, int kChunks>
+__device__ __forceinline__ void pg_load_tile(const PgArgs& a, const PgSeg& g, PgPages& pages, const CUtensorMap* map,
+                                             int j, uint8_t* dst, uint64_t* full, int lane) {
+  const int box = min(128, a.page);         // keys per box
+  const int p0 = (j << 7) >> a.page_shift;  // the tile's first page
+  const int k0 = max(g.keys.lo - (j << 7), 0) / box;
+  const int k1 = (min(g.keys.hi - (j << 7), 128) + box - 1) / box;
+  if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>((k1 - k0) * box * kRowBytes * kChunks));
+  __syncwarp();
+  const int k = k0 + lane / kChunks, c = lane % kChunks;
+  const int id = pages.get(a, g, p0, k, lane);
+  if (k < k1) {
+    const int row = (j << 7) & (a.page - 1) & ~(box - 1);  // inside a page of 256
+    const bool good = id >= 0 && id < a.P;
+    if (!good) plan_fail(a.status, 44);
+    // a bad page number reads as zeros: a coordinate past the pool
+    if (FA_IN_BOUNDS(row + box <= a.page && p0 + k < a.max_pages && k * box < 128, a.status, 502))
+      tma_load_3d(dst + c * 128 * kRowBytes + k * box * kRowBytes, map, full, c * 64, row,
+                  good ? id * a.H_kv + g.kvh : a.P * a.H_kv);
+  }
+  __syncwarp();
+}
+
+// The scale bytes of a lane's four keys of tile j; 2^0 for keys the unit does not see.
+__device__ __forceinline__ void pg_fetch_scales(const PgArgs& a, const PgSeg& g, int j, int lane, uint32_t& kw,
+                                                uint32_t& vw) {
+  kw = vw = 0x7f7f7f7fu;
+  const int key = (j << 7) + lane * 4;
+  if (key + 3 < g.keys.lo || key >= g.keys.hi) return;
+  const int pg = key >> a.page_shift;
+  const int id = pg < a.max_pages ? __ldg(a.table + static_cast<int64_t>(g.b) * a.max_pages + pg) : -1;
+  if (id < 0 || id >= a.P) return;
+  const int64_t at = (static_cast<int64_t>(id) * a.H_kv + g.kvh) * a.page + (key & (a.page - 1));
+  if (!FA_IN_BOUNDS(at >= 0 && at + 4 <= static_cast<int64_t>(a.P) * a.H_kv * a.page, a.status, 511)) return;
+  kw = __ldg(reinterpret_cast<const uint32_t*>(a.k_scales + at));
+  vw = __ldg(reinterpret_cast<const uint32_t*>(a.v_scales + at));
+}
+
+// The largest exponent of a tile's scale bytes (NaN apart) over the keys the unit sees, or -1000.
+__device__ __forceinline__ int pg_top(const PgSeg& g, int j, int lane, uint32_t w) {
+  int top = -1000;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int key = (j << 7) + lane * 4 + x;
+    const int b = (w >> (8 * x)) & 255;
+    if (key >= g.keys.lo && key < g.keys.hi && b != 255) top = max(top, b - 127);
+  }
+  return __reduce_max_sync(0xffffffffu, top);
+}
+
+// The factor 2^(byte - 127 - e) of a scale byte as fp32 and as fp16 bits; NaN for 255, and zero
+// for what lies far below 2^e.
+__device__ __forceinline__ float pg_factor(int byte, int e) {
+  const int d = byte - 127 - e;
+  return byte == 255 ? __uint_as_float(0x7fc00000u) : (d < -126 ? 0.f : __int_as_float((127 + d) << 23));
+}
+__device__ __forceinline__ uint32_t pg_factor16(int byte, int e) {
+  const int d = min(byte - 127 - e, 0);
+  return byte == 255 ? 0x7e00u : (d >= -14 ? static_cast<uint32_t>(15 + d) << 10 : (d >= -24 ? 1u << (24 + d) : 0u));
+}
+
+// Sets value rows [z0, z1) of a tile to zero (one warp).  kRowBytes per chunk, kChunks chunks.
+template <int kRowBytes, int kChunks>
+__device__ __forceinline__ void pg_zero_rows(uint8_t* tile, int z0, int z1, int lane) {
+  constexpr int kUnits = kRowBytes / 16;
+  for (int u = lane; u < (z1 - z0) * kUnits * kChunks; u += 32) {
+    const int c = u % kChunks, x = u / kChunks;
+    *reinterpret_cast<uint4*>(tile + c * 128 * kRowBytes + z0 * kRowBytes + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// Value rows of tile j that the unit does not see are zeroed: zero weights times stale infinities
+// would not be zero (one warp, after the tile has landed).
+template <int kRowBytes, int kChunks>
+__device__ __forceinline__ void pg_clean(const PgSeg& g, int j, uint8_t* tile, int lane) {
+  const int z0 = max(g.keys.lo - (j << 7), 0), z1 = min(g.keys.hi - (j << 7), 128);
+  if (z0 > 0 || z1 < 128) {
+    pg_zero_rows<kRowBytes, kChunks>(tile, 0, z0, lane);
+    pg_zero_rows<kRowBytes, kChunks>(tile, z1, 128, lane);
+    fence_proxy_async_smem();
+    __syncwarp();
+  }
+}
+
+// ---------------------------------------------------------------- queries for e4m3 pages
+// Every query row is scaled by a power of two, 2^e the smallest with max|row| <= 448 * 2^e, and
+//   kPieces   cut into two e4m3 pieces: the rounding of q / 2^e and that of the rest; exact for
+//             bf16, 8 significant bits of an fp16's 11, down to 2^-18 of the row's largest
+//   otherwise written as fp16: exact for both types, down to 2^-33 of the row's largest
+// Piece i of (token, head) lies at out[((i T + token) H + head) D], fp16 rows likewise; factors
+// 2^e at q_scale[token H + head].  D / 16 lanes per row.
+template <int D, Elem E, bool kPieces>
+__global__ void __launch_bounds__(256) fa_paged_scale_q_kernel(const void* q, int64_t token_stride, int64_t head_stride,
+                                                               uint8_t* out, float* q_scale, int T, int H,
+                                                               int* status) {
+  constexpr int L = D / 16;
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / L;
+  const int item = threadIdx.x % L;
+  const bool live = row < static_cast<int64_t>(T) * H;
+  const int64_t token = row / H;
+  const int h = static_cast<int>(row - token * H);
+  float f[16];
+  float amax = 0.f;
+  if (live) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const typename ElemOps<E>::T*>(q) +
+                                                      token * token_stride + h * head_stride + item * 16);
+    const uint4 x0 = __ldg(src), x1 = __ldg(src + 1);
+    const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 v = ElemOps<E>::unpack(w[i]);
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (fabsf(f[i]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(f[i]));
+      else f[i] = __uint_as_float(0x7fc00000u);
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < L; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const int e = e4m3_exponent<Elem::kBf16>(amax);
+  const float inv = __int_as_float((127 - e) << 23);
+  if (!live || !FA_IN_BOUNDS(token < T && h < H && item * 16 + 16 <= D, status, 510)) return;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] *= inv;
+  if constexpr (kPieces) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      uint32_t c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = pack_e4m3x4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        const float2 a = e4m3x2_to_float2(c[i]), b = e4m3x2_to_float2(c[i] >> 16);
+        f[4 * i] -= a.x;
+        f[4 * i + 1] -= a.y;
+        f[4 * i + 2] -= b.x;
+        f[4 * i + 3] -= b.y;
+      }
+      *reinterpret_cast<uint4*>(out + ((static_cast<int64_t>(p) * T + token) * H + h) * D + item * 16) =
+          make_uint4(c[0], c[1], c[2], c[3]);
+    }
+  } else {
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = pack_f16x2(f[2 * i], f[2 * i + 1]);
+    uint4* dst = reinterpret_cast<uint4*>(out + (row * D + item * 16) * 2);
+    dst[0] = make_uint4(c[0], c[1], c[2], c[3]);
+    dst[1] = make_uint4(c[4], c[5], c[6], c[7]);
+  }
+  if (item == 0) q_scale[row] = __int_as_float((127 + e) << 23);
+}
+
+// ---------------------------------------------------------------- joining the partial results
+// Per row: LSE = log sum_s exp(lse_s) and O = sum_s exp(lr_s - LR) O_s with LR = log sum_s
+// exp(lr_s), the convex combination one CTA would have formed.  Units that one CTA computed
+// were written by it; rows of units without keys get O = 0, LSE = -inf.  Block (unit,
+// key/value head, part) of four warps; W warps share a row's partial results.
+template <int D, Elem E, typename Cfg, int W>
+__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PgArgs a) {
+  using T = typename ElemOps<E>::T;
+  constexpr unsigned kFull = 0xffffffffu;
+  constexpr int V = D / 32;  // columns per lane
+  __shared__ float acc_sh[W > 1 ? W : 1][D];
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int G = a.H / a.H_kv;
+  const int kvh = blockIdx.y;
+  const int unit = blockIdx.x;
+  const int b = find_seq(a.meta + 2, a.B, unit, lane);
+  if (b >= a.B) return;
+  const PgSeq s = pg_seq(a, b);
+  const int u = unit - a.meta[2 + b];
+  const int tok0 = u * 2 * a.TQ;
+  const int ntok = min(2 * a.TQ, s.n - tok0);
+  const PgKeys k = pg_unit_keys(a, s, u);
+  const int T_u = k.t1 - k.t0;
+  const int* costs = a.meta + 2 + a.B + 1;
+  int start = costs[b] + kvh * ((costs[b + 1] - costs[b]) / a.H_kv);
+  int before = 0;  // the sequence's units before this one are pairs
+  for (int x = lane; x < u; x += 32) {
+    const PgKeys kx = pg_unit_keys(a, s, x);
+    before += (kx.t1 - kx.t0) * Cfg::kPairCost;
+  }
+  start += static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(before)));
+  const int per = a.meta[1];
+  const int cf = start / per;
+  const int cost = pg_is_pair(a, s, u) ? Cfg::kPairCost : Cfg::kSplitCost;
+  const int cl = T_u > 0 ? (start + (T_u - 1) * cost) / per : cf;
+  if (T_u > 0 && cf == cl) return;  // written by its CTA
+  const int parts = T_u > 0 ? cl - cf + 1 : 0;
+  const int rows = G * ntok;
+  for (int row = blockIdx.z * (4 / W) + warp / W; row < rows; row += gridDim.z * (4 / W)) {
+    const int tile = row / (G * a.TQ);
+    const int rc = row - tile * G * a.TQ;
+    const int iq = row / G, h = kvh * G + (row - iq * G);
+    const int64_t token = static_cast<int64_t>(s.q0) + tok0 + iq;
+    // index of partial result i of this row
+    auto at = [&](int i) -> int64_t {
+      const int slot = 2 * (cf + i) + (i == 0);
+      return (static_cast<int64_t>(slot) * Cfg::kSubs + tile) * Cfg::kRows + rc;
+    };
+    float mx_l = -INFINITY, mx_r = -INFINITY, s_l = 0.f, s_r = 0.f;
+    for (int i = lane; i < parts; i += 32) {
+      const int64_t x = at(i);
+      if (!FA_IN_BOUNDS(x >= 0 && x < a.slots * Cfg::kSubs * Cfg::kRows, a.status, 507)) continue;
+      const float2 v = *reinterpret_cast<const float2*>(a.part_lse + x * 2);
+      mx_l = fmaxf(mx_l, v.x);
+      mx_r = fmaxf(mx_r, v.y);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      mx_l = fmaxf(mx_l, __shfl_xor_sync(kFull, mx_l, o));
+      mx_r = fmaxf(mx_r, __shfl_xor_sync(kFull, mx_r, o));
+    }
+    if (mx_l == -INFINITY) mx_l = 0.f;  // no key, or NaN only: the sums decide
+    if (mx_r == -INFINITY) mx_r = 0.f;
+    for (int i = lane; i < parts; i += 32) {
+      const int64_t x = at(i);
+      if (!FA_IN_BOUNDS(x >= 0 && x < a.slots * Cfg::kSubs * Cfg::kRows, a.status, 508)) continue;
+      const float2 v = *reinterpret_cast<const float2*>(a.part_lse + x * 2);
+      s_l += expf(v.x - mx_l);
+      s_r += expf(v.y - mx_r);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s_l += __shfl_xor_sync(kFull, s_l, o);
+      s_r += __shfl_xor_sync(kFull, s_r, o);
+    }
+    float acc[V];
+#pragma unroll
+    for (int x = 0; x < V; ++x) acc[x] = 0.f;
+    const float inv = s_r == 0.f ? 0.f : 1.0f / s_r;
+    // 32 partial results at a time: a lane forms one weight, then the warp sums the rows with
+    // the weights broadcast; a partial result without keys was not written and is not read
+    for (int base = (W > 1 ? warp * 32 : 0); base < parts; base += 32 * W) {
+      float wl = 0.f;
+      int64_t x = 0;
+      if (base + lane < parts) {
+        x = at(base + lane);
+        const float v = a.part_lse[x * 2 + 1];
+        wl = v == -INFINITY ? 0.f : expf(v - mx_r) * inv;
+      }
+      const int cnt = min(32, parts - base);
+#pragma unroll 4
+      for (int t = 0; t < cnt; ++t) {
+        const float wgt = __shfl_sync(kFull, wl, t);
+        const int64_t xt = __shfl_sync(kFull, x, t);
+        if (wgt == 0.f) continue;
+        const float* po = a.part_o + xt * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(po);
+          acc[0] = fmaf(wgt, v.x, acc[0]);
+          acc[1] = fmaf(wgt, v.y, acc[1]);
+          acc[2] = fmaf(wgt, v.z, acc[2]);
+          acc[3] = fmaf(wgt, v.w, acc[3]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(po);
+          acc[0] = fmaf(wgt, v.x, acc[0]);
+          acc[1] = fmaf(wgt, v.y, acc[1]);
+        }
+      }
+    }
+    if constexpr (W > 1) {
+#pragma unroll
+      for (int x = 0; x < V; ++x) acc_sh[warp][lane * V + x] = acc[x];
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int x = 0; x < V; ++x) {
+          acc[x] = 0.f;
+#pragma unroll
+          for (int y = 0; y < W; ++y) acc[x] += acc_sh[y][lane * V + x];
+        }
+      }
+      __syncthreads();
+      if (warp != 0) continue;
+    }
+    if (FA_IN_BOUNDS(token >= 0 && token < a.T && h < a.H, a.status, 509)) {
+      T* orow = static_cast<T*>(a.out) + (token * a.H + h) * D + lane * V;
+      if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(orow) =
+            make_uint2(ElemOps<E>::pack(acc[0], acc[1]), ElemOps<E>::pack(acc[2], acc[3]));
+      else
+        *reinterpret_cast<uint32_t*>(orow) = ElemOps<E>::pack(acc[0], acc[1]);
+      if (lane == 0) a.lse[static_cast<int64_t>(h) * a.T + token] = s_l == 0.f ? -INFINITY : mx_l + logf(s_l);
+    }
+  }
+}
+
+}  // namespace fa

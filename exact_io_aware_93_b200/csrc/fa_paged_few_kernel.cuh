@@ -1,0 +1,724 @@
+// fa_paged_few_kernel.cuh -- exact attention over a paged cache for few query rows per key/value
+// head (up to 32: single tokens, drafted tokens), for sm_100a.  The work list, the page loads and
+// the join of partial results are in fa_paged_common.cuh.
+//
+// The cache is a stream: nothing but its bytes should cost time, so the KEYS take the 128 rows of
+// the tensor core's tile and the few query rows its narrow side:
+//   S^T = K Q^T    M = 128 keys, N = the rows, both operands as they lie in shared memory
+//   O^T += V^T P^T M = d, N = the rows, V read MN-major
+// A product then moves its 128-row operand once (32 cycles of shared memory) and the narrow side
+// is nearly free: 16 products of 32 cycles per tile (8 with e4m3 pages) where rows-first tiles
+// need 16 of 64.  A softmax thread owns one KEY of a tile and all rows, so a tile costs it as many
+// exponentials as there are rows, the sums stay in registers until the segment ends, and the
+// narrow score tiles leave tensor memory for four of them in flight.
+//
+// The two softmax groups take alternate key tiles, each with its own accumulator.  A group's
+// rows share one reference maximum per row over its 128 threads: per tile each warp posts whether
+// one of its scores exceeds the reference by 2^8; only then do the four warps exchange maxima and
+// rescale O^T.  Weights P^T go to shared memory as the next product's B operand.
+//
+// e4m3 pages.  The codes are operands as they are (kind::f8f6f4): a tile moves half the bytes and
+// nothing is converted.
+//   Q   two e4m3 pieces per row (fa_paged_scale_q_kernel), as rows r and RW + r of the tile: the
+//       two score columns are added by the key's thread
+//   P   the weight, an fp16 value rounded to 9 bits, is the sum of three e5m2 pieces (e5m2 is the
+//       upper byte of an fp16): relative error 2^-9 down to 2^-23 of the largest weight.  e5m2
+//       and not e4m3 for its range: a long tail of small weights beside a large one keeps its
+//       mass.  The pieces are rows of P^T, their products columns of O^T, added at the end.
+//   scales  a key's 2^ek and 2^(ev - E) are one number each for its thread; E is the largest
+//       value exponent of the group's tiles so far (O^T is rescaled when it grows).
+// (The rows-first form of this kernel took 187 us for 16 sequences of 16-32K tokens; it waited for
+// its softmax and its products in turn.)
+//
+// Warp roles (384 threads): warps 0-3 and 4-7 the softmax groups, warp 8 the schedule and the TMA
+// loads, warp 9 the MMA issuer, warps 10 and 11 the scales of groups 0 and 1.
+#pragma once
+
+#include "fa_paged_common.cuh"
+
+namespace fa {
+
+constexpr int kPPieces = 3;      // e5m2 pieces of a weight
+constexpr float kPShift = 7.0f;  // weights cut into pieces are 2^(x - m + 7) <= 2^15
+
+template <int D, bool Q8, int RW>
+struct PfCfg {
+  static constexpr int kRows = RW;      // rows of a tile and of a partial result
+  static constexpr int kSubs = 1;
+  static constexpr int kPairCost = 1;   // units are single tiles
+  static constexpr int kSplitCost = 1;
+  static constexpr int kThreads = 384;
+  static constexpr int kAhead = 3;      // key tiles whose scores run ahead of their values
+  static constexpr int kSBufs = 4;
+  // a row in shared memory: 128-byte chunks of 64 16-bit elements, or D codes (D = 64 in the
+  // 64-byte swizzle)
+  static constexpr int kRowBytes = Q8 ? D : 128;
+  static constexpr int kChunks = Q8 ? 1 : D / 64;
+  static constexpr int kChunkBytes = 128 * kRowBytes;
+  static constexpr int kTileBytes = kChunks * kChunkBytes;
+  // N of the products: rows, or two pieces of each; and three pieces, in whole 16s
+  static constexpr int kNS = Q8 ? 2 * RW : (RW < 16 ? 16 : RW);
+  static constexpr int kNO = Q8 ? (3 * RW + 15) / 16 * 16 : (RW < 16 ? 16 : RW);
+  static constexpr int kQPartBytes = kNS * kRowBytes;
+  static constexpr int kQBytes = kChunks * kQPartBytes;
+  static constexpr int kPChunks = Q8 ? 1 : 2;         // 128 keys of a row in 128-byte chunks
+  static constexpr int kPChunkBytes = kNO * 128;
+  static constexpr int kPBytes = kPChunks * kPChunkBytes;
+  static constexpr int kStages = (Q8 ? (RW == 32 ? 10 : 12) : (RW == 32 ? 5 : 6)) * (128 / D);
+  static constexpr int kScaleRing = 4;
+  static constexpr int kSegRing = 4;
+  static constexpr int kSegReaders = 9 + (Q8 ? 2 : 0);  // warps
+  static constexpr uint32_t kOCol = kSBufs * kNS;
+  static constexpr uint32_t kCols = kOCol + 2 * kNO;
+  static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512);
+  static_assert(kCols <= 512 && RW % 8 == 0, "tensor memory");
+};
+
+// Scale bytes of one key tile and the largest value exponent so far.
+struct PfScales {
+  uint32_t k[32];
+  uint32_t v[32];
+  int e;
+  int pad[3];
+};
+
+template <int D, bool Q8, int RW>
+struct __align__(1024) PfSmem {
+  using Cfg = PfCfg<D, Q8, RW>;
+  uint8_t kv[Cfg::kStages][Cfg::kTileBytes];
+  uint8_t q[2][Cfg::kQBytes];
+  uint8_t p[2][Cfg::kPBytes];               // each group's P^T
+  alignas(16) float part[RW][D];            // group 1's O on its way to group 0
+  PfScales scales[2][Q8 ? Cfg::kScaleRing : 1];
+  float2 sums[2][4][RW];                    // l, lr of each group's warps
+  float ref[2][RW];                         // each group's reference maxima
+  float weight[2][RW];                      // of each group's O in the result
+  float top[2][4][RW];                      // maxima of a group's warps, when one is raised
+  uint8_t flag[2][2][4];                    // tiles' parity: does a warp want to raise
+  PgSeg segs[Cfg::kSegRing];
+  uint64_t q_full[2];
+  uint64_t q_empty[2];
+  uint64_t kv_full[Cfg::kStages];
+  uint64_t kv_empty[Cfg::kStages];
+  uint64_t sc_full[2][Cfg::kScaleRing];
+  uint64_t sc_empty[2][Cfg::kScaleRing];
+  uint64_t seg_full[Cfg::kSegRing];
+  uint64_t seg_empty[Cfg::kSegRing];
+  uint64_t s_full[Cfg::kSBufs];
+  uint64_t s_empty[Cfg::kSBufs];
+  uint64_t p_full[2];
+  uint64_t p_empty[2];  // the group's last product is complete
+  uint64_t group[2];    // a group's warps
+  uint64_t groups;      // both groups
+  uint64_t mma_drain;
+  PgPlan plan;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Columns of tensor memory, N a multiple of 8.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t t, uint32_t (&r)[N]) {
+  if constexpr (N % 32 == 0) {
+#pragma unroll
+    for (int c = 0; c < N; c += 32) tmem_ld32(t + c, r + c);
+  } else if constexpr (N % 16 == 0) {
+#pragma unroll
+    for (int c = 0; c < N; c += 16) tmem_ld16(t + c, r + c);
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; c += 8) tmem_ld8(t + c, r + c);
+  }
+}
+
+// Largest value over the warp (NaN apart or not: either leaves the row NaN).
+__device__ __forceinline__ float warp_max(float x) {
+  const int b = __float_as_int(x);
+  const int m = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+  return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
+}
+
+template <int D, Elem E, bool Q8, int RW>
+__global__ void __launch_bounds__(384, 1)
+    fa_paged_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const PgArgs a) {
+  using Cfg = PfCfg<D, Q8, RW>;
+  using T = typename ElemOps<E>::T;
+  constexpr int NS = Cfg::kStages;
+  constexpr int NSC = Cfg::kScaleRing;
+  constexpr int NSEG = Cfg::kSegRing;
+  constexpr int NB = Cfg::kSBufs;
+  constexpr unsigned kFull = 0xffffffffu;
+  extern __shared__ uint8_t smem_raw[];
+  PfSmem<D, Q8, RW>& sm = *reinterpret_cast<PfSmem<D, Q8, RW>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                                ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int G = a.H / a.H_kv;
+  int* status = a.status;
+
+  if (threadIdx.x == 0) {
+    sm.abort_flag = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_empty[i], 1);
+      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.p_empty[i], 1);
+      mbar_init(&sm.group[i], 4);
+      if constexpr (Q8) {
+        for (int s = 0; s < NSC; ++s) {
+          mbar_init(&sm.sc_full[i][s], 1);
+          mbar_init(&sm.sc_empty[i][s], 4);
+        }
+      }
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&sm.kv_full[s], 1);
+      mbar_init(&sm.kv_empty[s], 1);
+    }
+    for (int s = 0; s < NB; ++s) {
+      mbar_init(&sm.s_full[s], 1);
+      mbar_init(&sm.s_empty[s], 4);
+    }
+    for (int s = 0; s < NSEG; ++s) {
+      mbar_init(&sm.seg_full[s], 1);
+      mbar_init(&sm.seg_empty[s], Cfg::kSegReaders);
+    }
+    mbar_init(&sm.groups, 8);
+    mbar_init(&sm.mma_drain, 1);
+    fence_mbar_init();
+  }
+  // rows of a query tile that hold no query are never loaded
+  for (uint32_t i = threadIdx.x; i < 2u * Cfg::kQBytes / 16; i += Cfg::kThreads)
+    reinterpret_cast<uint4*>(sm.q[0])[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  if (warp == 9) {
+    tmem_alloc(&sm.tmem_base, Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 8) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    pg_plan<Cfg>(a, lane, &sm.plan, blockIdx.x == 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = sm.tmem_base;
+
+  // Readers of the segment ring: the next segment, or null at the end or after an abort; a
+  // reader gives the one it holds back first.
+  uint32_t nseg = 0;
+  auto next_seg = [&](const WaitCtx& wc) -> const PgSeg* {
+    if (nseg > 0) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.seg_empty[(nseg - 1) % NSEG]);
+    }
+    const int i = nseg % NSEG;
+    if (!__all_sync(kFull, mbar_wait(&sm.seg_full[i], (nseg / NSEG) & 1, wc))) return nullptr;
+    ++nseg;
+    return sm.segs[i].nt > 0 ? &sm.segs[i] : nullptr;
+  };
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ schedule and TMA loads
+    const WaitCtx wc{&sm.abort_flag, status, 31};
+    PgWalk<Cfg> w(a, sm.plan);
+    PgSeg g;
+    PgPages pages{};
+    uint32_t it = 0, qcnt[2] = {0, 0};
+    bool ok = true;
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, wc)); };
+    while (ok) {
+      const int i = nseg % NSEG;
+      const bool more = w.next(a, g);
+      if (more) pages.start(a, g, lane);
+      ok = wait_all(&sm.seg_empty[i], ((nseg / NSEG) & 1) ^ 1);
+      if (!ok) break;
+      if (lane == 0) {
+        if (!more) g.nt = 0;
+        sm.segs[i] = g;
+        mbar_arrive(&sm.seg_full[i]);
+      }
+      const int qs = nseg & 1;
+      ++nseg;
+      if (!more) break;
+      ok = wait_all(&sm.q_empty[qs], (qcnt[qs] & 1) ^ 1);
+      if (!ok) break;
+      // a box of G heads x TQ tokens per chunk, or per piece
+      constexpr int kBoxes = Q8 ? 2 : Cfg::kChunks;
+      if (lane == 0)
+        mbar_arrive_expect_tx(&sm.q_full[qs], static_cast<uint32_t>(kBoxes * Cfg::kRowBytes * G * a.TQ));
+      __syncwarp();
+      if (lane < kBoxes &&
+          FA_IN_BOUNDS(g.q0 >= 0 && g.q0 < a.T && g.kvh < a.H_kv && G * a.TQ <= RW, status, 520))
+        tma_load_4d(sm.q[qs] + lane * (Q8 ? RW * Cfg::kRowBytes : Cfg::kQPartBytes), &tm_q, &sm.q_full[qs],
+                    Q8 ? 0 : lane * 64, 0, g.kvh, Q8 ? lane * a.T + g.q0 : g.q0);
+      __syncwarp();
+      ++qcnt[qs];
+      ok = pg_loads<Cfg::kAhead>(g, [&](bool isv, int j) -> bool {
+        const int slot = it % NS;
+        if (!wait_all(&sm.kv_empty[slot], ((it / NS) & 1) ^ 1)) return false;
+        ++it;
+        pg_load_tile<Cfg::kRowBytes, Cfg::kChunks>(a, g, pages, isv ? &tm_v : &tm_k, j, sm.kv[slot], &sm.kv_full[slot],
+                                                   lane);
+        return true;
+      });
+    }
+    if (!ok && lane == 0) {
+      // Unwinding: wait (bounded) for the copies still in flight before the CTA exits.
+      for (uint32_t idx = (it > static_cast<uint32_t>(NS) ? it - NS : 0); idx < it; ++idx)
+        mbar_wait_drain(&sm.kv_full[idx % NS], (idx / NS) & 1, status);
+      for (int i = 0; i < 2; ++i)
+        if (qcnt[i] > 0) mbar_wait_drain(&sm.q_full[i], (qcnt[i] - 1) & 1, status);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer (whole warp)
+    const WaitCtx wc{&sm.abort_flag, status, 32};
+    // K, Q K-major; V MN-major, P K-major
+    constexpr uint32_t idesc_s =
+        Q8 ? idesc_kind_f8(128, Cfg::kNS, 0, 0, 0) : idesc_kind_f16(128, Cfg::kNS, 0, 0, ElemOps<E>::kMmaType);
+    constexpr uint32_t idesc_o =
+        Q8 ? idesc_kind_f8(D, Cfg::kNO, 1, 0, 1) : idesc_kind_f16(D, Cfg::kNO, 1, 0, ElemOps<E>::kMmaType);
+    constexpr uint32_t kGroup = 8 * Cfg::kRowBytes;  // 8-row groups
+    auto desc = [](const void* p, uint32_t lbo, uint32_t sbo) {
+      return Cfg::kRowBytes == 64 ? sdesc_sw64(smem_u32(p), lbo, sbo) : sdesc_sw128(smem_u32(p), lbo, sbo);
+    };
+    const uint64_t dq0 = desc(sm.q[0], 16, kGroup);
+    const uint64_t dp0 = sdesc_sw128(smem_u32(sm.p[0]), 16, 1024);
+    const uint64_t dk0 = desc(sm.kv[0], 16, kGroup);
+    const uint64_t dv0 = desc(sm.kv[0], Cfg::kChunkBytes, kGroup);
+    auto issue_s = [&](int buf, int qs, int slot) {
+      const uint64_t dk = dk0 + static_cast<uint64_t>((slot * Cfg::kTileBytes) >> 4);
+      const uint64_t dq = dq0 + static_cast<uint64_t>((qs * Cfg::kQBytes) >> 4);
+      const uint32_t tS = tbase + buf * Cfg::kNS;
+      if constexpr (Q8) {
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk)
+          umma_ss_f8_w(tS, dk + ((kk * 32) >> 4), dq + ((kk * 32) >> 4), idesc_s, kk > 0);
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss_w(tS, dk + (((kk / 4) * Cfg::kChunkBytes + (kk % 4) * 32) >> 4),
+                    dq + (((kk / 4) * Cfg::kQPartBytes + (kk % 4) * 32) >> 4), idesc_s, kk > 0);
+      }
+    };
+    auto issue_pv = [&](int grp, int slot, uint32_t acc) {
+      const uint64_t dv = dv0 + static_cast<uint64_t>((slot * Cfg::kTileBytes) >> 4);
+      const uint64_t dp = dp0 + static_cast<uint64_t>((grp * Cfg::kPBytes) >> 4);
+      const uint32_t tO = tbase + Cfg::kOCol + grp * Cfg::kNO;
+      if constexpr (Q8) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_ss_f8_w(tO, dv + ((kk * 32 * Cfg::kRowBytes) >> 4), dp + ((kk * 32) >> 4), idesc_o, (kk > 0) || acc);
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_ss_w(tO, dv + ((kk * 16 * 128) >> 4), dp + (((kk / 4) * Cfg::kPChunkBytes + (kk % 4) * 32) >> 4), idesc_o,
+                    (kk > 0) || acc);
+      }
+    };
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, wc)); };
+    uint32_t it = 0, qcnt = 0, scnt = 0, pcnt[2] = {0, 0};
+    bool ok = true;
+    while (ok) {
+      const PgSeg* gp = next_seg(wc);
+      if (gp == nullptr) break;
+      const PgSeg& g = *gp;
+      const int nt = g.nt, kt0 = g.kt0;
+      const int qs = (nseg - 1) & 1;
+      ok = wait_all(&sm.q_full[qs], (qcnt >> 1) & 1);
+      if (!ok) break;
+      ++qcnt;
+      ok = pg_loads<Cfg::kAhead>(g, [&](bool isv, int j) -> bool {
+        const int slot = it % NS;
+        if (!wait_all(&sm.kv_full[slot], (it / NS) & 1)) return false;
+        ++it;
+        const int t = j - kt0;
+        if (!isv) {
+          const int buf = scnt % NB;
+          if (!wait_all(&sm.s_empty[buf], ((scnt / NB) & 1) ^ 1)) return false;
+          ++scnt;
+          tc_fence_after();
+          issue_s(buf, qs, slot);
+          umma_commit_w(&sm.s_full[buf]);
+          if (t == nt - 1) umma_commit_w(&sm.q_empty[qs]);
+        } else {
+          const int grp = t & 1;
+          pg_clean<Cfg::kRowBytes, Cfg::kChunks>(g, j, sm.kv[slot], lane);
+          if (!wait_all(&sm.p_full[grp], (grp ? pcnt[1] : pcnt[0]) & 1)) return false;
+          if (grp) ++pcnt[1]; else ++pcnt[0];
+          tc_fence_after();
+          issue_pv(grp, slot, t >= 2);
+          umma_commit_w(&sm.p_empty[grp]);
+        }
+        umma_commit_w(&sm.kv_empty[slot]);
+        return true;
+      });
+    }
+    // Wait for every MMA issued to finish before the columns are freed.
+    umma_commit_w(&sm.mma_drain);
+    mbar_wait_drain(&sm.mma_drain, 0, status);
+    __syncwarp();
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------ scales of group warp - 10
+    if constexpr (Q8) {
+      const int grp = warp - 10;
+      const WaitCtx wc{&sm.abort_flag, status, 35};
+      uint32_t cnt = 0;
+      bool ok = true;
+      while (ok) {
+        const PgSeg* gp = next_seg(wc);
+        if (gp == nullptr) break;
+        const PgSeg& g = *gp;
+        const int jend = g.kt0 + g.nt;
+        int e = -1000;
+        uint32_t kw = 0, vw = 0, kn = 0, vn = 0;
+        if (g.kt0 + grp < jend) pg_fetch_scales(a, g, g.kt0 + grp, lane, kw, vw);
+        for (int j = g.kt0 + grp; j < jend; j += 2) {
+          if (j + 2 < jend) pg_fetch_scales(a, g, j + 2, lane, kn, vn);  // in flight over this tile
+          e = max(e, pg_top(g, j, lane, vw));
+          const int slot = cnt % NSC;
+          ok = __all_sync(kFull, mbar_wait(&sm.sc_empty[grp][slot], ((cnt / NSC) & 1) ^ 1, wc));
+          if (!ok) break;
+          ++cnt;
+          PfScales& sc = sm.scales[grp][slot];
+          sc.k[lane] = kw;
+          sc.v[lane] = vw;
+          if (lane == 0) sc.e = max(e, -127);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.sc_full[grp][slot]);
+          kw = kn;
+          vw = vn;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax groups
+    const int grp = warp >> 2;
+    const int wq = warp & 3;
+    const int me = wq * 32 + lane;  // this thread's key of a tile
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tO = tbase + Cfg::kOCol + grp * Cfg::kNO + lane_off;
+    const WaitCtx wc{&sm.abort_flag, status, 33 + grp};
+    uint8_t* const prow = sm.p[grp];
+    uint32_t tiles = 0, mine = 0, gcnt = 0, xcnt = 0;  // score tiles, the group's, barriers passed
+    bool ok = true;
+    auto sync4 = [&]() -> bool {  // the group's warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.group[grp]);
+      const bool r = __all_sync(kFull, mbar_wait(&sm.group[grp], gcnt & 1, wc));
+      ++gcnt;
+      return r;
+    };
+    auto sync8 = [&]() -> bool {  // both groups
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.groups);
+      const bool r = __all_sync(kFull, mbar_wait(&sm.groups, xcnt & 1, wc));
+      ++xcnt;
+      return r;
+    };
+    while (ok) {
+      const PgSeg* gp = next_seg(wc);
+      if (gp == nullptr) break;
+      const PgSeg& g = *gp;
+      const int M = G * g.ntok;
+      const int nt = g.nt, kt0 = g.kt0;
+      // every row sees the keys from all_lo to all_hi
+      const int all_hi = a.causal ? g.pos0 : g.len - 1;
+      const int all_lo = a.window >= 0 ? g.pos0 + g.ntok - 1 - a.window : 0;
+      float ref[RW], l[RW], lr[RW], c_row[Q8 ? RW : 1];
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        ref[r] = -INFINITY;
+        l[r] = lr[r] = 0.f;
+      }
+      if constexpr (Q8) {
+        // log2 units per score: the scale and the row's query factor
+        int i = 0, h = 0;
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+          c_row[r] = a.scale_log2;
+          if (r < M && FA_IN_BOUNDS(g.q0 + i < a.T && h < G, status, 521))
+            c_row[r] *= __ldg(a.q_scale + (static_cast<int64_t>(g.q0) + i) * a.H + g.kvh * G + h);
+          if (++h == G) h = 0, ++i;
+        }
+      }
+      int e_ref = 0;
+      bool first = true;
+      for (int t = grp; t < nt; t += 2) {
+        const int ss = mine % NSC;
+        float kf = 1.f, vf = 1.f;
+        int e = 0;
+        if constexpr (Q8) {
+          ok = __all_sync(kFull, mbar_wait(&sm.sc_full[grp][ss], (mine / NSC) & 1, wc));
+          if (!ok) break;
+          const PfScales& sc = sm.scales[grp][ss];
+          e = sc.e;
+          kf = e8m0_to_float(reinterpret_cast<const uint8_t*>(sc.k)[me]);
+          vf = pg_factor(reinterpret_cast<const uint8_t*>(sc.v)[me], e);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.sc_empty[grp][ss]);
+        }
+        const uint32_t tile = tiles + t;
+        const int buf = tile % NB;
+        ok = __all_sync(kFull, mbar_wait(&sm.s_full[buf], (tile / NB) & 1, wc));
+        if (!ok) break;
+        tc_fence_after();
+        float x[RW];  // scores in log2 units
+        {
+          uint32_t s[Q8 ? 2 * RW : RW];
+          tmem_ld_cols(tbase + buf * Cfg::kNS + lane_off, s);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.s_empty[buf]);
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            if constexpr (Q8)
+              x[r] = (__uint_as_float(s[r]) + __uint_as_float(s[RW + r])) * kf * c_row[r];
+            else
+              x[r] = __uint_as_float(s[r]) * a.scale_log2;
+          }
+        }
+        const int k0 = (kt0 + t) << 7;
+        if (k0 + 127 > all_hi || k0 < all_lo) {
+          const int key = k0 + me;
+          int i = 0, h = 0;
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            const int pos = g.pos0 + i;
+            const int hi = a.causal ? min(pos, g.len - 1) : g.len - 1;
+            const int lo = a.window >= 0 ? pos - a.window : 0;
+            if (key > hi || key < lo) x[r] = -INFINITY;
+            if (++h == G) h = 0, ++i;
+          }
+          if constexpr (Q8) {
+            if (key >= g.keys.hi || key < g.keys.lo) vf = 0.f;  // a stale scale may be NaN
+          }
+        }
+        bool raise = false;
+#pragma unroll
+        for (int r = 0; r < RW; ++r) raise = raise || (r < M && x[r] > ref[r] + kTau);
+        const bool grown = Q8 && !first && e > e_ref;
+        const bool any = __any_sync(kFull, raise);
+        if (lane == 0) sm.flag[grp][mine & 1][wq] = any || grown;
+        ok = sync4();
+        if (!ok) break;
+        const uint32_t raised = *reinterpret_cast<const uint32_t*>(sm.flag[grp][mine & 1]);
+        // the group's previous product is complete: P^T may be overwritten, O^T rescaled
+        ok = __all_sync(kFull, mbar_wait(&sm.p_empty[grp], (mine & 1) ^ 1, wc));
+        if (!ok) break;
+        if (raised) {
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            const float m = warp_max(x[r]);
+            if (lane == 0) sm.top[grp][wq][r] = m;
+          }
+          ok = sync4();
+          if (!ok) break;
+          const float shrink = (grown && e - e_ref <= 126) ? __int_as_float((127 + e_ref - e) << 23) : (grown ? 0.f : 1.f);
+          float alpha[RW];
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            const float m = fmaxf(fmaxf(sm.top[grp][0][r], sm.top[grp][1][r]),
+                                  fmaxf(sm.top[grp][2][r], sm.top[grp][3][r]));
+            const bool up = m > ref[r] + kTau;
+            alpha[r] = up ? ex2_approx(ref[r] - m) : 1.f;
+            l[r] *= alpha[r];
+            lr[r] *= alpha[r];
+            if (up) ref[r] = m;
+            alpha[r] *= shrink;
+          }
+          if (!first) {
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < (Q8 ? 3 * RW : RW); c += 8) {
+              uint32_t o[8];
+              tmem_ld8(tO + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 8; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha[(c + y) % RW]);
+              tmem_st8(tO + c, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        e_ref = e;
+        // weights, and their place in P^T: row r, this thread's key
+        if constexpr (Q8) {
+          const uint32_t at = me & 15;
+          const uint32_t unit = me >> 4;
+#pragma unroll
+          for (int r = 0; r < RW; r += 2) {
+            float w[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float p = ex2_approx(x[r + y] - (ref[r + y] == -INFINITY ? 0.f : ref[r + y]) + kPShift);
+              l[r + y] += p;
+              w[y] = p * vf;
+            }
+            // fp16, rounded to 9 significant bits; its upper byte is the e5m2 truncation, and each
+            // remainder is exact in fp16
+            uint32_t v = pack_f16x2(w[0], w[1]) + 0x00020002u;
+#pragma unroll
+            for (int piece = 0; piece < kPPieces; ++piece) {
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                prow[(piece * RW + r + y) * 128 + ((unit ^ ((r + y) & 7)) << 4) + at] =
+                    static_cast<uint8_t>(v >> (8 + 16 * y));
+              if (piece + 1 < kPPieces)
+                asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v) : "r"(v), "r"(v & 0xff00ff00u));
+            }
+          }
+        } else {
+          const uint32_t base = (me >> 6) * Cfg::kPChunkBytes + (me & 7) * 2;
+          const uint32_t unit = (me >> 3) & 7;
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            const float p = ex2_approx(x[r] - (ref[r] == -INFINITY ? 0.f : ref[r]));
+            const T v = ElemOps<E>::one(p);
+            l[r] += p;
+            // bf16: the rounded weights normalise O, as in softmax_row
+            lr[r] += E == Elem::kBf16 ? static_cast<float>(v) : p;
+            *reinterpret_cast<T*>(prow + base + r * 128 + ((unit ^ (r & 7)) << 4)) = v;
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[grp]);
+        ++mine;
+        first = false;
+      }
+      tiles += nt;
+      if (!ok) break;
+      // Sums over the group's keys, then both groups' weights of each row
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        if constexpr (Q8) lr[r] = l[r];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          l[r] += __shfl_xor_sync(kFull, l[r], o);
+          if constexpr (!Q8) lr[r] += __shfl_xor_sync(kFull, lr[r], o);
+        }
+        if constexpr (Q8) lr[r] = l[r];
+        if (lane == 0) sm.sums[grp][wq][r] = make_float2(l[r], lr[r]);
+        if (wq == 0 && lane == 0) sm.ref[grp][r] = Q8 ? ref[r] - kPShift : ref[r];
+      }
+      // the group's last product (none: passes at once)
+      ok = __all_sync(kFull, mbar_wait(&sm.p_empty[grp], (mine & 1) ^ 1, wc));
+      if (!ok) break;
+      tc_fence_after();
+      if (Q8 && wq == 0 && lane == 0) sm.top[grp][0][0] = e8m0_to_float(static_cast<uint32_t>(e_ref + 127));
+      ok = sync8();
+      if (!ok) break;
+      const int64_t part0 = (static_cast<int64_t>(blockIdx.x) * 2 + g.slot) * Cfg::kRows;
+      if (grp == 0 && me < M) {
+        float2 sum[2];
+        float m[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          sum[y] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            sum[y].x += sm.sums[y][z][me].x;
+            sum[y].y += sm.sums[y][z][me].y;
+          }
+          m[y] = sm.ref[y][me];
+        }
+        const float mm = fmaxf(m[0], m[1]);
+        const float top = mm == -INFINITY ? 0.f : mm;
+        const float e0 = ex2_approx(m[0] - top), e1 = ex2_approx(m[1] - top);
+        const float ls = e0 * sum[0].x + e1 * sum[1].x, lrs = e0 * sum[0].y + e1 * sum[1].y;
+        sm.weight[0][me] = sum[0].y == 0.f || lrs == 0.f ? 0.f : e0 * (Q8 ? sm.top[0][0][0] : 1.f) / lrs;
+        sm.weight[1][me] = sum[1].y == 0.f || lrs == 0.f ? 0.f : e1 * (Q8 ? sm.top[1][0][0] : 1.f) / lrs;
+        const float lse_l = ls == 0.f ? -INFINITY : (top + lg2_approx(ls)) * kLn2;
+        const float lse_r = lrs == 0.f ? -INFINITY : (top + lg2_approx(lrs)) * kLn2;
+        const int i = me / G;
+        const int64_t token = static_cast<int64_t>(g.q0) + i;
+        const int h = g.kvh * G + me - i * G;
+        if (g.whole) {
+          if (FA_IN_BOUNDS(token >= 0 && token < a.T && h < a.H, status, 522))
+            a.lse[static_cast<int64_t>(h) * a.T + token] = lse_l;
+        } else if (FA_IN_BOUNDS(part0 + me < a.slots * Cfg::kRows, status, 523)) {
+          *reinterpret_cast<float2*>(a.part_lse + (part0 + me) * 2) = make_float2(lse_l, lse_r);
+        }
+      }
+      ok = sync8();
+      if (!ok) break;
+      // O^T: a thread holds one column of the rows, of the group's own keys (a group without tiles
+      // has weight 0 and unwritten columns)
+      const int d = D == 128 ? me : wq * 16 + lane;
+      const bool has = !first;
+      const bool live = D == 128 || lane < 16;
+      auto rows8 = [&](int r0, float (&v)[8]) {
+#pragma unroll
+        for (int y = 0; y < 8; ++y) v[y] = 0.f;
+        if (has) {
+#pragma unroll
+          for (int piece = 0; piece < (Q8 ? kPPieces : 1); ++piece) {
+            uint32_t o[8];
+            tmem_ld8(tO + piece * RW + r0, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 8; ++y) v[y] += __uint_as_float(o[y]);
+          }
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const float w = r0 + y < M ? sm.weight[grp][r0 + y] : 0.f;
+            v[y] = w == 0.f ? 0.f : v[y] * w;
+          }
+        }
+      };
+      if (grp == 1) {
+#pragma unroll 1
+        for (int r0 = 0; r0 < M; r0 += 8) {
+          float v[8];
+          rows8(r0, v);
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            if (live) sm.part[r0 + y][d] = v[y];
+        }
+      }
+      ok = sync8();
+      if (!ok) break;
+      if (grp == 0) {
+#pragma unroll 1
+        for (int r0 = 0; r0 < M; r0 += 8) {
+          float v[8];
+          rows8(r0, v);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int r = r0 + y;
+            if (!live || r >= M) continue;
+            const float o = v[y] + sm.part[r][d];
+            const int i = r / G;
+            const int64_t token = static_cast<int64_t>(g.q0) + i;
+            const int h = g.kvh * G + r - i * G;
+            if (g.whole) {
+              if (FA_IN_BOUNDS(token >= 0 && token < a.T && h < a.H && d < D, status, 524))
+                static_cast<T*>(a.out)[(token * a.H + h) * D + d] = ElemOps<E>::one(o);
+            } else if (FA_IN_BOUNDS(part0 + r < a.slots * Cfg::kRows && d < D, status, 525)) {
+              a.part_o[(part0 + r) * D + d] = o;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tbase, Cfg::kTmemCols);
+  }
+}
+
+}  // namespace fa

@@ -25,46 +25,62 @@ struct PagedCall {
   cudaStream_t stream;
 };
 
-// The kernel's variant (PgCfg's R) by the rows that one key/value head contributes at most: 4
-// copies of up to 16 rows in a tile, 2 of up to 32, otherwise 0 for tiles of 128 rows; with e4m3
-// pages 8 for 4 copies of up to 8 rows of four lanes each.
-inline int paged_copies(const fa_paged_problem& p) {
-  const long long rows = static_cast<long long>(p.H / p.H_kv) * p.max_q;
-  if (p.quant && rows <= 8) return 8;
-  return rows <= 16 ? 4 : (rows <= 32 ? 2 : 0);
+// Which kernels a call takes.  A key/value head's rows, (H / H_kv) * n for n new tokens, choose
+// per sequence: up to `rows` of them the few-rows kernel (n <= few_q), more the tiles of 128.
+//   all sequences few (max_q says so): that kernel alone, at the smallest of 8, 16, 32 rows
+//   all sequences max_q tokens long (T = B max_q): the tiles alone
+//   a mixture: both, one after the other, single tokens in the first at the smallest size
+struct PagedSplit {
+  int rows;   // 8, 16, 32, or 0: the few-rows kernel is not used
+  int few_q;  // its most tokens per sequence
+  bool many;
+};
+inline PagedSplit paged_split(const fa_paged_problem& p) {
+  const int G = p.H / p.H_kv;
+  const long long rows = static_cast<long long>(G) * p.max_q;
+  if (rows <= 32) return {rows <= 8 ? 8 : (rows <= 16 ? 16 : 32), p.max_q, false};
+  if (G > 32 || static_cast<long long>(p.B) * p.max_q == p.T) return {0, 0, true};
+  const int r = G <= 8 ? 8 : (G <= 16 ? 16 : 32);
+  return {r, r / G, true};
 }
-inline int paged_tile_tokens(const fa_paged_problem& p) {
-  return paged_copies(p) ? p.max_q : 128 / (p.H / p.H_kv);
-}
-// At most this many units (pairs of tiles) per key/value head: each sequence's last may be short.
-inline long long paged_units(const fa_paged_problem& p) {
-  const long long tokens = 2ll * paged_tile_tokens(p);
-  const long long each = static_cast<long long>(p.B) * ((p.max_q + tokens - 1) / tokens);
+// At most this many units (pairs of tiles of TQ tokens) per key/value head among sequences of up
+// to n tokens: each sequence's last may be short.
+inline long long paged_units(const fa_paged_problem& p, int n, int TQ) {
+  const long long tokens = 2ll * TQ;
+  const long long each = static_cast<long long>(p.B) * ((n + tokens - 1) / tokens);
   const long long all = p.T / tokens + p.B;
   return each < all ? each : all;
 }
 
-// Workspace regions: the plan (total, tiles per CTA, unit and key-tile prefixes), then the
-// partial log-sums [rows, 2] and the partial outputs [rows, d]; a CTA leaves at most two
-// partial segments of 256 rows (8, 16 or 32 where a tile holds copies).  With e4m3 pages also the
-// query pieces (2 bytes per element) and a factor per query row.
+// Workspace regions of each kernel used: the plan (total, work per CTA, unit and work prefixes),
+// the partial log-sums [rows, 2] and outputs [rows, d] (a CTA leaves at most two partial segments,
+// of `rows` or 256 rows), and with e4m3 pages the scaled queries (2 bytes per element); then a
+// factor per query row.
 struct PagedLayout {
-  size_t meta, part_lse, part_o, pieces, q_scale, total;
-  long long slots;
+  struct Pass {
+    size_t meta, part_lse, part_o, q;
+  };
+  Pass few, many;
+  size_t q_scale, total;
 };
 inline PagedLayout paged_layout(const fa_paged_problem& p, int grid) {
   const auto round256 = [](size_t x) { return (x + 255) / 256 * 256; };
-  const int R = paged_copies(p);
-  const size_t rows = 2 * static_cast<size_t>(grid) * (R == 0 ? 256 : (R == 8 ? 8 : 64 / R));
-  PagedLayout L;
-  L.slots = 2ll * grid;
-  L.meta = 0;
-  L.part_lse = round256((2 + 2 * (static_cast<size_t>(p.B) + 1)) * 4);
-  L.part_o = L.part_lse + round256(rows * 2 * 4);
-  L.pieces = L.part_o + round256(rows * static_cast<size_t>(p.d) * 4);
+  const PagedSplit s = paged_split(p);
   const size_t q_rows = p.quant ? static_cast<size_t>(p.T) * p.H : 0;
-  L.q_scale = L.pieces + round256(q_rows * p.d * 2);
-  L.total = L.q_scale + q_rows * 4;
+  PagedLayout L{};
+  size_t at = 0;
+  const auto pass = [&](PagedLayout::Pass& x, size_t rows) {
+    rows *= 2 * static_cast<size_t>(grid);
+    x.meta = at;
+    x.part_lse = x.meta + round256((2 + 2 * (static_cast<size_t>(p.B) + 1)) * 4);
+    x.part_o = x.part_lse + round256(rows * 2 * 4);
+    x.q = x.part_o + round256(rows * static_cast<size_t>(p.d) * 4);
+    at = x.q + round256(q_rows * p.d * 2);
+  };
+  if (s.rows) pass(L.few, s.rows);
+  if (s.many) pass(L.many, 256);
+  L.q_scale = at;
+  L.total = at + q_rows * 4;
   return L;
 }
 

@@ -196,6 +196,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
+// 32 lanes x 32-bit, 8 consecutive columns per thread.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
 // 32 lanes x 32-bit, 16 consecutive columns per thread.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -265,9 +272,9 @@ __host__ __device__ constexpr uint32_t idesc_kind_f16(int M, int N, int a_mn_maj
          | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// kind::f8f6f4 with fp32 accumulator; A of format `a_type` (0 = e4m3, 1 = e5m2), B e4m3.
-__host__ __device__ constexpr uint32_t idesc_kind_f8(int M, int N, int a_mn_major, int b_mn_major, uint32_t a_type) {
-  return idesc_kind_f16(M, N, a_mn_major, b_mn_major, 0) | (a_type << 7);
+// kind::f8f6f4 with fp32 accumulator; A e4m3, B of format `b_type` (0 = e4m3, 1 = e5m2).
+__host__ __device__ constexpr uint32_t idesc_kind_f8(int M, int N, int a_mn_major, int b_mn_major, uint32_t b_type) {
+  return idesc_kind_f16(M, N, a_mn_major, b_mn_major, 0) | (b_type << 10);
 }
 
 // MMA issue.  Every lane of the calling warp executes these with the same operands and one
