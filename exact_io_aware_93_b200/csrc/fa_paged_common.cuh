@@ -373,6 +373,10 @@ __device__ __forceinline__ void pg_zero_rows(uint8_t* tile, int z0, int z1, int 
   }
 }
 
+__device__ __forceinline__ bool pg_cleans(const PgSeg& g, int j) {
+  return g.keys.lo > j << 7 || g.keys.hi < (j + 1) << 7;
+}
+
 // Value rows of tile j that the unit does not see are zeroed: zero weights times stale infinities
 // would not be zero (one warp, after the tile has landed).
 template <int kRowBytes, int kChunks>

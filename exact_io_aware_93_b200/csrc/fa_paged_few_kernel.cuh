@@ -105,7 +105,6 @@ struct __align__(1024) PfSmem {
   uint64_t seg_full[Cfg::kSegRing];
   uint64_t seg_empty[Cfg::kSegRing];
   uint64_t s_full[Cfg::kSBufs];
-  uint64_t s_empty[Cfg::kSBufs];
   uint64_t p_full[2];
   uint64_t p_empty[2];  // the group's last product is complete
   uint64_t group[2];    // a group's warps
@@ -150,8 +149,8 @@ __global__ void __launch_bounds__(384, 1)
   constexpr int NB = Cfg::kSBufs;
   constexpr unsigned kFull = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
-  PfSmem<D, Q8, RW>& sm = *reinterpret_cast<PfSmem<D, Q8, RW>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                                ~static_cast<uintptr_t>(1023));
+  // aligned by an offset and not through an integer: the compiler keeps seeing shared memory
+  PfSmem<D, Q8, RW>& sm = *reinterpret_cast<PfSmem<D, Q8, RW>*>(smem_raw + (1024u - (smem_u32(smem_raw) & 1023u)) % 1024u);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int G = a.H / a.H_kv;
@@ -178,7 +177,6 @@ __global__ void __launch_bounds__(384, 1)
     }
     for (int s = 0; s < NB; ++s) {
       mbar_init(&sm.s_full[s], 1);
-      mbar_init(&sm.s_empty[s], 4);
     }
     for (int s = 0; s < NSEG; ++s) {
       mbar_init(&sm.seg_full[s], 1);
@@ -331,34 +329,51 @@ __global__ void __launch_bounds__(384, 1)
       const PgSeg& g = *gp;
       const int nt = g.nt, kt0 = g.kt0;
       const int qs = (nseg - 1) & 1;
-      ok = wait_all(&sm.q_full[qs], (qcnt >> 1) & 1);
+      // Scores of tile t: its buffer was last read for tile t - 4, whose weights (posted after the
+      // read) the products of tile t - 4 have been waited for.
+      auto scores = [&](int t) {
+        const int slot = it % NS;
+        ++it;
+        const int buf = scnt % NB;
+        ++scnt;
+        issue_s(buf, qs, slot);
+        umma_commit_w(&sm.s_full[buf]);
+        umma_commit_w(&sm.kv_empty[slot]);
+        if (t == nt - 1) umma_commit_w(&sm.q_empty[qs]);
+      };
+      ok = mbar_wait_lanes(lane == 0 ? &sm.q_full[qs] : (lane == 1 ? &sm.kv_full[it % NS] : nullptr),
+                           lane == 0 ? (qcnt >> 1) & 1 : (it / NS) & 1, wc);
       if (!ok) break;
       ++qcnt;
-      ok = pg_loads<Cfg::kAhead>(g, [&](bool isv, int j) -> bool {
-        const int slot = it % NS;
-        if (!wait_all(&sm.kv_full[slot], (it / NS) & 1)) return false;
-        ++it;
-        const int t = j - kt0;
-        if (!isv) {
-          const int buf = scnt % NB;
-          if (!wait_all(&sm.s_empty[buf], ((scnt / NB) & 1) ^ 1)) return false;
-          ++scnt;
-          tc_fence_after();
-          issue_s(buf, qs, slot);
-          umma_commit_w(&sm.s_full[buf]);
-          if (t == nt - 1) umma_commit_w(&sm.q_empty[qs]);
-        } else {
-          const int grp = t & 1;
-          pg_clean<Cfg::kRowBytes, Cfg::kChunks>(g, j, sm.kv[slot], lane);
-          if (!wait_all(&sm.p_full[grp], (grp ? pcnt[1] : pcnt[0]) & 1)) return false;
-          if (grp) ++pcnt[1]; else ++pcnt[0];
-          tc_fence_after();
-          issue_pv(grp, slot, t >= 2);
-          umma_commit_w(&sm.p_empty[grp]);
+      tc_fence_after();
+      scores(0);
+      for (int t = 1; t < Cfg::kAhead && t < nt && ok; ++t) {
+        ok = __all_sync(kFull, mbar_wait(&sm.kv_full[it % NS], (it / NS) & 1, wc));
+        if (ok) scores(t);
+      }
+      for (int t = 0; t < nt && ok; ++t) {
+        const int grp = t & 1;
+        const int slot = it % NS;  // V_t; K_{t + kAhead} follows
+        const uint32_t p = grp ? pcnt[1] : pcnt[0];
+        const bool more = t + Cfg::kAhead < nt;
+        const bool cleans = pg_cleans(g, kt0 + t);
+        if (cleans) {
+          ok = __all_sync(kFull, mbar_wait(&sm.kv_full[slot], (it / NS) & 1, wc));
+          if (!ok) break;
+          pg_clean<Cfg::kRowBytes, Cfg::kChunks>(g, kt0 + t, sm.kv[slot], lane);
         }
+        const uint32_t mine = it + (lane == 1);
+        ok = mbar_wait_lanes(lane < 1 + more ? &sm.kv_full[mine % NS] : (lane == 2 ? &sm.p_full[grp] : nullptr),
+                             lane == 2 ? p & 1 : (mine / NS) & 1, wc);
+        if (!ok) break;
+        ++it;
+        if (grp) ++pcnt[1]; else ++pcnt[0];
+        tc_fence_after();
+        issue_pv(grp, slot, t >= 2);
+        umma_commit_w(&sm.p_empty[grp]);
         umma_commit_w(&sm.kv_empty[slot]);
-        return true;
-      });
+        if (more) scores(t + Cfg::kAhead);
+      }
     }
     // Wait for every MMA issued to finish before the columns are freed.
     umma_commit_w(&sm.mma_drain);
@@ -474,9 +489,6 @@ __global__ void __launch_bounds__(384, 1)
           uint32_t s[Q8 ? 2 * RW : RW];
           tmem_ld_cols(tbase + buf * Cfg::kNS + lane_off, s);
           tmem_wait_ld();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.s_empty[buf]);
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
             if constexpr (Q8)

@@ -22,7 +22,8 @@
 // Warp roles (384 threads, 512 with e4m3 pages): warps 0-3 and 4-7 the softmax groups, warp 8 the
 // schedule and the TMA loads, warp 9 the MMA issuer, warps 10-11 the scales, warps 12-15 the
 // conversion.
-// Tensor memory: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [256+D,256+2D); P overwrites S.
+// Tensor memory: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [256+D,256+2D); P
+// overwrites the second half of S.
 #pragma once
 
 #include "fa_paged_common.cuh"
@@ -123,8 +124,8 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
   constexpr int NSEG = Cfg::kSegRing;
   constexpr unsigned kFull = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
-  PgSmem<D, E, Q8>& sm = *reinterpret_cast<PgSmem<D, E, Q8>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                                    ~static_cast<uintptr_t>(1023));
+  // aligned by an offset and not through an integer: the compiler keeps seeing shared memory
+  PgSmem<D, E, Q8>& sm = *reinterpret_cast<PgSmem<D, E, Q8>*>(smem_raw + (1024u - (smem_u32(smem_raw) & 1023u)) % 1024u);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int G = a.H / a.H_kv;
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
         const uint64_t dv = dv0 + static_cast<uint64_t>((slot * Cfg::kTileBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
-          umma_ts_w(tbase + Cfg::kOCol + i * D, tbase + i * 128 + kk * 8, dv + ((kk * 16 * 128) >> 4), idesc_o,
+          umma_ts_w(tbase + Cfg::kOCol + i * D, tbase + i * 128 + 64 + kk * 8, dv + ((kk * 16 * 128) >> 4), idesc_o,
                     (kk > 0) || acc);
       };
       auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, wc)); };
@@ -332,7 +333,8 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
             const int sv = slot;
             clean(sv, j);
             int skn = -1;
-            if (j + 1 < jhi) {
+            // K_{j+1}: with three slots of converted tiles it is not there before V_{j-1}'s is free
+            if (!Q8 && j + 1 < jhi) {
               ok = take();
               if (!ok) break;
               skn = slot;
@@ -346,6 +348,13 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
                 issue_pv(i, sv, j > rg[i].lo);
                 if (j + 1 == rg[i].hi) umma_commit_w(&sm.o_done[i]);
               }
+              if (Q8 && i == 1) umma_commit_w(&sm.kv_empty[sv]);
+              if (Q8 && i == 0 && j + 1 < jhi) {
+                ok = take();
+                if (!ok) break;
+                tc_fence_after();
+                skn = slot;
+              }
               if (in(i, j + 1)) {
                 issue_s(i, i, skn);
                 umma_commit_w(&sm.s_full[i]);
@@ -353,7 +362,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
               }
             }
             if (!ok) break;
-            umma_commit_w(&sm.kv_empty[sv]);
+            if (!Q8) umma_commit_w(&sm.kv_empty[sv]);
             if (skn >= 0) umma_commit_w(&sm.kv_empty[skn]);
           }
           for (int i = 0; i < 2; ++i)
@@ -508,19 +517,19 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
 #pragma unroll 1
           for (int base = r0; base < 128; base += U * kStep) {
             uint4 c[U];
-            uint32_t f[U], o[U][8];
+            uint32_t f[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               c[u] = *reinterpret_cast<const uint4*>(sm.raw[rs] + (base + u * kStep) * D + in_unit * 16);
               f[u] = sm.factors[fs][base + u * kStep];
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) pg_convert16(c[u], f[u], o[u]);
-#pragma unroll
             for (int u = 0; u < U; ++u) {
+              uint32_t o[8];
+              pg_convert16(c[u], f[u], o);
               uint8_t* p = dst + (base + u * kStep) * 128;
-              const uint4 lo = make_uint4(o[u][0], o[u][1], o[u][2], o[u][3]);
-              const uint4 hi = make_uint4(o[u][4], o[u][5], o[u][6], o[u][7]);
+              const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]);
+              const uint4 hi = make_uint4(o[4], o[5], o[6], o[7]);
               *reinterpret_cast<uint4*>(p + (first << 4)) = odd ? hi : lo;
               *reinterpret_cast<uint4*>(p + (second << 4)) = odd ? lo : hi;
             }
@@ -602,63 +611,73 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
         tc_fence_after();
         if (rows_here) {
           const int k0 = j << 7;
-          uint32_t s[kBN];
-#pragma unroll
-          for (int c = 0; c < kBN; c += 32) tmem_ld32(tS + c, s + c);
-          tmem_wait_ld();
           float c_tile = c_row;
           if constexpr (Q8) c_tile *= sm.scales[grp][ss].k;
-          if (k0 + kBN - 1 > all_hi || k0 < all_lo) {
-            const int lim = vis_hi - k0, first = vis_lo - k0;
-#pragma unroll
-            for (int c = 0; c < kBN; ++c)
-              if (c > lim || c < first) s[c] = __float_as_uint(-INFINITY);
-          }
-          float mx8[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) mx8[x] = fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 8]));
-#pragma unroll
-          for (int c = 16; c < kBN; c += 16)
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              mx8[x] = fmax3(mx8[x], __uint_as_float(s[c + x]), __uint_as_float(s[c + 8 + x]));
-          const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
-                                 fmaxf(mx8[6], mx8[7]));
-          const float m_new = mx * c_tile;
-          const bool raise = m_new > m_ref + kTau;
-          bool grown = false;  // the value exponent grew: O is held in units of 2^e_ref
-          float alpha = raise ? ex2_approx(m_ref - m_new) : 1.0f;
-          if (raise) {
-            l *= alpha;
-            lr *= alpha;
-            m_ref = m_new;
-          }
-          if constexpr (Q8) {
-            const int e = sm.scales[grp][ss].e;
-            grown = j > j0 && e > e_ref;
-            if (grown) alpha = e - e_ref > 126 ? 0.f : alpha * __int_as_float((127 + e_ref - e) << 23);
-            e_ref = e;
-          }
-          if (__any_sync(kFull, raise) || grown) {
-            if (j > j0) {
-              // the commit that signalled this S covers the group's previous P.V
+          const bool masked = k0 + kBN - 1 > all_hi || k0 < all_lo;
+          // A row is taken in halves, first for its maximum and then for its weights, in one rolled
+          // loop: the roles' code together has to stay in the instruction cache (unrolled, with the
+          // conversion beside it, every warp ran two to three times slower).  P lies over the second
+          // half of S, which is read last before it is overwritten.
+          float mx = -INFINITY, m_use = 0.f;
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(tO + c, o);
-                tmem_wait_ld();
+          for (int pass = 0; pass < 4; ++pass) {
+            const int half = pass == 1 || pass == 2;
+            uint32_t s[64];
+            tmem_ld32(tS + half * 64, s);
+            tmem_ld32(tS + half * 64 + 32, s + 32);
+            tmem_wait_ld();
+            if (masked) {
+              const int lim = vis_hi - k0 - half * 64, first = vis_lo - k0 - half * 64;
 #pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-                tmem_st32(tO + c, o);
+              for (int c = 0; c < 64; ++c)
+                if (c > lim || c < first) s[c] = __float_as_uint(-INFINITY);
+            }
+            if (pass < 2) {
+              float mx8[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) mx8[x] = fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 8]));
+#pragma unroll
+              for (int c = 16; c < 64; c += 16)
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                  mx8[x] = fmax3(mx8[x], __uint_as_float(s[c + x]), __uint_as_float(s[c + 8 + x]));
+              mx = fmaxf(mx, fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+              if (pass == 0) continue;
+              const float m_new = mx * c_tile;
+              const bool raise = m_new > m_ref + kTau;
+              bool grown = false;  // the value exponent grew: O is held in units of 2^e_ref
+              float alpha = raise ? ex2_approx(m_ref - m_new) : 1.0f;
+              if (raise) {
+                l *= alpha;
+                lr *= alpha;
+                m_ref = m_new;
               }
-              tmem_wait_st();
+              if constexpr (Q8) {
+                const int e = sm.scales[grp][ss].e;
+                grown = j > j0 && e > e_ref;
+                if (grown) alpha = e - e_ref > 126 ? 0.f : alpha * __int_as_float((127 + e_ref - e) << 23);
+                e_ref = e;
+              }
+              if ((__any_sync(kFull, raise) || grown) && j > j0) {
+                // the commit that signalled this S covers the group's previous P.V
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                  uint32_t o[32];
+                  tmem_ld32(tO + c, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                  tmem_st32(tO + c, o);
+                }
+                tmem_wait_st();
+              }
+              m_use = m_ref == -INFINITY ? 0.f : m_ref;
+            } else {
+              uint32_t p[32];
+              softmax_row<Q8 ? Elem::kF16 : E, 64>(s, p, c_tile, m_use, l, lr);
+              tmem_st32(tS + 64 + half * 32, p);
             }
           }
-          const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-          uint32_t p[kBN / 2];
-          softmax_row<Q8 ? Elem::kF16 : E>(s, p, c_tile, m_use, l, lr);
-#pragma unroll
-          for (int x = 0; x < kBN / 2; x += 32) tmem_st32(tS + x, p + x);
           tmem_wait_st();
         }
         tc_fence_before();
