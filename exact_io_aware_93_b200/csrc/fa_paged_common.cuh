@@ -29,6 +29,46 @@
 
 namespace fa {
 
+// Bounded waits, smaller than mbar_wait: these kernels have many and their code has to stay in
+// the instruction cache.  A wait that runs out (2 s) leaves its site in the CTA's abort flag,
+// which ends every other wait; the flag is reported once, when the CTA ends (pg_report).
+struct PgWait {
+  volatile int* abort_flag;
+  int site;
+};
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+// One warp waits for up to a barrier per lane (null: none) together: barriers that are ready cost
+// one round trip to shared memory, not one each.
+__device__ __forceinline__ bool pg_wait_lanes(uint64_t* bar, uint32_t parity, const PgWait& w) {
+  const uint32_t a = smem_u32(bar);
+  bool done = bar == nullptr;
+  const uint32_t t0 = globaltimer_lo();
+  while (true) {
+    if (!done) done = mbar_test(a, parity);
+    if (__all_sync(0xffffffffu, done)) return true;
+    bool stop = *w.abort_flag != 0;
+    if (globaltimer_lo() - t0 > static_cast<uint32_t>(FA_WAIT_TIMEOUT_NS)) {
+      if (!stop) *w.abort_flag = w.site;
+      stop = true;
+    }
+    if (__any_sync(0xffffffffu, stop)) return false;
+  }
+}
+__device__ __forceinline__ bool pg_wait(uint64_t* bar, uint32_t parity, const PgWait& w) {
+  return pg_wait_lanes(bar, parity, w);
+}
+// At the end of a CTA, after its last barrier: one thread.
+__device__ __forceinline__ void pg_report(const int* abort_flag, int* status) {
+  if (*abort_flag != 0) {
+    atomicCAS(status, 0, 6 /* FA_ERR_TIMEOUT */);
+    atomicCAS(status + 1, 0, *abort_flag);
+  }
+}
+
 struct PgArgs {
   const int* cu;          // [B + 1]
   const int* seqlens;     // [B]

@@ -210,31 +210,30 @@ __global__ void __launch_bounds__(384, 1)
   // Readers of the segment ring: the next segment, or null at the end or after an abort; a
   // reader gives the one it holds back first.
   uint32_t nseg = 0;
-  auto next_seg = [&](const WaitCtx& wc) -> const PgSeg* {
+  auto next_seg = [&](const PgWait& wc) -> const PgSeg* {
     if (nseg > 0) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.seg_empty[(nseg - 1) % NSEG]);
     }
     const int i = nseg % NSEG;
-    if (!__all_sync(kFull, mbar_wait(&sm.seg_full[i], (nseg / NSEG) & 1, wc))) return nullptr;
+    if (!pg_wait(&sm.seg_full[i], (nseg / NSEG) & 1, wc)) return nullptr;
     ++nseg;
     return sm.segs[i].nt > 0 ? &sm.segs[i] : nullptr;
   };
 
   if (warp == 8) {
     // ------------------------------------------------------------ schedule and TMA loads
-    const WaitCtx wc{&sm.abort_flag, status, 31};
+    const PgWait wc{&sm.abort_flag, 31};
     PgWalk<Cfg> w(a, sm.plan);
     PgSeg g;
     PgPages pages{};
     uint32_t it = 0, qcnt[2] = {0, 0};
     bool ok = true;
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, wc)); };
     while (ok) {
       const int i = nseg % NSEG;
       const bool more = w.next(a, g);
       if (more) pages.start(a, g, lane);
-      ok = wait_all(&sm.seg_empty[i], ((nseg / NSEG) & 1) ^ 1);
+      ok = pg_wait(&sm.seg_empty[i], ((nseg / NSEG) & 1) ^ 1, wc);
       if (!ok) break;
       if (lane == 0) {
         if (!more) g.nt = 0;
@@ -244,7 +243,7 @@ __global__ void __launch_bounds__(384, 1)
       const int qs = nseg & 1;
       ++nseg;
       if (!more) break;
-      ok = wait_all(&sm.q_empty[qs], (qcnt[qs] & 1) ^ 1);
+      ok = pg_wait(&sm.q_empty[qs], (qcnt[qs] & 1) ^ 1, wc);
       if (!ok) break;
       // a box of G heads x TQ tokens per chunk, or per piece
       constexpr int kBoxes = Q8 ? 2 : Cfg::kChunks;
@@ -259,7 +258,7 @@ __global__ void __launch_bounds__(384, 1)
       ++qcnt[qs];
       ok = pg_loads<Cfg::kAhead>(g, [&](bool isv, int j) -> bool {
         const int slot = it % NS;
-        if (!wait_all(&sm.kv_empty[slot], ((it / NS) & 1) ^ 1)) return false;
+        if (!pg_wait(&sm.kv_empty[slot], ((it / NS) & 1) ^ 1, wc)) return false;
         ++it;
         pg_load_tile<Cfg::kRowBytes, Cfg::kChunks>(a, g, pages, isv ? &tm_v : &tm_k, j, sm.kv[slot], &sm.kv_full[slot],
                                                    lane);
@@ -276,7 +275,7 @@ __global__ void __launch_bounds__(384, 1)
     __syncwarp();
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer (whole warp)
-    const WaitCtx wc{&sm.abort_flag, status, 32};
+    const PgWait wc{&sm.abort_flag, 32};
     // K, Q K-major; V MN-major, P K-major
     constexpr uint32_t idesc_s =
         Q8 ? idesc_kind_f8(128, Cfg::kNS, 0, 0, 0) : idesc_kind_f16(128, Cfg::kNS, 0, 0, ElemOps<E>::kMmaType);
@@ -320,7 +319,6 @@ __global__ void __launch_bounds__(384, 1)
                     (kk > 0) || acc);
       }
     };
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, wc)); };
     uint32_t it = 0, qcnt = 0, scnt = 0, pcnt[2] = {0, 0};
     bool ok = true;
     while (ok) {
@@ -329,51 +327,50 @@ __global__ void __launch_bounds__(384, 1)
       const PgSeg& g = *gp;
       const int nt = g.nt, kt0 = g.kt0;
       const int qs = (nseg - 1) & 1;
-      // Scores of tile t: its buffer was last read for tile t - 4, whose weights (posted after the
-      // read) the products of tile t - 4 have been waited for.
-      auto scores = [&](int t) {
-        const int slot = it % NS;
-        ++it;
-        const int buf = scnt % NB;
-        ++scnt;
-        issue_s(buf, qs, slot);
-        umma_commit_w(&sm.s_full[buf]);
-        umma_commit_w(&sm.kv_empty[slot]);
-        if (t == nt - 1) umma_commit_w(&sm.q_empty[qs]);
-      };
-      ok = mbar_wait_lanes(lane == 0 ? &sm.q_full[qs] : (lane == 1 ? &sm.kv_full[it % NS] : nullptr),
-                           lane == 0 ? (qcnt >> 1) & 1 : (it / NS) & 1, wc);
-      if (!ok) break;
-      ++qcnt;
-      tc_fence_after();
-      scores(0);
-      for (int t = 1; t < Cfg::kAhead && t < nt && ok; ++t) {
-        ok = __all_sync(kFull, mbar_wait(&sm.kv_full[it % NS], (it / NS) & 1, wc));
-        if (ok) scores(t);
-      }
-      for (int t = 0; t < nt && ok; ++t) {
+      // Step n issues the products of tile n - kAhead with its weights and the scores of tile n.
+      // A score buffer was last read for the tile four before, whose weights (posted after the
+      // read) have been waited for by then.
+      for (int n = 0; n < nt + Cfg::kAhead; ++n) {
+        const int t = n - Cfg::kAhead;
+        const bool pv = t >= 0, sc = n < nt;
         const int grp = t & 1;
-        const int slot = it % NS;  // V_t; K_{t + kAhead} follows
         const uint32_t p = grp ? pcnt[1] : pcnt[0];
-        const bool more = t + Cfg::kAhead < nt;
-        const bool cleans = pg_cleans(g, kt0 + t);
-        if (cleans) {
-          ok = __all_sync(kFull, mbar_wait(&sm.kv_full[slot], (it / NS) & 1, wc));
+        const uint32_t itk = it + pv;
+        // the ring's order is V_t, K_n
+        if (pv && pg_cleans(g, kt0 + t)) {
+          ok = pg_wait(&sm.kv_full[it % NS], (it / NS) & 1, wc);
           if (!ok) break;
-          pg_clean<Cfg::kRowBytes, Cfg::kChunks>(g, kt0 + t, sm.kv[slot], lane);
+          pg_clean<Cfg::kRowBytes, Cfg::kChunks>(g, kt0 + t, sm.kv[it % NS], lane);
         }
-        const uint32_t mine = it + (lane == 1);
-        ok = mbar_wait_lanes(lane < 1 + more ? &sm.kv_full[mine % NS] : (lane == 2 ? &sm.p_full[grp] : nullptr),
-                             lane == 2 ? p & 1 : (mine / NS) & 1, wc);
+        uint64_t* bar = nullptr;
+        uint32_t parity = 0;
+        if (lane == 0 && pv) bar = &sm.kv_full[it % NS], parity = (it / NS) & 1;
+        if (lane == 1 && pv) bar = &sm.p_full[grp], parity = p & 1;
+        if (lane == 2 && sc) bar = &sm.kv_full[itk % NS], parity = (itk / NS) & 1;
+        if (lane == 3 && n == 0) bar = &sm.q_full[qs], parity = (qcnt >> 1) & 1;
+        ok = pg_wait_lanes(bar, parity, wc);
         if (!ok) break;
-        ++it;
-        if (grp) ++pcnt[1]; else ++pcnt[0];
         tc_fence_after();
-        issue_pv(grp, slot, t >= 2);
-        umma_commit_w(&sm.p_empty[grp]);
-        umma_commit_w(&sm.kv_empty[slot]);
-        if (more) scores(t + Cfg::kAhead);
+        if (pv) {
+          if (grp) ++pcnt[1]; else ++pcnt[0];
+          const int slot = it % NS;
+          ++it;
+          issue_pv(grp, slot, t >= 2);
+          umma_commit_w(&sm.p_empty[grp]);
+          umma_commit_w(&sm.kv_empty[slot]);
+        }
+        if (sc) {
+          const int slot = it % NS;
+          ++it;
+          const int buf = scnt % NB;
+          ++scnt;
+          issue_s(buf, qs, slot);
+          umma_commit_w(&sm.s_full[buf]);
+          umma_commit_w(&sm.kv_empty[slot]);
+          if (n == nt - 1) umma_commit_w(&sm.q_empty[qs]);
+        }
       }
+      ++qcnt;
     }
     // Wait for every MMA issued to finish before the columns are freed.
     umma_commit_w(&sm.mma_drain);
@@ -383,7 +380,7 @@ __global__ void __launch_bounds__(384, 1)
     // ------------------------------------------------------------ scales of group warp - 10
     if constexpr (Q8) {
       const int grp = warp - 10;
-      const WaitCtx wc{&sm.abort_flag, status, 35};
+      const PgWait wc{&sm.abort_flag, 35};
       uint32_t cnt = 0;
       bool ok = true;
       while (ok) {
@@ -398,7 +395,7 @@ __global__ void __launch_bounds__(384, 1)
           if (j + 2 < jend) pg_fetch_scales(a, g, j + 2, lane, kn, vn);  // in flight over this tile
           e = max(e, pg_top(g, j, lane, vw));
           const int slot = cnt % NSC;
-          ok = __all_sync(kFull, mbar_wait(&sm.sc_empty[grp][slot], ((cnt / NSC) & 1) ^ 1, wc));
+          ok = pg_wait(&sm.sc_empty[grp][slot], ((cnt / NSC) & 1) ^ 1, wc);
           if (!ok) break;
           ++cnt;
           PfScales& sc = sm.scales[grp][slot];
@@ -419,21 +416,21 @@ __global__ void __launch_bounds__(384, 1)
     const int me = wq * 32 + lane;  // this thread's key of a tile
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tO = tbase + Cfg::kOCol + grp * Cfg::kNO + lane_off;
-    const WaitCtx wc{&sm.abort_flag, status, 33 + grp};
+    const PgWait wc{&sm.abort_flag, 33 + grp};
     uint8_t* const prow = sm.p[grp];
     uint32_t tiles = 0, mine = 0, gcnt = 0, xcnt = 0;  // score tiles, the group's, barriers passed
     bool ok = true;
     auto sync4 = [&]() -> bool {  // the group's warps
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.group[grp]);
-      const bool r = __all_sync(kFull, mbar_wait(&sm.group[grp], gcnt & 1, wc));
+      const bool r = pg_wait(&sm.group[grp], gcnt & 1, wc);
       ++gcnt;
       return r;
     };
     auto sync8 = [&]() -> bool {  // both groups
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.groups);
-      const bool r = __all_sync(kFull, mbar_wait(&sm.groups, xcnt & 1, wc));
+      const bool r = pg_wait(&sm.groups, xcnt & 1, wc);
       ++xcnt;
       return r;
     };
@@ -467,11 +464,20 @@ __global__ void __launch_bounds__(384, 1)
       bool first = true;
       for (int t = grp; t < nt; t += 2) {
         const int ss = mine % NSC;
+        const uint32_t tile = tiles + t;
+        const int buf = tile % NB;
+        // the scores, the scales, and the group's previous products: P^T may then be overwritten and
+        // O^T rescaled
+        ok = pg_wait_lanes(lane == 0   ? &sm.s_full[buf]
+                           : lane == 1 ? &sm.p_empty[grp]
+                           : Q8 && lane == 2 ? &sm.sc_full[grp][ss]
+                                             : nullptr,
+                           lane == 0 ? (tile / NB) & 1 : (lane == 1 ? (mine & 1) ^ 1 : (mine / NSC) & 1), wc);
+        if (!ok) break;
+        tc_fence_after();
         float kf = 1.f, vf = 1.f;
         int e = 0;
         if constexpr (Q8) {
-          ok = __all_sync(kFull, mbar_wait(&sm.sc_full[grp][ss], (mine / NSC) & 1, wc));
-          if (!ok) break;
           const PfScales& sc = sm.scales[grp][ss];
           e = sc.e;
           kf = e8m0_to_float(reinterpret_cast<const uint8_t*>(sc.k)[me]);
@@ -479,11 +485,6 @@ __global__ void __launch_bounds__(384, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.sc_empty[grp][ss]);
         }
-        const uint32_t tile = tiles + t;
-        const int buf = tile % NB;
-        ok = __all_sync(kFull, mbar_wait(&sm.s_full[buf], (tile / NB) & 1, wc));
-        if (!ok) break;
-        tc_fence_after();
         float x[RW];  // scores in log2 units
         {
           uint32_t s[Q8 ? 2 * RW : RW];
@@ -522,9 +523,6 @@ __global__ void __launch_bounds__(384, 1)
         ok = sync4();
         if (!ok) break;
         const uint32_t raised = *reinterpret_cast<const uint32_t*>(sm.flag[grp][mine & 1]);
-        // the group's previous product is complete: P^T may be overwritten, O^T rescaled
-        ok = __all_sync(kFull, mbar_wait(&sm.p_empty[grp], (mine & 1) ^ 1, wc));
-        if (!ok) break;
         if (raised) {
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
@@ -547,7 +545,6 @@ __global__ void __launch_bounds__(384, 1)
             alpha[r] *= shrink;
           }
           if (!first) {
-            tc_fence_after();
 #pragma unroll
             for (int c = 0; c < (Q8 ? 3 * RW : RW); c += 8) {
               uint32_t o[8];
@@ -623,7 +620,7 @@ __global__ void __launch_bounds__(384, 1)
         if (wq == 0 && lane == 0) sm.ref[grp][r] = Q8 ? ref[r] - kPShift : ref[r];
       }
       // the group's last product (none: passes at once)
-      ok = __all_sync(kFull, mbar_wait(&sm.p_empty[grp], (mine & 1) ^ 1, wc));
+      ok = pg_wait(&sm.p_empty[grp], (mine & 1) ^ 1, wc);
       if (!ok) break;
       tc_fence_after();
       if (Q8 && wq == 0 && lane == 0) sm.top[grp][0][0] = e8m0_to_float(static_cast<uint32_t>(e_ref + 127));
@@ -731,6 +728,7 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     tmem_dealloc(tbase, Cfg::kTmemCols);
   }
+  if (threadIdx.x == 0) pg_report(&sm.abort_flag, status);
 }
 
 }  // namespace fa

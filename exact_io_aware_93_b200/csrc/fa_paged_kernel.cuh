@@ -190,13 +190,13 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
   // Readers of the segment ring: the next segment, or null at the end or after an abort; a
   // reader gives the one it holds back first.
   uint32_t nseg = 0;
-  auto next_seg = [&](const WaitCtx& wc) -> const PgSeg* {
+  auto next_seg = [&](const PgWait& wc) -> const PgSeg* {
     if (nseg > 0) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.seg_empty[(nseg - 1) % NSEG]);
     }
     const int i = nseg % NSEG;
-    if (!__all_sync(kFull, mbar_wait(&sm.seg_full[i], (nseg / NSEG) & 1, wc))) return nullptr;
+    if (!pg_wait(&sm.seg_full[i], (nseg / NSEG) & 1, wc)) return nullptr;
     ++nseg;
     return sm.segs[i].nt > 0 ? &sm.segs[i] : nullptr;
   };
@@ -206,15 +206,14 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
     regs_set<Cfg::kLaunch, Cfg::kRegsOther>();
     if (warp == 8) {
       // ---------------------------------------------------------- schedule and TMA loads
-      const WaitCtx wc{&sm.abort_flag, status, 31};
+      const PgWait wc{&sm.abort_flag, 31};
       PgWalk<Cfg> w(a, sm.plan);
       PgSeg g;
       PgPages pages{};
       uint32_t it = 0, qcnt[2] = {0, 0};
       bool ok = true;
-      auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, wc)); };
       auto load_q = [&](int slot, int tok) -> bool {
-        if (!wait_all(&sm.q_empty[slot], (qcnt[slot] & 1) ^ 1)) return false;
+        if (!pg_wait(&sm.q_empty[slot], (qcnt[slot] & 1) ^ 1, wc)) return false;
         if (lane == 0)
           mbar_arrive_expect_tx(&sm.q_full[slot], static_cast<uint32_t>(Cfg::kChunks * 128 * G * a.TQ));
         __syncwarp();
@@ -229,7 +228,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
         const int i = nseg % NSEG;
         const bool more = w.next(a, g);
         if (more) pages.start(a, g, lane);
-        ok = wait_all(&sm.seg_empty[i], ((nseg / NSEG) & 1) ^ 1);
+        ok = pg_wait(&sm.seg_empty[i], ((nseg / NSEG) & 1) ^ 1, wc);
         if (!ok) break;
         if (lane == 0) {
           if (!more) g.nt = 0;
@@ -248,7 +247,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
         ok = pg_loads<2>(g, [&](bool isv, int j) -> bool {
           constexpr int N = Q8 ? Cfg::kRaw : NS;
           const int slot = it % N;
-          if (!wait_all(Q8 ? &sm.raw_empty[slot] : &sm.kv_empty[slot], ((it / N) & 1) ^ 1)) return false;
+          if (!pg_wait(Q8 ? &sm.raw_empty[slot] : &sm.kv_empty[slot], ((it / N) & 1) ^ 1, wc)) return false;
           ++it;
           if constexpr (Q8)
             pg_load_tile<D, 1>(a, g, pages, isv ? &tm_v : &tm_k, j, sm.raw[slot], &sm.raw_full[slot], lane);
@@ -268,7 +267,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
       __syncwarp();
     } else if (warp == 9) {
       // ---------------------------------------------------------- MMA issuer (whole warp)
-      const WaitCtx wc{&sm.abort_flag, status, 32};
+      const PgWait wc{&sm.abort_flag, 32};
       // Q, K K-major; P in TMEM, V MN-major
       constexpr uint32_t kType = Q8 ? 0 : ElemOps<E>::kMmaType;  // e4m3 pages: all operands fp16
       constexpr uint32_t idesc_s = idesc_kind_f16(128, kBN, 0, 0, kType);
@@ -292,118 +291,79 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
           umma_ts_w(tbase + Cfg::kOCol + i * D, tbase + i * 128 + 64 + kk * 8, dv + ((kk * 16 * 128) >> 4), idesc_o,
                     (kk > 0) || acc);
       };
-      auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, wc)); };
       uint32_t it = 0, qcnt[2] = {0, 0}, pcnt[2] = {0, 0};
       bool ok = true;
-      int slot = 0;
-      auto take = [&]() -> bool {
-        slot = it % NS;
-        const bool r = wait_all(&sm.kv_full[slot], (it / NS) & 1);
-        ++it;
-        return r;
-      };
       while (ok) {
         const PgSeg* gp = next_seg(wc);
         if (gp == nullptr) break;
         const PgSeg& g = *gp;
-        const int kt0 = g.kt0, nt = g.nt;
-        auto clean = [&](int sv, int j) {  // the conversion does it for e4m3 pages
-          if constexpr (!Q8) pg_clean<128, Cfg::kChunks>(g, j, sm.kv[sv], lane);
-        };
-        if (g.pair) {
-          const PgRange rg[2] = {g.tile[0], g.tile[1]};
-          const int jhi = kt0 + nt;
-          auto in = [&](int i, int j) { return j >= rg[i].lo && j < rg[i].hi; };
-          for (int i = 0; i < 2 && ok; ++i)
-            if (rg[i].hi > rg[i].lo) ok = wait_all(&sm.q_full[i], qcnt[i] & 1);
-          if (!ok) break;
-          ok = take();
-          if (!ok) break;
-          tc_fence_after();
-          for (int i = 0; i < 2; ++i) {
-            if (!in(i, kt0)) continue;
-            issue_s(i, i, slot);
-            umma_commit_w(&sm.s_full[i]);
-            if (rg[i].hi == kt0 + 1) umma_commit_w(&sm.q_empty[i]);
-          }
-          umma_commit_w(&sm.kv_empty[slot]);
-          for (int j = kt0; j < jhi && ok; ++j) {
-            ok = take();
-            if (!ok) break;
-            const int sv = slot;
-            clean(sv, j);
-            int skn = -1;
-            // K_{j+1}: with three slots of converted tiles it is not there before V_{j-1}'s is free
-            if (!Q8 && j + 1 < jhi) {
-              ok = take();
-              if (!ok) break;
-              skn = slot;
-            }
-            for (int i = 0; i < 2 && ok; ++i) {
-              if (in(i, j)) {
-                ok = wait_all(&sm.p_full[i], pcnt[i] & 1);
-                if (!ok) break;
-                ++pcnt[i];
-                tc_fence_after();
-                issue_pv(i, sv, j > rg[i].lo);
-                if (j + 1 == rg[i].hi) umma_commit_w(&sm.o_done[i]);
-              }
-              if (Q8 && i == 1) umma_commit_w(&sm.kv_empty[sv]);
-              if (Q8 && i == 0 && j + 1 < jhi) {
-                ok = take();
-                if (!ok) break;
-                tc_fence_after();
-                skn = slot;
-              }
-              if (in(i, j + 1)) {
-                issue_s(i, i, skn);
-                umma_commit_w(&sm.s_full[i]);
-                if (j + 2 == rg[i].hi) umma_commit_w(&sm.q_empty[i]);
-              }
-            }
-            if (!ok) break;
-            if (!Q8) umma_commit_w(&sm.kv_empty[sv]);
-            if (skn >= 0) umma_commit_w(&sm.kv_empty[skn]);
-          }
-          for (int i = 0; i < 2; ++i)
-            if (rg[i].hi > rg[i].lo) ++qcnt[i];
+        const bool pair = g.pair;
+        const int kt0 = g.kt0, kend = g.kt0 + g.nt;
+        // group i's key tiles: all of its range, or every other one
+        const PgRange rg0 = pair ? g.tile[0] : PgRange{kt0, kend}, rg1 = pair ? g.tile[1] : rg0;
+        if (pair) {
+          uint64_t* q = lane == 0 && rg0.hi > rg0.lo ? &sm.q_full[0] : (lane == 1 && rg1.hi > rg1.lo ? &sm.q_full[1] : nullptr);
+          ok = pg_wait_lanes(q, (lane ? qcnt[1] : qcnt[0]) & 1, wc);
         } else {
-          ok = wait_all(&sm.q_full[0], qcnt[0] & 1);
-          if (!ok) break;
-          ++qcnt[0];
-          tc_fence_after();
-          for (int t = 0; t < 2 && t < nt && ok; ++t) {
-            ok = take();
-            if (!ok) break;
-            tc_fence_after();
-            issue_s(t, 0, slot);
-            umma_commit_w(&sm.s_full[t]);
-            umma_commit_w(&sm.kv_empty[slot]);
-            if (t == nt - 1) umma_commit_w(&sm.q_empty[0]);
-          }
-          for (int t = 0; t < nt && ok; ++t) {
-            const int i = t & 1;
-            ok = take();
-            if (!ok) break;
-            clean(slot, kt0 + t);
-            ok = wait_all(&sm.p_full[i], (i ? pcnt[1] : pcnt[0]) & 1);
-            if (!ok) break;
-            if (i) ++pcnt[1]; else ++pcnt[0];
-            tc_fence_after();
-            issue_pv(i, slot, t >= 2);
-            umma_commit_w(&sm.kv_empty[slot]);
-            if (t + 2 >= nt) umma_commit_w(&sm.o_done[i]);
-            if (t + 2 < nt) {
-              ok = take();
+          ok = pg_wait(&sm.q_full[0], qcnt[0] & 1, wc);
+        }
+        if (!ok) break;
+        // Step n: the products of group i = n mod 2 with the values of tile j, then its scores of
+        // tile js (pair: j + 1, two steps per tile that share the slots; split: j + 2).
+        int sv = -1, sk = -1;
+        const int steps = pair ? 2 * (g.nt + 1) : g.nt + 2;
+        for (int n = 0; n < steps; ++n) {
+          const int i = n & 1;
+          const int j = pair ? kt0 - 1 + (n >> 1) : kt0 - 2 + n;
+          const int js = pair ? j + 1 : j + 2;
+          const PgRange r = i ? rg1 : rg0;
+          const bool pv = j >= r.lo && j < r.hi, sc = js >= r.lo && js < r.hi;
+          const bool fresh = !pair || i == 0;  // this step takes its tiles from the ring
+          if (fresh) {
+            sv = sk = -1;
+            if (j >= kt0) sv = it % NS;
+            const uint32_t itk = it + (j >= kt0);
+            if (js < kend) sk = itk % NS;
+            if (!Q8 && sv >= 0 && pg_cleans(g, j)) {
+              ok = pg_wait(&sm.kv_full[sv], (it / NS) & 1, wc);
               if (!ok) break;
-              tc_fence_after();
-              issue_s(i, 0, slot);
-              umma_commit_w(&sm.s_full[i]);
-              umma_commit_w(&sm.kv_empty[slot]);
-              if (t + 2 == nt - 1) umma_commit_w(&sm.q_empty[0]);
+              pg_clean<128, Cfg::kChunks>(g, j, sm.kv[sv], lane);
             }
           }
+          // with a ring of three converted tiles K_{j+1} is not there before V_{j-1}'s slot is free:
+          // it is waited for after the products
+          const uint32_t itv = it, itk = it + (j >= kt0);
+          uint64_t* bar = nullptr;
+          uint32_t parity = 0;
+          if (lane == 0 && fresh && sv >= 0) bar = &sm.kv_full[sv], parity = (itv / NS) & 1;
+          if (lane == 1 && pv) bar = &sm.p_full[i], parity = (i ? pcnt[1] : pcnt[0]) & 1;
+          if (!Q8 && lane == 2 && fresh && sk >= 0) bar = &sm.kv_full[sk], parity = (itk / NS) & 1;
+          ok = pg_wait_lanes(bar, parity, wc);
+          if (!ok) break;
+          tc_fence_after();
+          if (pv) {
+            if (i) ++pcnt[1]; else ++pcnt[0];
+            issue_pv(i, sv, j - (pair ? 1 : 2) >= r.lo);
+            if (pair ? j + 1 == r.hi : j + 2 >= r.hi) umma_commit_w(&sm.o_done[i]);
+          }
+          const bool last = !pair || i == 1;  // the slots' last use
+          if (last && sv >= 0) umma_commit_w(&sm.kv_empty[sv]);
+          if (Q8 && fresh && sk >= 0) {
+            ok = pg_wait(&sm.kv_full[sk], (itk / NS) & 1, wc);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          if (sc) {
+            issue_s(i, pair ? i : 0, sk);
+            umma_commit_w(&sm.s_full[i]);
+            if (js + 1 == r.hi) umma_commit_w(&sm.q_empty[pair ? i : 0]);
+          }
+          if (last && sk >= 0) umma_commit_w(&sm.kv_empty[sk]);
+          if (fresh) it += (sv >= 0) + (sk >= 0);
         }
+        if (!ok) break;
+        if (rg0.hi > rg0.lo) ++qcnt[0];
+        if (pair && rg1.hi > rg1.lo) ++qcnt[1];
       }
       // Wait for every MMA issued to finish before the columns are freed.
       umma_commit_w(&sm.mma_drain);
@@ -413,7 +373,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
       // ---------------------------------------------------------- scales
       // Warp 10 gives each softmax group its tiles' exponents, warp 11 the conversion the factors
       // of every row; both follow every tile, so that they agree on the value exponent.
-      const WaitCtx wc{&sm.abort_flag, status, 35};
+      const PgWait wc{&sm.abort_flag, 35};
       uint32_t cnt[2] = {0, 0};
       bool ok = true;
       while (ok) {
@@ -433,7 +393,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
             for (int grp = 0; grp < 2; ++grp) {
               if (!(g.pair ? j >= g.tile[grp].lo && j < g.tile[grp].hi : ((j - g.kt0) & 1) == grp)) continue;
               const int slot = cnt[grp] % NSC;
-              ok = __all_sync(kFull, mbar_wait(&sm.sc_empty[grp][slot], ((cnt[grp] / NSC) & 1) ^ 1, wc));
+              ok = pg_wait(&sm.sc_empty[grp][slot], ((cnt[grp] / NSC) & 1) ^ 1, wc);
               if (!ok) break;
               ++cnt[grp];
               if (lane == 0) {
@@ -459,7 +419,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
             if (isv) e = max(e, top);
             const int ref = max(isv ? e : top, -127);
             const int slot = cnt[0] % NSC;
-            if (!__all_sync(kFull, mbar_wait(&sm.fac_empty[slot], ((cnt[0] / NSC) & 1) ^ 1, wc))) return false;
+            if (!pg_wait(&sm.fac_empty[slot], ((cnt[0] / NSC) & 1) ^ 1, wc)) return false;
             ++cnt[0];
             uint32_t f[4];
 #pragma unroll
@@ -486,7 +446,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
     // ------------------------------------------------------------ codes to fp16 tiles
     if constexpr (Q8) {
       regs_set<Cfg::kLaunch, Cfg::kRegsOther>();
-      const WaitCtx wc{&sm.abort_flag, status, 36};
+      const PgWait wc{&sm.abort_flag, 36};
       constexpr int L = D / 16;          // threads per row
       constexpr int kStep = 128 / L;     // rows per pass
       constexpr int U = 4;
@@ -508,9 +468,11 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
         const PgSeg& g = *gp;
         ok = pg_loads<2>(g, [&](bool isv, int j) -> bool {
           const int rs = it % Cfg::kRaw, ks = it % NS, fs = it % NSC;
-          if (!__all_sync(kFull, mbar_wait(&sm.fac_full[fs], (it / NSC) & 1, wc)) ||
-              !__all_sync(kFull, mbar_wait(&sm.raw_full[rs], (it / Cfg::kRaw) & 1, wc)) ||
-              !__all_sync(kFull, mbar_wait(&sm.kv_empty[ks], ((it / NS) & 1) ^ 1, wc)))
+          if (!pg_wait_lanes(lane == 0   ? &sm.fac_full[fs]
+                             : lane == 1 ? &sm.raw_full[rs]
+                             : lane == 2 ? &sm.kv_empty[ks]
+                                         : nullptr,
+                             lane == 0 ? (it / NSC) & 1 : (lane == 1 ? (it / Cfg::kRaw) & 1 : ((it / NS) & 1) ^ 1), wc))
             return false;
           ++it;
           uint8_t* dst = sm.kv[ks] + (item >> 2) * Cfg::kChunkBytes;
@@ -565,7 +527,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tbase + grp * 128 + lane_off;
     const uint32_t tO = tbase + Cfg::kOCol + grp * D + lane_off;
-    const WaitCtx wc{&sm.abort_flag, status, 33 + grp};
+    const PgWait wc{&sm.abort_flag, 33 + grp};
     uint32_t scnt = 0, ocnt = 0, gcnt = 0;  // scnt also counts the group's scale entries
     bool ok = true;
     while (ok) {
@@ -601,11 +563,8 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
       float m_ref = -INFINITY, l = 0.f, lr = 0.f;
       for (int j = j0; j < j1; j += dj) {
         const int ss = scnt % NSC;
-        if constexpr (Q8) {
-          ok = __all_sync(kFull, mbar_wait(&sm.sc_full[grp][ss], (scnt / NSC) & 1, wc));
-          if (!ok) break;
-        }
-        ok = __all_sync(kFull, mbar_wait(&sm.s_full[grp], scnt & 1, wc));
+        ok = pg_wait_lanes(lane == 0 ? &sm.s_full[grp] : (Q8 && lane == 1 ? &sm.sc_full[grp][ss] : nullptr),
+                           lane == 0 ? scnt & 1 : (scnt / NSC) & 1, wc);
         if (!ok) break;
         ++scnt;
         tc_fence_after();
@@ -691,7 +650,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
       float unit = 1.0f;  // of O
       if constexpr (Q8) unit = e8m0_to_float(static_cast<uint32_t>(e_ref + 127));
       if (any) {
-        ok = __all_sync(kFull, mbar_wait(&sm.o_done[grp], ocnt & 1, wc));
+        ok = pg_wait(&sm.o_done[grp], ocnt & 1, wc);
         if (!ok) break;
         ++ocnt;
         tc_fence_after();
@@ -736,66 +695,49 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
           *reinterpret_cast<float2*>(a.part_lse + (part0 + rc) * 2) = make_float2(lse_l, lse_r);
         }
       };
-      if (pair) {
-        // O normalised by the sum of the rounded weights, and the log-sums of both
-        const float inv = lr == 0.f ? 0.f : unit / lr;
-        if (rows_here) {
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            if (any) {
-              tmem_ld32(tO + c, o);
-              tmem_wait_ld();
-            }
-            float v[32];
-#pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] = lr == 0.f ? 0.f : __uint_as_float(o[x]) * inv;
-            if (real) put(rc, c, v);
-          }
-          if (real) put_lse(m_ref, l, lr);
-        }
-      } else {
-        // Join the groups: weights 2^(m_k - max m) / sum of lr, group 1's columns handed over through
-        // shared memory
-        auto sync_groups = [&]() -> bool {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.groups);
-          const bool r = __all_sync(kFull, mbar_wait(&sm.groups, gcnt & 1, wc));
-          ++gcnt;
-          return r;
-        };
-        constexpr int SC = Cfg::kStageCols;
-        constexpr int kUnits = SC / 4;  // 16-byte units of a staged row; unit u sits at u ^ key(row)
-        auto key = [](int r) { return (r >> 1) & (kUnits - 1); };
+      // Weight of this group's O: a tile's own (pair: normalised by the sum of the rounded weights),
+      // or its share of the two groups' (split: 2^(m_k - max m) / sum of lr, group 1's columns handed
+      // over through shared memory).
+      auto sync_groups = [&]() -> bool {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.groups);
+        const bool r = pg_wait(&sm.groups, gcnt & 1, wc);
+        ++gcnt;
+        return r;
+      };
+      constexpr int SC = Cfg::kStageCols;
+      constexpr int kUnits = SC / 4;  // 16-byte units of a staged row; unit u sits at u ^ key(row)
+      auto key = [](int r) { return (r >> 1) & (kUnits - 1); };
+      if (!pair) {
         if (real) sm.stat[grp][rc] = make_float3(m_ref, l, lr);
         ok = sync_groups();
         if (!ok) break;
-        float mm = -INFINITY, ls = 0.f, lrs = 0.f, wgt = 0.f;
-        if (real) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) mm = fmaxf(mm, sm.stat[k][rc].x);
-          const float ref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float3 st = sm.stat[k][rc];
-            const float e = ex2_approx(st.x - ref);
-            ls += e * st.y;
-            lrs += e * st.z;
-          }
-          wgt = (lr == 0.f || lrs == 0.f) ? 0.f : ex2_approx(m_ref - ref) * unit / lrs;
-          if (grp == 0) put_lse(ref, ls, lrs);
-        }
+      }
+      float mm = m_ref, ls = l, lrs = lr, wgt = 1.f;
+      if (!pair && real) {
+        const float3 st = sm.stat[grp ^ 1][rc];
+        mm = fmaxf(m_ref, st.x);
+        const float ref = mm == -INFINITY ? 0.f : mm;
+        const float mine = ex2_approx(m_ref - ref), other = ex2_approx(st.x - ref);
+        // the same order in both groups
+        ls = grp == 0 ? mine * l + other * st.y : other * st.y + mine * l;
+        lrs = grp == 0 ? mine * lr + other * st.z : other * st.z + mine * lr;
+        wgt = mine;
+      }
+      wgt = lr == 0.f || lrs == 0.f ? 0.f : wgt * unit / lrs;
+      if (real && (pair || grp == 0)) put_lse(mm, ls, lrs);
 #pragma unroll 1
-        for (int c = 0; c < D; c += SC) {
-          float* stage = sm.stage[(c / SC) % Cfg::kStageBufs];
-          uint32_t o[SC];
-          float v[SC];
-          if (any && rows_here) {
-            tmem_ld16(tO + c, o);
-            tmem_wait_ld();
-          }
+      for (int c = 0; c < D; c += SC) {
+        float* stage = sm.stage[(c / SC) % Cfg::kStageBufs];
+        uint32_t o[SC];
+        float v[SC];
+        if (any && rows_here) {
+          tmem_ld16(tO + c, o);
+          tmem_wait_ld();
+        }
 #pragma unroll
-          for (int x = 0; x < SC; ++x) v[x] = lr == 0.f ? 0.f : __uint_as_float(o[x]) * wgt;
+        for (int x = 0; x < SC; ++x) v[x] = wgt == 0.f ? 0.f : __uint_as_float(o[x]) * wgt;
+        if (!pair) {
           if (real && grp == 1) {
 #pragma unroll
             for (int x = 0; x < kUnits; ++x)
@@ -804,7 +746,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
           }
           ok = sync_groups();
           if (!ok) break;
-          if (grp == 0 && real) {
+          if (real && grp == 0) {
 #pragma unroll
             for (int x = 0; x < kUnits; ++x) {
               const float4 y = *reinterpret_cast<const float4*>(stage + rc * SC + ((x ^ key(rc)) << 2));
@@ -813,15 +755,15 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
               v[4 * x + 2] += y.z;
               v[4 * x + 3] += y.w;
             }
-            put(rc, c, v);
-          }
-          if (Cfg::kStageBufs == 1) {  // with two buffers the next barrier says that one is free
-            ok = sync_groups();
-            if (!ok) break;
           }
         }
-        if (!ok) break;
+        if (real && (pair || grp == 0)) put(rc, c, v);
+        if (!pair && Cfg::kStageBufs == 1) {  // with two buffers the next barrier says that one is free
+          ok = sync_groups();
+          if (!ok) break;
+        }
       }
+      if (!ok) break;
       tc_fence_before();
     }
   }
@@ -832,6 +774,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tbase, Cfg::kTmemCols);
   }
+  if (threadIdx.x == 0) pg_report(&sm.abort_flag, status);
 }
 
 }  // namespace fa
