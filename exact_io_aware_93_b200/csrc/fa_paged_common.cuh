@@ -46,12 +46,15 @@ __device__ __forceinline__ uint32_t globaltimer_lo() {
 __device__ __forceinline__ bool pg_wait_lanes(uint64_t* bar, uint32_t parity, const PgWait& w) {
   const uint32_t a = smem_u32(bar);
   bool done = bar == nullptr;
-  const uint32_t t0 = globaltimer_lo();
-  while (true) {
+  uint32_t t0 = 0;
+  for (uint32_t spins = 0;; ++spins) {
     if (!done) done = mbar_test(a, parity);
     if (__all_sync(0xffffffffu, done)) return true;
+    if (spins % 64 != 63) continue;  // the timer is slow to read
+    const uint32_t now = globaltimer_lo();
+    if (spins == 63) t0 = now;
     bool stop = *w.abort_flag != 0;
-    if (globaltimer_lo() - t0 > static_cast<uint32_t>(FA_WAIT_TIMEOUT_NS)) {
+    if (now - t0 > static_cast<uint32_t>(FA_WAIT_TIMEOUT_NS)) {
       if (!stop) *w.abort_flag = w.site;
       stop = true;
     }
@@ -345,40 +348,86 @@ struct PgPages {
 template <int kRowBytes, int kChunks>
 __device__ __forceinline__ void pg_load_tile(const PgArgs& a, const PgSeg& g, PgPages& pages, const CUtensorMap* map,
                                              int j, uint8_t* dst, uint64_t* full, int lane) {
-  const int box = min(128, a.page);         // keys per box
+  const int bs = min(7, a.page_shift);      // box: 1 << bs keys
   const int p0 = (j << 7) >> a.page_shift;  // the tile's first page
-  const int k0 = max(g.keys.lo - (j << 7), 0) / box;
-  const int k1 = (min(g.keys.hi - (j << 7), 128) + box - 1) / box;
-  if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>((k1 - k0) * box * kRowBytes * kChunks));
-  __syncwarp();
+  const int k0 = max(g.keys.lo - (j << 7), 0) >> bs;
+  const int k1 = (min(g.keys.hi - (j << 7), 128) + (1 << bs) - 1) >> bs;
   const int k = k0 + lane / kChunks, c = lane % kChunks;
   const int id = pages.get(a, g, p0, k, lane);
+  if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(((k1 - k0) << bs) * kRowBytes * kChunks));
+  __syncwarp();
   if (k < k1) {
-    const int row = (j << 7) & (a.page - 1) & ~(box - 1);  // inside a page of 256
+    const int row = (j << 7) & (a.page - 1) & ~((1 << bs) - 1);  // inside a page of 256
     const bool good = id >= 0 && id < a.P;
     if (!good) plan_fail(a.status, 44);
     // a bad page number reads as zeros: a coordinate past the pool
-    if (FA_IN_BOUNDS(row + box <= a.page && p0 + k < a.max_pages && k * box < 128, a.status, 502))
-      tma_load_3d(dst + c * 128 * kRowBytes + k * box * kRowBytes, map, full, c * 64, row,
+    if (FA_IN_BOUNDS(row + (1 << bs) <= a.page && p0 + k < a.max_pages && (k << bs) < 128, a.status, 502))
+      tma_load_3d(dst + c * 128 * kRowBytes + (k << bs) * kRowBytes, map, full, c * 64, row,
                   good ? id * a.H_kv + g.kvh : a.P * a.H_kv);
   }
   __syncwarp();
 }
 
-// The scale bytes of a lane's four keys of tile j; 2^0 for keys the unit does not see.
-__device__ __forceinline__ void pg_fetch_scales(const PgArgs& a, const PgSeg& g, int j, int lane, uint32_t& kw,
-                                                uint32_t& vw) {
-  kw = vw = 0x7f7f7f7fu;
-  const int key = (j << 7) + lane * 4;
-  if (key + 3 < g.keys.lo || key >= g.keys.hi) return;
-  const int pg = key >> a.page_shift;
-  const int id = pg < a.max_pages ? __ldg(a.table + static_cast<int64_t>(g.b) * a.max_pages + pg) : -1;
-  if (id < 0 || id >= a.P) return;
-  const int64_t at = (static_cast<int64_t>(id) * a.H_kv + g.kvh) * a.page + (key & (a.page - 1));
-  if (!FA_IN_BOUNDS(at >= 0 && at + 4 <= static_cast<int64_t>(a.P) * a.H_kv * a.page, a.status, 511)) return;
-  kw = __ldg(reinterpret_cast<const uint32_t*>(a.k_scales + at));
-  vw = __ldg(reinterpret_cast<const uint32_t*>(a.v_scales + at));
-}
+// A loading warp's copies in flight: the ring slots it filled last and their phases.  After an
+// abort it waits (bounded) for them before the CTA exits.
+struct PgInFlight {
+  uint32_t slots = 0, phases = 0;
+  __device__ __forceinline__ void add(int slot, uint32_t phase) {
+    slots |= 1u << slot;
+    phases = (phases & ~(1u << slot)) | (phase << slot);
+  }
+  __device__ __forceinline__ void drain(uint64_t* full, int* status) const {
+    for (uint32_t left = slots; left; left &= left - 1) {
+      const int slot = __ffs(left) - 1;
+      mbar_wait_drain(full + slot, (phases >> slot) & 1, status);
+    }
+  }
+};
+
+// The scale bytes of a lane's four keys of every tile of a segment in turn, fetched four tiles
+// ahead: a fetch is two dependent reads of global memory.
+struct PgScaleStream {
+  uint32_t k[4], v[4], nk[4], nv[4];
+  // the bytes of the lane's four keys of tile j; 2^0 for keys the unit does not see
+  __device__ __forceinline__ static void fetch(const PgArgs& a, const PgSeg& g, int j, int lane, uint32_t& kw,
+                                               uint32_t& vw) {
+    kw = vw = 0x7f7f7f7fu;
+    const int key = (j << 7) + lane * 4;
+    if (key + 3 < g.keys.lo || key >= g.keys.hi) return;
+    const int pg = key >> a.page_shift;
+    const int id = pg < a.max_pages ? __ldg(a.table + static_cast<int64_t>(g.b) * a.max_pages + pg) : -1;
+    if (id < 0 || id >= a.P) return;
+    const int64_t at = (static_cast<int64_t>(id) * a.H_kv + g.kvh) * a.page + (key & (a.page - 1));
+    if (!FA_IN_BOUNDS(at >= 0 && at + 4 <= static_cast<int64_t>(a.P) * a.H_kv * a.page, a.status, 511)) return;
+    kw = __ldg(reinterpret_cast<const uint32_t*>(a.k_scales + at));
+    vw = __ldg(reinterpret_cast<const uint32_t*>(a.v_scales + at));
+  }
+  // f(tile, key bytes, value bytes) for every tile; returns false to stop.
+  template <typename F>
+  __device__ __forceinline__ bool run(const PgArgs& a, const PgSeg& g, int lane, F f) {
+    const int jend = g.kt0 + g.nt;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (g.kt0 + x < jend) fetch(a, g, g.kt0 + x, lane, nk[x], nv[x]);
+    for (int j0 = g.kt0; j0 < jend; j0 += 4) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        k[x] = nk[x];
+        v[x] = nv[x];
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (j0 + 4 + x < jend) fetch(a, g, j0 + 4 + x, lane, nk[x], nv[x]);
+#pragma unroll 1
+      for (int x = 0; x < 4 && j0 + x < jend; ++x) {
+        const uint32_t kw = x == 0 ? k[0] : (x == 1 ? k[1] : (x == 2 ? k[2] : k[3]));
+        const uint32_t vw = x == 0 ? v[0] : (x == 1 ? v[1] : (x == 2 ? v[2] : v[3]));
+        if (!f(j0 + x, kw, vw)) return false;
+      }
+    }
+    return true;
+  }
+};
 
 // The largest exponent of a tile's scale bytes (NaN apart) over the keys the unit sees, or -1000.
 __device__ __forceinline__ int pg_top(const PgSeg& g, int j, int lane, uint32_t w) {

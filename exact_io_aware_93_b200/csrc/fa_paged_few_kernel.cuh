@@ -30,8 +30,9 @@
 // (The rows-first form of this kernel took 187 us for 16 sequences of 16-32K tokens; it waited for
 // its softmax and its products in turn.)
 //
-// Warp roles (384 threads): warps 0-3 and 4-7 the softmax groups, warp 8 the schedule and the TMA
-// loads, warp 9 the MMA issuer, warps 10 and 11 the scales of groups 0 and 1.
+// Warp roles (384 threads): warps 0-3 and 4-7 the softmax groups, warp 8 the schedule and the loads
+// of Q and K, warp 10 those of V (one warp for both took 700 cycles a load and bounded the kernel),
+// warp 9 the MMA issuer, warp 11 the scales.
 #pragma once
 
 #include "fa_paged_common.cuh"
@@ -67,7 +68,7 @@ struct PfCfg {
   static constexpr int kStages = (Q8 ? (RW == 32 ? 10 : 12) : (RW == 32 ? 5 : 6)) * (128 / D);
   static constexpr int kScaleRing = 4;
   static constexpr int kSegRing = 4;
-  static constexpr int kSegReaders = 9 + (Q8 ? 2 : 0);  // warps
+  static constexpr int kSegReaders = 10 + (Q8 ? 1 : 0);  // warps
   static constexpr uint32_t kOCol = kSBufs * kNS;
   static constexpr uint32_t kCols = kOCol + 2 * kNO;
   static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512);
@@ -227,6 +228,7 @@ __global__ void __launch_bounds__(384, 1)
     PgWalk<Cfg> w(a, sm.plan);
     PgSeg g;
     PgPages pages{};
+    PgInFlight flight;
     uint32_t it = 0, qcnt[2] = {0, 0};
     bool ok = true;
     while (ok) {
@@ -258,20 +260,44 @@ __global__ void __launch_bounds__(384, 1)
       ++qcnt[qs];
       ok = pg_loads<Cfg::kAhead>(g, [&](bool isv, int j) -> bool {
         const int slot = it % NS;
-        if (!pg_wait(&sm.kv_empty[slot], ((it / NS) & 1) ^ 1, wc)) return false;
+        const uint32_t phase = (it / NS) & 1;
         ++it;
-        pg_load_tile<Cfg::kRowBytes, Cfg::kChunks>(a, g, pages, isv ? &tm_v : &tm_k, j, sm.kv[slot], &sm.kv_full[slot],
-                                                   lane);
+        if (isv) return true;
+        if (!pg_wait(&sm.kv_empty[slot], phase ^ 1, wc)) return false;
+        flight.add(slot, phase);
+        pg_load_tile<Cfg::kRowBytes, Cfg::kChunks>(a, g, pages, &tm_k, j, sm.kv[slot], &sm.kv_full[slot], lane);
         return true;
       });
     }
     if (!ok && lane == 0) {
-      // Unwinding: wait (bounded) for the copies still in flight before the CTA exits.
-      for (uint32_t idx = (it > static_cast<uint32_t>(NS) ? it - NS : 0); idx < it; ++idx)
-        mbar_wait_drain(&sm.kv_full[idx % NS], (idx / NS) & 1, status);
+      flight.drain(sm.kv_full, status);
       for (int i = 0; i < 2; ++i)
         if (qcnt[i] > 0) mbar_wait_drain(&sm.q_full[i], (qcnt[i] - 1) & 1, status);
     }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ loads of V
+    const PgWait wc{&sm.abort_flag, 37};
+    PgPages pages{};
+    PgInFlight flight;
+    uint32_t it = 0;
+    bool ok = true;
+    while (ok) {
+      const PgSeg* gp = next_seg(wc);
+      if (gp == nullptr) break;
+      pages.start(a, *gp, lane);
+      ok = pg_loads<Cfg::kAhead>(*gp, [&](bool isv, int j) -> bool {
+        const int slot = it % NS;
+        const uint32_t phase = (it / NS) & 1;
+        ++it;
+        if (!isv) return true;
+        if (!pg_wait(&sm.kv_empty[slot], phase ^ 1, wc)) return false;
+        flight.add(slot, phase);
+        pg_load_tile<Cfg::kRowBytes, Cfg::kChunks>(a, *gp, pages, &tm_v, j, sm.kv[slot], &sm.kv_full[slot], lane);
+        return true;
+      });
+    }
+    if (sm.abort_flag != 0 && lane == 0) flight.drain(sm.kv_full, status);
     __syncwarp();
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer (whole warp)
@@ -376,37 +402,34 @@ __global__ void __launch_bounds__(384, 1)
     umma_commit_w(&sm.mma_drain);
     mbar_wait_drain(&sm.mma_drain, 0, status);
     __syncwarp();
-  } else if (warp >= 10) {
-    // ------------------------------------------------------------ scales of group warp - 10
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ scales
     if constexpr (Q8) {
-      const int grp = warp - 10;
       const PgWait wc{&sm.abort_flag, 35};
-      uint32_t cnt = 0;
+      PgScaleStream stream;
+      uint32_t cnt[2] = {0, 0};
       bool ok = true;
       while (ok) {
         const PgSeg* gp = next_seg(wc);
         if (gp == nullptr) break;
         const PgSeg& g = *gp;
-        const int jend = g.kt0 + g.nt;
-        int e = -1000;
-        uint32_t kw = 0, vw = 0, kn = 0, vn = 0;
-        if (g.kt0 + grp < jend) pg_fetch_scales(a, g, g.kt0 + grp, lane, kw, vw);
-        for (int j = g.kt0 + grp; j < jend; j += 2) {
-          if (j + 2 < jend) pg_fetch_scales(a, g, j + 2, lane, kn, vn);  // in flight over this tile
-          e = max(e, pg_top(g, j, lane, vw));
-          const int slot = cnt % NSC;
-          ok = pg_wait(&sm.sc_empty[grp][slot], ((cnt / NSC) & 1) ^ 1, wc);
-          if (!ok) break;
-          ++cnt;
+        int e0 = -127, e1 = -127;  // of each group's tiles
+        ok = stream.run(a, g, lane, [&](int j, uint32_t kw, uint32_t vw) -> bool {
+          const int grp = (j - g.kt0) & 1;
+          const int e = max(grp ? e1 : e0, pg_top(g, j, lane, vw));
+          if (grp) e1 = e; else e0 = e;
+          const uint32_t c = grp ? cnt[1] : cnt[0];
+          const int slot = c % NSC;
+          if (!pg_wait(&sm.sc_empty[grp][slot], ((c / NSC) & 1) ^ 1, wc)) return false;
+          if (grp) ++cnt[1]; else ++cnt[0];
           PfScales& sc = sm.scales[grp][slot];
           sc.k[lane] = kw;
           sc.v[lane] = vw;
-          if (lane == 0) sc.e = max(e, -127);
+          if (lane == 0) sc.e = e;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.sc_full[grp][slot]);
-          kw = kn;
-          vw = vn;
-        }
+          return true;
+        });
       }
     }
   } else {

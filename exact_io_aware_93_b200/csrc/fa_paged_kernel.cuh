@@ -20,8 +20,8 @@
 // memory beside operands that already saturate it.)
 //
 // Warp roles (384 threads, 512 with e4m3 pages): warps 0-3 and 4-7 the softmax groups, warp 8 the
-// schedule and the TMA loads, warp 9 the MMA issuer, warps 10-11 the scales, warps 12-15 the
-// conversion.
+// schedule and the loads of Q and K, warp 10 those of V, warp 9 the MMA issuer, warp 11 the scales,
+// warps 12-15 the conversion.
 // Tensor memory: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [256+D,256+2D); P
 // overwrites the second half of S.
 #pragma once
@@ -58,7 +58,7 @@ struct PgCfg {
   static constexpr int kRawBytes = Q8 ? 128 * D : 16;
   static constexpr int kScaleRing = 4;
   static constexpr int kSegRing = 4;
-  static constexpr int kSegReaders = Q8 ? 15 : 9;     // warps
+  static constexpr int kSegReaders = Q8 ? 15 : 10;    // warps
   static constexpr uint32_t kOCol = 256;
   static constexpr uint32_t kTmemCols = 512;
 };
@@ -88,7 +88,7 @@ struct __align__(1024) PgSmem {
   uint8_t kv[Cfg::kStages][Cfg::kTileBytes];
   uint8_t raw[Cfg::kRaw][Cfg::kRawBytes];
   alignas(16) float stage[Cfg::kStageBufs][128 * Cfg::kStageCols];  // a split segment's columns being joined
-  alignas(16) uint32_t factors[Q8 ? Cfg::kScaleRing : 1][128];      // fp16, twice
+  alignas(16) uint32_t factors[Q8 ? Cfg::kScaleRing : 1][2][128];   // of K's and V's rows: fp16, twice
   PgTileScale scales[2][Cfg::kScaleRing];                           // of each softmax group's tiles
   float3 stat[2][128];                                              // m, l, lr of a split segment's groups
   PgSeg segs[Cfg::kSegRing];
@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
       PgWalk<Cfg> w(a, sm.plan);
       PgSeg g;
       PgPages pages{};
+      PgInFlight flight;
       uint32_t it = 0, qcnt[2] = {0, 0};
       bool ok = true;
       auto load_q = [&](int slot, int tok) -> bool {
@@ -247,23 +248,51 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
         ok = pg_loads<2>(g, [&](bool isv, int j) -> bool {
           constexpr int N = Q8 ? Cfg::kRaw : NS;
           const int slot = it % N;
-          if (!pg_wait(Q8 ? &sm.raw_empty[slot] : &sm.kv_empty[slot], ((it / N) & 1) ^ 1, wc)) return false;
+          const uint32_t phase = (it / N) & 1;
           ++it;
+          if (isv) return true;
+          if (!pg_wait(Q8 ? &sm.raw_empty[slot] : &sm.kv_empty[slot], phase ^ 1, wc)) return false;
+          flight.add(slot, phase);
           if constexpr (Q8)
-            pg_load_tile<D, 1>(a, g, pages, isv ? &tm_v : &tm_k, j, sm.raw[slot], &sm.raw_full[slot], lane);
+            pg_load_tile<D, 1>(a, g, pages, &tm_k, j, sm.raw[slot], &sm.raw_full[slot], lane);
           else
-            pg_load_tile<128, Cfg::kChunks>(a, g, pages, isv ? &tm_v : &tm_k, j, sm.kv[slot], &sm.kv_full[slot], lane);
+            pg_load_tile<128, Cfg::kChunks>(a, g, pages, &tm_k, j, sm.kv[slot], &sm.kv_full[slot], lane);
           return true;
         });
       }
       if (!ok && lane == 0) {
-        // Unwinding: wait (bounded) for the copies still in flight before the CTA exits.
-        constexpr uint32_t N = Q8 ? Cfg::kRaw : NS;
-        for (uint32_t idx = (it > N ? it - N : 0); idx < it; ++idx)
-          mbar_wait_drain(Q8 ? &sm.raw_full[idx % N] : &sm.kv_full[idx % N], (idx / N) & 1, status);
+        flight.drain(Q8 ? sm.raw_full : sm.kv_full, status);
         for (int i = 0; i < 2; ++i)
           if (qcnt[i] > 0) mbar_wait_drain(&sm.q_full[i], (qcnt[i] - 1) & 1, status);
       }
+      __syncwarp();
+    } else if (warp == 10) {
+      // ---------------------------------------------------------- loads of V
+      const PgWait wc{&sm.abort_flag, 37};
+      PgPages pages{};
+      PgInFlight flight;
+      uint32_t it = 0;
+      bool ok = true;
+      while (ok) {
+        const PgSeg* gp = next_seg(wc);
+        if (gp == nullptr) break;
+        pages.start(a, *gp, lane);
+        ok = pg_loads<2>(*gp, [&](bool isv, int j) -> bool {
+          constexpr int N = Q8 ? Cfg::kRaw : NS;
+          const int slot = it % N;
+          const uint32_t phase = (it / N) & 1;
+          ++it;
+          if (!isv) return true;
+          if (!pg_wait(Q8 ? &sm.raw_empty[slot] : &sm.kv_empty[slot], phase ^ 1, wc)) return false;
+          flight.add(slot, phase);
+          if constexpr (Q8)
+            pg_load_tile<D, 1>(a, *gp, pages, &tm_v, j, sm.raw[slot], &sm.raw_full[slot], lane);
+          else
+            pg_load_tile<128, Cfg::kChunks>(a, *gp, pages, &tm_v, j, sm.kv[slot], &sm.kv_full[slot], lane);
+          return true;
+        });
+      }
+      if (sm.abort_flag != 0 && lane == 0) flight.drain(Q8 ? sm.raw_full : sm.kv_full, status);
       __syncwarp();
     } else if (warp == 9) {
       // ---------------------------------------------------------- MMA issuer (whole warp)
@@ -371,75 +400,48 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
       __syncwarp();
     } else if constexpr (Q8) {
       // ---------------------------------------------------------- scales
-      // Warp 10 gives each softmax group its tiles' exponents, warp 11 the conversion the factors
-      // of every row; both follow every tile, so that they agree on the value exponent.
       const PgWait wc{&sm.abort_flag, 35};
-      uint32_t cnt[2] = {0, 0};
+      PgScaleStream stream;
+      uint32_t tiles = 0, cnt[2] = {0, 0};
       bool ok = true;
       while (ok) {
         const PgSeg* gp = next_seg(wc);
         if (gp == nullptr) break;
         const PgSeg& g = *gp;
-        const int jend = g.kt0 + g.nt;
-        if (warp == 10) {
-          int e = -1000;
-          uint32_t kw, vw, kn = 0, vn = 0;
-          pg_fetch_scales(a, g, g.kt0, lane, kw, vw);
-          for (int j = g.kt0; j < jend && ok; ++j) {
-            if (j + 1 < jend) pg_fetch_scales(a, g, j + 1, lane, kn, vn);  // in flight over this tile
-            const int top = pg_top(g, j, lane, kw);
-            e = max(e, pg_top(g, j, lane, vw));
+        int e = -127;
+        ok = stream.run(a, g, lane, [&](int j, uint32_t kw, uint32_t vw) -> bool {
+          const int top = max(pg_top(g, j, lane, kw), -127);
+          e = max(e, pg_top(g, j, lane, vw));
+          // the conversion's factors of the tile's rows
+          const int fs = tiles % NSC;
+          if (!pg_wait(&sm.fac_empty[fs], ((tiles / NSC) & 1) ^ 1, wc)) return false;
+          ++tiles;
 #pragma unroll
-            for (int grp = 0; grp < 2; ++grp) {
-              if (!(g.pair ? j >= g.tile[grp].lo && j < g.tile[grp].hi : ((j - g.kt0) & 1) == grp)) continue;
-              const int slot = cnt[grp] % NSC;
-              ok = pg_wait(&sm.sc_empty[grp][slot], ((cnt[grp] / NSC) & 1) ^ 1, wc);
-              if (!ok) break;
-              ++cnt[grp];
-              if (lane == 0) {
-                sm.scales[grp][slot] = PgTileScale{e8m0_to_float(static_cast<uint32_t>(max(top, -127) + 127)), max(e, -127)};
-                mbar_arrive(&sm.sc_full[grp][slot]);
-              }
-              __syncwarp();
-            }
-            kw = kn;
-            vw = vn;
-          }
-        } else {
-          // the loads' order: K_j, V_j, or K_0, K_1, V_0, K_2, ..  A tile's words are fetched once
-          // and kept until its values are due, two tiles later at most
-          int e = -1000;
-          uint32_t kw[3] = {0, 0, 0}, vw[3] = {0, 0, 0};
-          pg_fetch_scales(a, g, g.kt0, lane, kw[0], vw[0]);
-          if (g.nt > 1) pg_fetch_scales(a, g, g.kt0 + 1, lane, kw[1], vw[1]);
-          ok = pg_loads<2>(g, [&](bool isv, int j) -> bool {
-            const int t = (j - g.kt0) % 3;
-            const uint32_t w = t == 0 ? (isv ? vw[0] : kw[0]) : (t == 1 ? (isv ? vw[1] : kw[1]) : (isv ? vw[2] : kw[2]));
-            const int top = pg_top(g, j, lane, w);
-            if (isv) e = max(e, top);
-            const int ref = max(isv ? e : top, -127);
-            const int slot = cnt[0] % NSC;
-            if (!pg_wait(&sm.fac_empty[slot], ((cnt[0] / NSC) & 1) ^ 1, wc)) return false;
-            ++cnt[0];
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t w = kv ? vw : kw;
             uint32_t f[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) f[x] = pg_factor16((w >> (8 * x)) & 255, ref) * 0x10001u;
-            *reinterpret_cast<uint4*>(sm.factors[slot] + lane * 4) = make_uint4(f[0], f[1], f[2], f[3]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.fac_full[slot]);
-            if (isv && j + 2 < jend) {  // V_j done: its place takes tile j + 3's, fetched ahead of K_{j+3}
-              if (j + 3 < jend) {
-                uint32_t x, y;
-                pg_fetch_scales(a, g, j + 3, lane, x, y);
-                if (t == 0) kw[0] = x, vw[0] = y;
-                else if (t == 1) kw[1] = x, vw[1] = y;
-                else kw[2] = x, vw[2] = y;
-              }
+            for (int x = 0; x < 4; ++x) f[x] = pg_factor16((w >> (8 * x)) & 255, kv ? e : top) * 0x10001u;
+            *reinterpret_cast<uint4*>(sm.factors[fs][kv] + lane * 4) = make_uint4(f[0], f[1], f[2], f[3]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.fac_full[fs]);
+          // each softmax group's exponents of its tiles
+#pragma unroll 1
+          for (int grp = 0; grp < 2; ++grp) {
+            if (!(g.pair ? j >= g.tile[grp].lo && j < g.tile[grp].hi : ((j - g.kt0) & 1) == grp)) continue;
+            const uint32_t c = grp ? cnt[1] : cnt[0];
+            const int slot = c % NSC;
+            if (!pg_wait(&sm.sc_empty[grp][slot], ((c / NSC) & 1) ^ 1, wc)) return false;
+            if (grp) ++cnt[1]; else ++cnt[0];
+            if (lane == 0) {
+              sm.scales[grp][slot] = PgTileScale{e8m0_to_float(static_cast<uint32_t>(top + 127)), e};
+              mbar_arrive(&sm.sc_full[grp][slot]);
             }
-            if (!isv && j == g.kt0 && g.nt > 2) pg_fetch_scales(a, g, j + 2, lane, kw[2], vw[2]);
-            return true;
-          });
-        }
+            __syncwarp();
+          }
+          return true;
+        });
       }
     }
   } else if (Q8 && warp >= 12) {
@@ -460,19 +462,21 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
       const int in_unit = D == 128 ? item ^ (r0 & 7) : item ^ ((r0 >> 1) & 3);
       const int odd = (item >> 2) & 1;
       const int first = ((item & 3) * 2 + odd) ^ (r0 & 7), second = ((item & 3) * 2 + 1 - odd) ^ (r0 & 7);
-      uint32_t it = 0;
+      uint32_t it = 0, tiles = 0;
       bool ok = true;
       while (ok) {
         const PgSeg* gp = next_seg(wc);
         if (gp == nullptr) break;
         const PgSeg& g = *gp;
         ok = pg_loads<2>(g, [&](bool isv, int j) -> bool {
-          const int rs = it % Cfg::kRaw, ks = it % NS, fs = it % NSC;
+          const int rs = it % Cfg::kRaw, ks = it % NS;
+          const uint32_t tile = tiles + (j - g.kt0);
+          const int fs = tile % NSC;
           if (!pg_wait_lanes(lane == 0   ? &sm.fac_full[fs]
                              : lane == 1 ? &sm.raw_full[rs]
                              : lane == 2 ? &sm.kv_empty[ks]
                                          : nullptr,
-                             lane == 0 ? (it / NSC) & 1 : (lane == 1 ? (it / Cfg::kRaw) & 1 : ((it / NS) & 1) ^ 1), wc))
+                             lane == 0 ? (tile / NSC) & 1 : (lane == 1 ? (it / Cfg::kRaw) & 1 : ((it / NS) & 1) ^ 1), wc))
             return false;
           ++it;
           uint8_t* dst = sm.kv[ks] + (item >> 2) * Cfg::kChunkBytes;
@@ -483,7 +487,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               c[u] = *reinterpret_cast<const uint4*>(sm.raw[rs] + (base + u * kStep) * D + in_unit * 16);
-              f[u] = sm.factors[fs][base + u * kStep];
+              f[u] = sm.factors[fs][isv][base + u * kStep];
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -511,10 +515,11 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
           if (lane == 0) {
             mbar_arrive(&sm.kv_full[ks]);
             mbar_arrive(&sm.raw_empty[rs]);
-            mbar_arrive(&sm.fac_empty[fs]);
+            if (isv) mbar_arrive(&sm.fac_empty[fs]);  // K_j came before
           }
           return true;
         });
+        tiles += g.nt;
       }
     }
   } else {
@@ -573,19 +578,21 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
           float c_tile = c_row;
           if constexpr (Q8) c_tile *= sm.scales[grp][ss].k;
           const bool masked = k0 + kBN - 1 > all_hi || k0 < all_lo;
-          // A row is taken in halves, first for its maximum and then for its weights, in one rolled
-          // loop: the roles' code together has to stay in the instruction cache (unrolled, with the
-          // conversion beside it, every warp ran two to three times slower).  P lies over the second
-          // half of S, which is read last before it is overwritten.
+          // A row is taken in halves, first for its maximum and then for its weights.  With e4m3 pages
+          // in one rolled loop: the roles' code together has to stay in the instruction cache
+          // (unrolled, with the conversion beside it, every warp ran two to three times slower).  P
+          // lies over the second half of S, which is read last before it is overwritten.
           float mx = -INFINITY, m_use = 0.f;
-#pragma unroll 1
+          uint32_t s[64];
+#pragma unroll(Q8 ? 1 : 4)
           for (int pass = 0; pass < 4; ++pass) {
             const int half = pass == 1 || pass == 2;
-            uint32_t s[64];
-            tmem_ld32(tS + half * 64, s);
-            tmem_ld32(tS + half * 64 + 32, s + 32);
-            tmem_wait_ld();
-            if (masked) {
+            if (Q8 || pass != 2) {  // unrolled, the second half is still at hand
+              tmem_ld32(tS + half * 64, s);
+              tmem_ld32(tS + half * 64 + 32, s + 32);
+              tmem_wait_ld();
+            }
+            if (masked && (Q8 || pass != 2)) {
               const int lim = vis_hi - k0 - half * 64, first = vis_lo - k0 - half * 64;
 #pragma unroll
               for (int c = 0; c < 64; ++c)

@@ -483,7 +483,7 @@ fa_status fa_get_status(void* stream);
  * fa_get_status, and in *site (if not NULL) where the first recorded error arose: for
  * FA_ERR_TIMEOUT the wait that ran out (forward: 1 loads, 2 MMA, 3 and 4 the softmax of the
  * first and second query block; backward: 11 loads, 12 MMA, 13 key rows, 14 dQ drain;
- * decode: 21 loads, 22 MMA, 23 softmax; paged attention: 31 loads, 32 MMA, 33 and 34 the softmax
+ * decode: 21 loads, 22 MMA, 23 softmax; paged attention: 31 and 37 loads, 32 MMA, 33 and 34 the softmax
  * groups, 35 the scales and 36 the conversion of e4m3 pages; 98 the final wait for issued MMAs or a wait while
  * unwinding after an abort; 99 the self-test),
  * for FA_ERR_PLAN the reader (41 fa_cache_append, 42 fa_cache_gather, 43 and 44 fa_paged: its
