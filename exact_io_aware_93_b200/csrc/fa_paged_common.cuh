@@ -344,10 +344,13 @@ struct PgPages {
   }
 };
 
-// Issues the boxes of key tile j that hold a key of the unit (whole warp; the slot is free).
+// Issues the boxes of key tile j that hold a key of the unit (whole warp; the slot is free).  With
+// `scales` also the tile's scale bytes, keys' and then values': every lane's arrive on their own
+// barrier.
 template <int kRowBytes, int kChunks>
 __device__ __forceinline__ void pg_load_tile(const PgArgs& a, const PgSeg& g, PgPages& pages, const CUtensorMap* map,
-                                             int j, uint8_t* dst, uint64_t* full, int lane) {
+                                             int j, uint8_t* dst, uint64_t* full, int lane, uint8_t* scales = nullptr,
+                                             uint64_t* scales_full = nullptr) {
   const int bs = min(7, a.page_shift);      // box: 1 << bs keys
   const int p0 = (j << 7) >> a.page_shift;  // the tile's first page
   const int k0 = max(g.keys.lo - (j << 7), 0) >> bs;
@@ -364,6 +367,19 @@ __device__ __forceinline__ void pg_load_tile(const PgArgs& a, const PgSeg& g, Pg
     if (FA_IN_BOUNDS(row + (1 << bs) <= a.page && p0 + k < a.max_pages && (k << bs) < 128, a.status, 502))
       tma_load_3d(dst + c * 128 * kRowBytes + (k << bs) * kRowBytes, map, full, c * 64, row,
                   good ? id * a.H_kv + g.kvh : a.P * a.H_kv);
+  }
+  if (scales) {
+    // four keys per lane, which lie in one page; keys that the unit does not see are left out
+    const int key = (j << 7) + lane * 4;
+    const int pg = pages.get(a, g, p0, (lane * 4) >> a.page_shift, lane);
+    if (key + 3 >= g.keys.lo && key < g.keys.hi && pg >= 0 && pg < a.P) {
+      const int64_t at = (static_cast<int64_t>(pg) * a.H_kv + g.kvh) * a.page + (key & (a.page - 1));
+      if (FA_IN_BOUNDS(at >= 0 && at + 4 <= static_cast<int64_t>(a.P) * a.H_kv * a.page, a.status, 513)) {
+        cp_async4(scales + lane * 4, a.k_scales + at);
+        cp_async4(scales + 128 + lane * 4, a.v_scales + at);
+      }
+    }
+    cp_async_arrive(scales_full);
   }
   __syncwarp();
 }

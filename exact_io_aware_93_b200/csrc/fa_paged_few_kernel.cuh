@@ -26,13 +26,14 @@
 //       and not e4m3 for its range: a long tail of small weights beside a large one keeps its
 //       mass.  The pieces are rows of P^T, their products columns of O^T, added at the end.
 //   scales  a key's 2^ek and 2^(ev - E) are one number each for its thread; E is the largest
-//       value exponent of the group's tiles so far (O^T is rescaled when it grows).
+//       value exponent of the group's tiles so far (O^T is rescaled when it grows).  The bytes
+//       come with the K tile, into a ring of their own that the softmax groups free.
 // (The rows-first form of this kernel took 187 us for 16 sequences of 16-32K tokens; it waited for
 // its softmax and its products in turn.)
 //
 // Warp roles (384 threads): warps 0-3 and 4-7 the softmax groups, warp 8 the schedule and the loads
 // of Q and K, warp 10 those of V (one warp for both took 700 cycles a load and bounded the kernel),
-// warp 9 the MMA issuer, warp 11 the scales.
+// warp 9 the MMA issuer, warp 11 idle.
 #pragma once
 
 #include "fa_paged_common.cuh"
@@ -66,21 +67,13 @@ struct PfCfg {
   static constexpr int kPChunkBytes = kNO * 128;
   static constexpr int kPBytes = kPChunks * kPChunkBytes;
   static constexpr int kStages = (Q8 ? (RW == 32 ? 10 : 12) : (RW == 32 ? 5 : 6)) * (128 / D);
-  static constexpr int kScaleRing = 4;
+  static constexpr int kScaleRing = 8;  // key tiles
   static constexpr int kSegRing = 4;
-  static constexpr int kSegReaders = 10 + (Q8 ? 1 : 0);  // warps
+  static constexpr int kSegReaders = 10;  // warps
   static constexpr uint32_t kOCol = kSBufs * kNS;
   static constexpr uint32_t kCols = kOCol + 2 * kNO;
   static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512);
   static_assert(kCols <= 512 && RW % 8 == 0, "tensor memory");
-};
-
-// Scale bytes of one key tile and the largest value exponent so far.
-struct PfScales {
-  uint32_t k[32];
-  uint32_t v[32];
-  int e;
-  int pad[3];
 };
 
 template <int D, bool Q8, int RW>
@@ -90,19 +83,20 @@ struct __align__(1024) PfSmem {
   uint8_t q[2][Cfg::kQBytes];
   uint8_t p[2][Cfg::kPBytes];               // each group's P^T
   alignas(16) float part[RW][D];            // group 1's O on its way to group 0
-  PfScales scales[2][Q8 ? Cfg::kScaleRing : 1];
+  alignas(16) uint8_t scales[Q8 ? Cfg::kScaleRing : 1][2][128];  // a key tile's, of keys and values
   float2 sums[2][4][RW];                    // l, lr of each group's warps
   float ref[2][RW];                         // each group's reference maxima
   float weight[2][RW];                      // of each group's O in the result
   float top[2][4][RW];                      // maxima of a group's warps, when one is raised
-  uint8_t flag[2][2][4];                    // tiles' parity: does a warp want to raise
+  alignas(16) int flag[2][2][4];            // by tiles' parity, of a group's warps: does one want to
+                                            // raise a maximum (bit 0), and its largest value exponent
   PgSeg segs[Cfg::kSegRing];
   uint64_t q_full[2];
   uint64_t q_empty[2];
   uint64_t kv_full[Cfg::kStages];
   uint64_t kv_empty[Cfg::kStages];
-  uint64_t sc_full[2][Cfg::kScaleRing];
-  uint64_t sc_empty[2][Cfg::kScaleRing];
+  uint64_t sc_full[Cfg::kScaleRing];
+  uint64_t sc_empty[Cfg::kScaleRing];
   uint64_t seg_full[Cfg::kSegRing];
   uint64_t seg_empty[Cfg::kSegRing];
   uint64_t s_full[Cfg::kSBufs];
@@ -165,12 +159,10 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&sm.p_full[i], 4);
       mbar_init(&sm.p_empty[i], 1);
       mbar_init(&sm.group[i], 4);
-      if constexpr (Q8) {
-        for (int s = 0; s < NSC; ++s) {
-          mbar_init(&sm.sc_full[i][s], 1);
-          mbar_init(&sm.sc_empty[i][s], 4);
-        }
-      }
+    }
+    for (int s = 0; s < NSC; ++s) {
+      mbar_init(&sm.sc_full[s], 32);
+      mbar_init(&sm.sc_empty[s], 4);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&sm.kv_full[s], 1);
@@ -229,7 +221,7 @@ __global__ void __launch_bounds__(384, 1)
     PgSeg g;
     PgPages pages{};
     PgInFlight flight;
-    uint32_t it = 0, qcnt[2] = {0, 0};
+    uint32_t it = 0, tiles = 0, qcnt[2] = {0, 0};
     bool ok = true;
     while (ok) {
       const int i = nseg % NSEG;
@@ -263,9 +255,19 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t phase = (it / NS) & 1;
         ++it;
         if (isv) return true;
-        if (!pg_wait(&sm.kv_empty[slot], phase ^ 1, wc)) return false;
+        const int ss = tiles % NSC;
+        const uint32_t sphase = (tiles / NSC) & 1;
+        if (!pg_wait_lanes(lane == 0 ? &sm.kv_empty[slot] : (Q8 && lane == 1 ? &sm.sc_empty[ss] : nullptr),
+                           (lane == 0 ? phase : sphase) ^ 1, wc))
+          return false;
+        ++tiles;
         flight.add(slot, phase);
-        pg_load_tile<Cfg::kRowBytes, Cfg::kChunks>(a, g, pages, &tm_k, j, sm.kv[slot], &sm.kv_full[slot], lane);
+        if constexpr (Q8) {
+          pg_load_tile<Cfg::kRowBytes, 1>(a, g, pages, &tm_k, j, sm.kv[slot], &sm.kv_full[slot], lane, sm.scales[ss][0],
+                                          &sm.sc_full[ss]);
+        } else {
+          pg_load_tile<Cfg::kRowBytes, Cfg::kChunks>(a, g, pages, &tm_k, j, sm.kv[slot], &sm.kv_full[slot], lane);
+        }
         return true;
       });
     }
@@ -274,6 +276,7 @@ __global__ void __launch_bounds__(384, 1)
       for (int i = 0; i < 2; ++i)
         if (qcnt[i] > 0) mbar_wait_drain(&sm.q_full[i], (qcnt[i] - 1) & 1, status);
     }
+    if constexpr (Q8) cp_async_wait_all();
     __syncwarp();
   } else if (warp == 10) {
     // ------------------------------------------------------------ loads of V
@@ -402,37 +405,7 @@ __global__ void __launch_bounds__(384, 1)
     umma_commit_w(&sm.mma_drain);
     mbar_wait_drain(&sm.mma_drain, 0, status);
     __syncwarp();
-  } else if (warp == 11) {
-    // ------------------------------------------------------------ scales
-    if constexpr (Q8) {
-      const PgWait wc{&sm.abort_flag, 35};
-      PgScaleStream stream;
-      uint32_t cnt[2] = {0, 0};
-      bool ok = true;
-      while (ok) {
-        const PgSeg* gp = next_seg(wc);
-        if (gp == nullptr) break;
-        const PgSeg& g = *gp;
-        int e0 = -127, e1 = -127;  // of each group's tiles
-        ok = stream.run(a, g, lane, [&](int j, uint32_t kw, uint32_t vw) -> bool {
-          const int grp = (j - g.kt0) & 1;
-          const int e = max(grp ? e1 : e0, pg_top(g, j, lane, vw));
-          if (grp) e1 = e; else e0 = e;
-          const uint32_t c = grp ? cnt[1] : cnt[0];
-          const int slot = c % NSC;
-          if (!pg_wait(&sm.sc_empty[grp][slot], ((c / NSC) & 1) ^ 1, wc)) return false;
-          if (grp) ++cnt[1]; else ++cnt[0];
-          PfScales& sc = sm.scales[grp][slot];
-          sc.k[lane] = kw;
-          sc.v[lane] = vw;
-          if (lane == 0) sc.e = e;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.sc_full[grp][slot]);
-          return true;
-        });
-      }
-    }
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ softmax groups
     const int grp = warp >> 2;
     const int wq = warp & 3;
@@ -486,27 +459,28 @@ __global__ void __launch_bounds__(384, 1)
       int e_ref = 0;
       bool first = true;
       for (int t = grp; t < nt; t += 2) {
-        const int ss = mine % NSC;
         const uint32_t tile = tiles + t;
-        const int buf = tile % NB;
+        const int buf = tile % NB, ss = tile % NSC;
         // the scores, the scales, and the group's previous products: P^T may then be overwritten and
         // O^T rescaled
         ok = pg_wait_lanes(lane == 0   ? &sm.s_full[buf]
                            : lane == 1 ? &sm.p_empty[grp]
-                           : Q8 && lane == 2 ? &sm.sc_full[grp][ss]
+                           : Q8 && lane == 2 ? &sm.sc_full[ss]
                                              : nullptr,
-                           lane == 0 ? (tile / NB) & 1 : (lane == 1 ? (mine & 1) ^ 1 : (mine / NSC) & 1), wc);
+                           lane == 0 ? (tile / NB) & 1 : (lane == 1 ? (mine & 1) ^ 1 : (tile / NSC) & 1), wc);
         if (!ok) break;
         tc_fence_after();
-        float kf = 1.f, vf = 1.f;
-        int e = 0;
+        float kf = 1.f;
+        int vb = 0, e = -127;  // the key's value scale byte, the largest exponent of the warp's keys
         if constexpr (Q8) {
-          const PfScales& sc = sm.scales[grp][ss];
-          e = sc.e;
-          kf = e8m0_to_float(reinterpret_cast<const uint8_t*>(sc.k)[me]);
-          vf = pg_factor(reinterpret_cast<const uint8_t*>(sc.v)[me], e);
+          kf = e8m0_to_float(sm.scales[ss][0][me]);
+          vb = sm.scales[ss][1][me];
+          const int key = ((kt0 + t) << 7) + me;
+          const bool in = key >= g.keys.lo && key < g.keys.hi;  // stale bytes may be anything
+          if (!in) vb = 127;
+          e = __reduce_max_sync(kFull, in && vb != 255 ? vb - 127 : -127);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.sc_empty[grp][ss]);
+          if (lane == 0) mbar_arrive(&sm.sc_empty[ss]);
         }
         float x[RW];  // scores in log2 units
         {
@@ -533,19 +507,22 @@ __global__ void __launch_bounds__(384, 1)
             if (key > hi || key < lo) x[r] = -INFINITY;
             if (++h == G) h = 0, ++i;
           }
-          if constexpr (Q8) {
-            if (key >= g.keys.hi || key < g.keys.lo) vf = 0.f;  // a stale scale may be NaN
-          }
         }
         bool raise = false;
 #pragma unroll
         for (int r = 0; r < RW; ++r) raise = raise || (r < M && x[r] > ref[r] + kTau);
-        const bool grown = Q8 && !first && e > e_ref;
         const bool any = __any_sync(kFull, raise);
-        if (lane == 0) sm.flag[grp][mine & 1][wq] = any || grown;
+        if (lane == 0) sm.flag[grp][mine & 1][wq] = e * 2 + any;
         ok = sync4();
         if (!ok) break;
-        const uint32_t raised = *reinterpret_cast<const uint32_t*>(sm.flag[grp][mine & 1]);
+        const int4 flags = *reinterpret_cast<const int4*>(sm.flag[grp][mine & 1]);
+        bool raised = (flags.x | flags.y | flags.z | flags.w) & 1, grown = false;
+        if constexpr (Q8) {
+          e = max(max(flags.x, flags.y), max(flags.z, flags.w)) >> 1;
+          if (!first) e = max(e, e_ref);
+          grown = !first && e > e_ref;
+          raised = raised || grown;
+        }
         if (raised) {
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
@@ -581,6 +558,7 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
         e_ref = e;
+        const float vf = Q8 ? pg_factor(vb, e) : 1.f;
         // weights, and their place in P^T: row r, this thread's key
         if constexpr (Q8) {
           const uint32_t at = me & 15;

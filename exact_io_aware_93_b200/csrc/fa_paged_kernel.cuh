@@ -328,7 +328,6 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
         const PgSeg& g = *gp;
         const bool pair = g.pair;
         const int kt0 = g.kt0, kend = g.kt0 + g.nt;
-        // group i's key tiles: all of its range, or every other one
         const PgRange rg0 = pair ? g.tile[0] : PgRange{kt0, kend}, rg1 = pair ? g.tile[1] : rg0;
         if (pair) {
           uint64_t* q = lane == 0 && rg0.hi > rg0.lo ? &sm.q_full[0] : (lane == 1 && rg1.hi > rg1.lo ? &sm.q_full[1] : nullptr);
@@ -337,58 +336,91 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
           ok = pg_wait(&sm.q_full[0], qcnt[0] & 1, wc);
         }
         if (!ok) break;
-        // Step n: the products of group i = n mod 2 with the values of tile j, then its scores of
-        // tile js (pair: j + 1, two steps per tile that share the slots; split: j + 2).
-        int sv = -1, sk = -1;
-        const int steps = pair ? 2 * (g.nt + 1) : g.nt + 2;
-        for (int n = 0; n < steps; ++n) {
-          const int i = n & 1;
-          const int j = pair ? kt0 - 1 + (n >> 1) : kt0 - 2 + n;
-          const int js = pair ? j + 1 : j + 2;
-          const PgRange r = i ? rg1 : rg0;
-          const bool pv = j >= r.lo && j < r.hi, sc = js >= r.lo && js < r.hi;
-          const bool fresh = !pair || i == 0;  // this step takes its tiles from the ring
-          if (fresh) {
-            sv = sk = -1;
-            if (j >= kt0) sv = it % NS;
-            const uint32_t itk = it + (j >= kt0);
-            if (js < kend) sk = itk % NS;
-            if (!Q8 && sv >= 0 && pg_cleans(g, j)) {
+        if (pair) {
+          // per key tile: PV_0(j), S_0(j+1), PV_1(j), S_1(j+1); the first round has scores only
+          for (int j = kt0 - 1; j < kend; ++j) {
+            const bool v = j >= kt0, k = j + 1 < kend;
+            const uint32_t itk = it + v;
+            const int sv = it % NS, sk = itk % NS;
+            if (!Q8 && v && pg_cleans(g, j)) {
               ok = pg_wait(&sm.kv_full[sv], (it / NS) & 1, wc);
               if (!ok) break;
               pg_clean<128, Cfg::kChunks>(g, j, sm.kv[sv], lane);
             }
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+              const PgRange r = i ? rg1 : rg0;
+              const bool pv = j >= r.lo && j < r.hi, sc = j + 1 >= r.lo && j + 1 < r.hi;
+              // with a ring of three converted tiles K_{j+1} is not there before V_{j-1}'s slot is
+              // free: there it is waited for after the products
+              uint64_t* bar = nullptr;
+              uint32_t parity = 0;
+              if (lane == 0 && pv) bar = &sm.p_full[i], parity = (i ? pcnt[1] : pcnt[0]) & 1;
+              if (lane == 1 && i == 0 && v) bar = &sm.kv_full[sv], parity = (it / NS) & 1;
+              if (lane == 2 && i == 0 && k && !Q8) bar = &sm.kv_full[sk], parity = (itk / NS) & 1;
+              ok = pg_wait_lanes(bar, parity, wc);
+              if (!ok) break;
+              tc_fence_after();
+              if (pv) {
+                if (i) ++pcnt[1]; else ++pcnt[0];
+                issue_pv(i, sv, j > r.lo);
+                if (j + 1 == r.hi) umma_commit_w(&sm.o_done[i]);
+              }
+              if (i == 1 && v) umma_commit_w(&sm.kv_empty[sv]);
+              if (Q8 && i == 0 && k) {
+                ok = pg_wait(&sm.kv_full[sk], (itk / NS) & 1, wc);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              if (sc) {
+                issue_s(i, i, sk);
+                umma_commit_w(&sm.s_full[i]);
+                if (j + 2 == r.hi) umma_commit_w(&sm.q_empty[i]);
+              }
+            }
+            if (!ok) break;
+            if (k) umma_commit_w(&sm.kv_empty[sk]);
+            it += v + k;
           }
-          // with a ring of three converted tiles K_{j+1} is not there before V_{j-1}'s slot is free:
-          // it is waited for after the products
-          const uint32_t itv = it, itk = it + (j >= kt0);
-          uint64_t* bar = nullptr;
-          uint32_t parity = 0;
-          if (lane == 0 && fresh && sv >= 0) bar = &sm.kv_full[sv], parity = (itv / NS) & 1;
-          if (lane == 1 && pv) bar = &sm.p_full[i], parity = (i ? pcnt[1] : pcnt[0]) & 1;
-          if (!Q8 && lane == 2 && fresh && sk >= 0) bar = &sm.kv_full[sk], parity = (itk / NS) & 1;
-          ok = pg_wait_lanes(bar, parity, wc);
-          if (!ok) break;
-          tc_fence_after();
-          if (pv) {
-            if (i) ++pcnt[1]; else ++pcnt[0];
-            issue_pv(i, sv, j - (pair ? 1 : 2) >= r.lo);
-            if (pair ? j + 1 == r.hi : j + 2 >= r.hi) umma_commit_w(&sm.o_done[i]);
-          }
-          const bool last = !pair || i == 1;  // the slots' last use
-          if (last && sv >= 0) umma_commit_w(&sm.kv_empty[sv]);
-          if (Q8 && fresh && sk >= 0) {
-            ok = pg_wait(&sm.kv_full[sk], (itk / NS) & 1, wc);
+        } else {
+          // PV_i(j), S_i(j+2), the groups in turn; the first two rounds have scores only
+          for (int j = kt0 - 2; j < kend; ++j) {
+            const int i = (j - kt0) & 1;
+            const bool v = j >= kt0, k = j + 2 < kend;
+            const uint32_t itk = it + v;
+            const int sv = it % NS, sk = itk % NS;
+            if (!Q8 && v && pg_cleans(g, j)) {
+              ok = pg_wait(&sm.kv_full[sv], (it / NS) & 1, wc);
+              if (!ok) break;
+              pg_clean<128, Cfg::kChunks>(g, j, sm.kv[sv], lane);
+            }
+            uint64_t* bar = nullptr;
+            uint32_t parity = 0;
+            if (lane == 0 && v) bar = &sm.p_full[i], parity = (i ? pcnt[1] : pcnt[0]) & 1;
+            if (lane == 1 && v) bar = &sm.kv_full[sv], parity = (it / NS) & 1;
+            if (lane == 2 && k && !(Q8 && v)) bar = &sm.kv_full[sk], parity = (itk / NS) & 1;
+            ok = pg_wait_lanes(bar, parity, wc);
             if (!ok) break;
             tc_fence_after();
+            if (v) {
+              if (i) ++pcnt[1]; else ++pcnt[0];
+              issue_pv(i, sv, j - 2 >= kt0);
+              umma_commit_w(&sm.kv_empty[sv]);
+              if (j + 2 >= kend) umma_commit_w(&sm.o_done[i]);
+            }
+            if (k) {
+              if (Q8 && v) {
+                ok = pg_wait(&sm.kv_full[sk], (itk / NS) & 1, wc);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              issue_s(i, 0, sk);
+              umma_commit_w(&sm.s_full[i]);
+              umma_commit_w(&sm.kv_empty[sk]);
+              if (j + 3 == kend) umma_commit_w(&sm.q_empty[0]);
+            }
+            it += v + k;
           }
-          if (sc) {
-            issue_s(i, pair ? i : 0, sk);
-            umma_commit_w(&sm.s_full[i]);
-            if (js + 1 == r.hi) umma_commit_w(&sm.q_empty[pair ? i : 0]);
-          }
-          if (last && sk >= 0) umma_commit_w(&sm.kv_empty[sk]);
-          if (fresh) it += (sv >= 0) + (sk >= 0);
         }
         if (!ok) break;
         if (rg0.hi > rg0.lo) ++qcnt[0];

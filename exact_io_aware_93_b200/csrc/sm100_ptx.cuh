@@ -167,6 +167,17 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+// Four bytes from global to shared memory, and the thread's arrival on an mbarrier once its copies
+// so far have landed (it counts among the barrier's expected arrivals).
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src))
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // fp32 add of one shared-memory box into global memory through a 3-D tensor map (a TMA
 // reduce: elements outside the tensor's extent are skipped), tracked by the issuing
 // thread's bulk-async group.  The box must start on the map's swizzle alignment and
