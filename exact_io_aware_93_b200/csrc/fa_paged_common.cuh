@@ -72,6 +72,14 @@ __device__ __forceinline__ void pg_report(const int* abort_flag, int* status) {
   }
 }
 
+// A unit computed by several CTAs, from the one that began it: what the join needs.
+struct PgSplit {
+  int parts;  // CTAs; 0: none
+  int kvh;
+  int q0;     // first token
+  int ntok;
+};
+
 struct PgArgs {
   const int* cu;          // [B + 1]
   const int* seqlens;     // [B]
@@ -81,7 +89,7 @@ struct PgArgs {
   const float* q_scale;   // e4m3 pages: [T, H] factors of the scaled queries
   void* out;              // [T, H, D]
   float* lse;             // [H, T]
-  int* meta;              // total, L, unit prefix [B + 1], key-tile prefix [B + 1]
+  PgSplit* splits;        // of each CTA: the unit that it began and did not finish
   float* part_lse;        // [slots * kSubs, kRows, 2]
   float* part_o;          // [slots * kSubs, kRows, D]
   int n_lo, n_hi;         // sequences with more than n_lo and up to n_hi new tokens are computed
@@ -96,22 +104,19 @@ struct PgSeq {
   int q0, n, len, units;
 };
 __device__ __forceinline__ PgSeq pg_seq(const PgArgs& a, int b) {
-  const long long c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
+  const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), len = __ldg(a.seqlens + b);
   PgSeq s;
   const bool in = c0 >= 0 && c0 <= a.T && c1 > c0;
-  s.q0 = in ? static_cast<int>(c0) : 0;
-  s.n = in ? static_cast<int>(min(min(c1 - c0, static_cast<long long>(a.max_q)), a.T - c0)) : 0;
+  s.q0 = in ? c0 : 0;
+  s.n = in ? min(min(c1 - c0, a.max_q), a.T - c0) : 0;
   if (s.n <= a.n_lo || s.n > a.n_hi) s.n = 0;
-  const long long cap = static_cast<long long>(a.max_pages) * a.page;
-  s.len = static_cast<int>(min(max(static_cast<long long>(__ldg(a.seqlens + b)), 0ll), cap));
-  s.units = ((s.n + a.TQ - 1) / a.TQ + 1) / 2;
+  s.len = min(max(len, 0), a.max_pages * a.page);
+  s.units = s.n <= 2 * a.TQ ? s.n > 0 : ((s.n + a.TQ - 1) / a.TQ + 1) / 2;
   return s;
 }
 __device__ __forceinline__ bool pg_seq_ok(const PgArgs& a, int b) {
-  const long long c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
-  const long long len = __ldg(a.seqlens + b);
-  return c0 >= 0 && c1 >= c0 && c1 <= a.T && c1 - c0 <= a.max_q && len >= 0 &&
-         len <= static_cast<long long>(a.max_pages) * a.page;
+  const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), len = __ldg(a.seqlens + b);
+  return c0 >= 0 && c1 >= c0 && c1 <= a.T && c1 - c0 <= a.max_q && len >= 0 && len <= a.max_pages * a.page;
 }
 
 // Keys [lo, hi) that the tokens at positions p0 .. p1 of a sequence of `len` keys see, and the
@@ -153,77 +158,68 @@ __device__ __forceinline__ int pg_seq_cost(const PgArgs& a, const PgSeq& s) {
 
 // This CTA's slice [t0, t1) of the work and the unit that t0 falls into, which starts at `start`.
 struct PgPlan {
-  int t0, t1, b, kvh, u, start;
+  int t0, t1, per, b, kvh, u, start;
 };
 
-// One warp.  With `write` it also stores the prefixes for the merge kernel and checks the
-// lengths and offsets.
+// One warp; CTA 0's also checks the lengths and offsets.
 template <typename Cfg>
-__device__ __forceinline__ void pg_plan(const PgArgs& a, int lane, PgPlan* out, bool write) {
+__device__ __forceinline__ void pg_plan(const PgArgs& a, int lane, PgPlan* out) {
   constexpr unsigned kFull = 0xffffffffu;
-  int total = 0;
+  int total = 0, acc = 0;
+  PgPlan p{0, 0, 0, 0, 0, 0, 0};
+  // first the total, then the sequence that the slice starts in; up to 32 sequences are read once
   PgSeq s{0, 0, 0, 0};
   int w = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int b = b0 + lane;
-    s = PgSeq{0, 0, 0, 0};
-    if (b < a.B) s = pg_seq(a, b);
-    w = pg_seq_cost<Cfg>(a, s);
-    total += static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(w * a.H_kv)));
-  }
-  const int grid = static_cast<int>(gridDim.x);
-  // at least a tile's cost, so that no CTA inside a unit's span is left without one of its tiles
-  const int per = max((total + grid - 1) / grid, Cfg::kPairCost);
-  const int t0 = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(blockIdx.x) * per));
-  const int t1 = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(t0) + per));
-  bool found = t0 >= t1;
-  if (found && lane == 0) *out = PgPlan{t0, t0, 0, 0, 0, t0};
-  int acc = 0, uacc = 0;
-  for (int b0 = 0; b0 < a.B && (!found || write); b0 += 32) {
-    const int b = b0 + lane;
-    if (a.B > 32) {  // up to 32 sequences are still at hand
-      s = PgSeq{0, 0, 0, 0};
-      if (b < a.B) s = pg_seq(a, b);
-      w = pg_seq_cost<Cfg>(a, s);
-    }
-    if (write && b < a.B && !pg_seq_ok(a, b)) plan_fail(a.status, 43);
-    int incl = w * a.H_kv, uincl = s.units;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(kFull, incl, o), y = __shfl_up_sync(kFull, uincl, o);
-      if (lane >= o) {
-        incl += x;
-        uincl += y;
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int b = b0 + lane;
+      if (round == 0 || a.B > 32) {
+        s = PgSeq{0, 0, 0, 0};
+        if (b < a.B) {
+          s = pg_seq(a, b);
+          if (round == 0 && blockIdx.x == 0 && !pg_seq_ok(a, b)) plan_fail(a.status, 43);
+        }
+        w = pg_seq_cost<Cfg>(a, s);
       }
-    }
-    incl += acc;
-    uincl += uacc;
-    const int excl = incl - w * a.H_kv;
-    if (write && b < a.B) {
-      a.meta[2 + b + 1] = uincl;
-      a.meta[2 + a.B + 1 + b + 1] = incl;
-    }
-    if (!found && b < a.B && excl <= t0 && t0 < incl) {  // one lane
-      const int kvh = (t0 - excl) / w;
-      int start = excl + kvh * w, u = 0;
-      while (true) {
-        const PgKeys k = pg_unit_keys(a, s, u);
-        const int c = (k.t1 - k.t0) * (pg_is_pair(a, s, u) ? Cfg::kPairCost : Cfg::kSplitCost);
-        if (t0 < start + c) break;
-        start += c;
-        ++u;
+      int incl = w * a.H_kv;
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += x;
       }
-      *out = PgPlan{t0, t1, b, kvh, u, start};
+      incl += acc;
+      const int excl = incl - w * a.H_kv;
+      if (round == 1 && excl <= p.t0 && p.t0 < incl) {  // one lane
+        p.b = b;
+        p.kvh = (p.t0 - excl) / w;
+        p.start = excl + p.kvh * w;
+        while (true) {
+          const PgKeys k = pg_unit_keys(a, s, p.u);
+          const int c = (k.t1 - k.t0) * (pg_is_pair(a, s, p.u) ? Cfg::kPairCost : Cfg::kSplitCost);
+          if (p.t0 < p.start + c) break;
+          p.start += c;
+          ++p.u;
+        }
+        *out = p;
+      }
+      acc = __shfl_sync(kFull, incl, 31);
+      if (round == 1 && acc > p.t0) return;
     }
-    found = found || (t0 < __shfl_sync(kFull, incl, 31));
-    acc = __shfl_sync(kFull, incl, 31);
-    uacc = __shfl_sync(kFull, uincl, 31);
-  }
-  if (write && lane == 0) {
-    a.meta[0] = total;
-    a.meta[1] = per;
-    a.meta[2] = 0;
-    a.meta[2 + a.B + 1] = 0;
+    if (round == 0) {
+      total = acc;
+      acc = 0;
+      // at least a tile's cost, so that no CTA inside a unit's span is left without one of its tiles
+      p.per = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), Cfg::kPairCost);
+      p.t0 = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(blockIdx.x) * p.per));
+      p.t1 = min(total - p.t0, p.per) + p.t0;
+      p.start = p.t0;
+      if (lane == 0) *out = p;  // the answer when there is nothing to do
+      if (p.t0 >= p.t1) return;
+      p.start = 0;
+      __syncwarp();
+    }
   }
 }
 
@@ -250,10 +246,11 @@ struct PgSeg {
 // Walks this CTA's slice segment by segment (the schedule's warp, every lane alike).
 template <typename Cfg>
 struct PgWalk {
-  int t0, t1, b, kvh, u, start;
+  int t0, t1, per, b, kvh, u, start;
   PgSeq s;
+  PgSplit split;  // of the last segment
   __device__ __forceinline__ PgWalk(const PgArgs& a, const PgPlan& p)
-      : t0(p.t0), t1(p.t1), b(p.b), kvh(p.kvh), u(p.u), start(p.start), s(pg_seq(a, p.b)) {}
+      : t0(p.t0), t1(p.t1), per(p.per), b(p.b), kvh(p.kvh), u(p.u), start(p.start), s(pg_seq(a, p.b)), split{0, 0, 0, 0} {}
   __device__ __forceinline__ bool next(const PgArgs& a, PgSeg& g) {
     while (start < t1) {
       if (u >= s.units) {
@@ -273,6 +270,7 @@ struct PgWalk {
       const int first = t0 > start ? (t0 - start + cost - 1) / cost : 0;
       const int last = min(T, (t1 - start + cost - 1) / cost);
       const int tok0 = u * 2 * a.TQ;
+      const int begin = start;
       start += T * cost;
       ++u;
       if (first >= last) continue;
@@ -288,6 +286,8 @@ struct PgWalk {
       g.pair = pair;
       g.whole = first == 0 && last == T;
       g.slot = first == 0;
+      if (first == 0 && last < T)
+        split = PgSplit{(begin + (T - 1) * cost) / per - static_cast<int>(blockIdx.x) + 1, kvh, g.q0, g.ntok};
       for (int i = 0; i < 2; ++i) {
         const int tok = i * a.TQ;
         const int n = min(a.TQ, g.ntok - tok);
@@ -567,60 +567,62 @@ __global__ void __launch_bounds__(256) fa_paged_scale_q_kernel(const void* q, in
 
 // ---------------------------------------------------------------- joining the partial results
 // Per row: LSE = log sum_s exp(lse_s) and O = sum_s exp(lr_s - LR) O_s with LR = log sum_s
-// exp(lr_s), the convex combination one CTA would have formed.  Units that one CTA computed
-// were written by it; rows of units without keys get O = 0, LSE = -inf.  Block (unit,
-// key/value head, part) of four warps; W warps share a row's partial results.
-template <int D, Elem E, typename Cfg, int W>
-__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PgArgs a) {
+// exp(lr_s), the convex combination one CTA would have formed.  Blocks (c, y) with c < `ctas` take
+// the unit that CTA c began and did not finish, W warps per row; further blocks c = ctas + b give
+// the rows of sequence b's units without keys O = 0, LSE = -inf.  All other rows were written by
+// their CTA.
+template <int D, Elem E, typename Cfg, int W, int kThreads>
+__global__ void __launch_bounds__(kThreads) fa_paged_merge_kernel(const PgArgs a, int ctas) {
   using T = typename ElemOps<E>::T;
   constexpr unsigned kFull = 0xffffffffu;
   constexpr int V = D / 32;  // columns per lane
+  constexpr int kRowsAtOnce = kThreads / 32 / W;
   __shared__ float acc_sh[W > 1 ? W : 1][D];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int G = a.H / a.H_kv;
-  const int kvh = blockIdx.y;
-  const int unit = blockIdx.x;
-  const int b = find_seq(a.meta + 2, a.B, unit, lane);
-  if (b >= a.B) return;
-  const PgSeq s = pg_seq(a, b);
-  const int u = unit - a.meta[2 + b];
-  const int tok0 = u * 2 * a.TQ;
-  const int ntok = min(2 * a.TQ, s.n - tok0);
-  const PgKeys k = pg_unit_keys(a, s, u);
-  const int T_u = k.t1 - k.t0;
-  const int* costs = a.meta + 2 + a.B + 1;
-  int start = costs[b] + kvh * ((costs[b + 1] - costs[b]) / a.H_kv);
-  int before = 0;  // the sequence's units before this one are pairs
-  for (int x = lane; x < u; x += 32) {
-    const PgKeys kx = pg_unit_keys(a, s, x);
-    before += (kx.t1 - kx.t0) * Cfg::kPairCost;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results are there
+  if (static_cast<int>(blockIdx.x) >= ctas) {
+    const int b = static_cast<int>(blockIdx.x) - ctas;
+    const PgSeq s = pg_seq(a, b);
+    // a token at a position >= 0 sees itself
+    if (blockIdx.y > 0 || (s.len > 0 && (!a.causal || s.len >= s.n))) return;
+    for (int u = 0; u < s.units; ++u) {
+      const PgKeys k = pg_unit_keys(a, s, u);
+      if (k.t1 > k.t0) continue;
+      const int tok0 = u * 2 * a.TQ;
+      const int rows = min(2 * a.TQ, s.n - tok0) * a.H;  // all key/value heads'
+      for (int row = warp; row < rows; row += kThreads / 32) {
+        const int64_t token = static_cast<int64_t>(s.q0) + tok0 + row / a.H;
+        const int h = row % a.H;
+        if (!FA_IN_BOUNDS(token >= 0 && token < a.T, a.status, 507)) continue;
+        for (int c = lane; c < D; c += 32) static_cast<T*>(a.out)[(token * a.H + h) * D + c] = ElemOps<E>::one(0.f);
+        if (lane == 0) a.lse[static_cast<int64_t>(h) * a.T + token] = -INFINITY;
+      }
+    }
+    return;
   }
-  start += static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(before)));
-  const int per = a.meta[1];
-  const int cf = start / per;
-  const int cost = pg_is_pair(a, s, u) ? Cfg::kPairCost : Cfg::kSplitCost;
-  const int cl = T_u > 0 ? (start + (T_u - 1) * cost) / per : cf;
-  if (T_u > 0 && cf == cl) return;  // written by its CTA
-  const int parts = T_u > 0 ? cl - cf + 1 : 0;
-  const int rows = G * ntok;
-  for (int row = blockIdx.z * (4 / W) + warp / W; row < rows; row += gridDim.z * (4 / W)) {
+  const PgSplit sp = a.splits[blockIdx.x];
+  const int rows = G * sp.ntok;
+  if (sp.parts == 0) return;
+  for (int row = blockIdx.y * kRowsAtOnce + warp / W; row < rows; row += gridDim.y * kRowsAtOnce) {
     const int tile = row / (G * a.TQ);
     const int rc = row - tile * G * a.TQ;
-    const int iq = row / G, h = kvh * G + (row - iq * G);
-    const int64_t token = static_cast<int64_t>(s.q0) + tok0 + iq;
-    // index of partial result i of this row
+    const int iq = row / G, h = sp.kvh * G + (row - iq * G);
+    const int64_t token = static_cast<int64_t>(sp.q0) + iq;
+    // index of partial result i of this row: the beginning lies in its CTA's second slot
     auto at = [&](int i) -> int64_t {
-      const int slot = 2 * (cf + i) + (i == 0);
+      const int slot = 2 * (static_cast<int>(blockIdx.x) + i) + (i == 0);
       return (static_cast<int64_t>(slot) * Cfg::kSubs + tile) * Cfg::kRows + rc;
     };
     float mx_l = -INFINITY, mx_r = -INFINITY, s_l = 0.f, s_r = 0.f;
-    for (int i = lane; i < parts; i += 32) {
+    float2 mine = make_float2(-INFINITY, -INFINITY);  // of the lane's last partial result
+    for (int i = lane; i < sp.parts; i += 32) {
       const int64_t x = at(i);
-      if (!FA_IN_BOUNDS(x >= 0 && x < a.slots * Cfg::kSubs * Cfg::kRows, a.status, 507)) continue;
-      const float2 v = *reinterpret_cast<const float2*>(a.part_lse + x * 2);
-      mx_l = fmaxf(mx_l, v.x);
-      mx_r = fmaxf(mx_r, v.y);
+      if (!FA_IN_BOUNDS(x >= 0 && x < a.slots * Cfg::kSubs * Cfg::kRows, a.status, 508)) continue;
+      mine = *reinterpret_cast<const float2*>(a.part_lse + x * 2);
+      mx_l = fmaxf(mx_l, mine.x);
+      mx_r = fmaxf(mx_r, mine.y);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -629,12 +631,10 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PgArgs a) {
     }
     if (mx_l == -INFINITY) mx_l = 0.f;  // no key, or NaN only: the sums decide
     if (mx_r == -INFINITY) mx_r = 0.f;
-    for (int i = lane; i < parts; i += 32) {
-      const int64_t x = at(i);
-      if (!FA_IN_BOUNDS(x >= 0 && x < a.slots * Cfg::kSubs * Cfg::kRows, a.status, 508)) continue;
-      const float2 v = *reinterpret_cast<const float2*>(a.part_lse + x * 2);
-      s_l += expf(v.x - mx_l);
-      s_r += expf(v.y - mx_r);
+    for (int i = lane; i < sp.parts; i += 32) {
+      if (sp.parts > 32) mine = *reinterpret_cast<const float2*>(a.part_lse + at(i) * 2);
+      s_l += expf(mine.x - mx_l);
+      s_r += expf(mine.y - mx_r);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -647,21 +647,18 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PgArgs a) {
     const float inv = s_r == 0.f ? 0.f : 1.0f / s_r;
     // 32 partial results at a time: a lane forms one weight, then the warp sums the rows with
     // the weights broadcast; a partial result without keys was not written and is not read
-    for (int base = (W > 1 ? warp * 32 : 0); base < parts; base += 32 * W) {
+    for (int base = (W > 1 ? (warp % W) * 32 : 0); base < sp.parts; base += 32 * W) {
       float wl = 0.f;
-      int64_t x = 0;
-      if (base + lane < parts) {
-        x = at(base + lane);
-        const float v = a.part_lse[x * 2 + 1];
+      if (base + lane < sp.parts) {
+        const float v = sp.parts > 32 ? a.part_lse[at(base + lane) * 2 + 1] : mine.y;
         wl = v == -INFINITY ? 0.f : expf(v - mx_r) * inv;
       }
-      const int cnt = min(32, parts - base);
+      const int cnt = min(32, sp.parts - base);
 #pragma unroll 4
       for (int t = 0; t < cnt; ++t) {
         const float wgt = __shfl_sync(kFull, wl, t);
-        const int64_t xt = __shfl_sync(kFull, x, t);
         if (wgt == 0.f) continue;
-        const float* po = a.part_o + xt * D + lane * V;
+        const float* po = a.part_o + at(base + t) * D + lane * V;
         if constexpr (V == 4) {
           const float4 v = *reinterpret_cast<const float4*>(po);
           acc[0] = fmaf(wgt, v.x, acc[0]);
@@ -675,7 +672,7 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PgArgs a) {
         }
       }
     }
-    if constexpr (W > 1) {
+    if constexpr (W > 1) {  // one row per block at a time
 #pragma unroll
       for (int x = 0; x < V; ++x) acc_sh[warp][lane * V + x] = acc[x];
       __syncthreads();

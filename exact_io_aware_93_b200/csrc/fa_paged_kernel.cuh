@@ -180,12 +180,15 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
-    pg_plan<Cfg>(a, lane, &sm.plan, blockIdx.x == 0);
+    pg_plan<Cfg>(a, lane, &sm.plan);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
+  // launched while the kernel that scales the queries may still run
+  if constexpr (Q8) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Readers of the segment ring: the next segment, or null at the end or after an abort; a
   // reader gives the one it holds back first.
@@ -260,6 +263,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
           return true;
         });
       }
+      if (lane == 0 && FA_IN_BOUNDS(static_cast<int>(blockIdx.x) * 2 < a.slots, status, 514)) a.splits[blockIdx.x] = w.split;
       if (!ok && lane == 0) {
         flight.drain(Q8 ? sm.raw_full : sm.kv_full, status);
         for (int i = 0; i < 2; ++i)

@@ -10,6 +10,23 @@
 
 namespace fa {
 
+// Launch; with `early` the blocks may start while the kernel before them in the stream ends, and wait
+// for it themselves (griddepcontrol.wait): about 1 us less between two kernels.
+template <typename... P, typename... Args>
+bool launch_after(bool early, void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
+}
+
 // One pass: the kernel for the sequences with n_lo < n <= n_hi new tokens, tiles of TQ tokens,
 // and the join of its partial results.  RW: rows of the few-rows kernel, 0 for tiles of 128.
 template <int D, Elem E, bool Q8, int RW>
@@ -54,7 +71,7 @@ fa_status launch_paged(DeviceInfo& di, const PagedCall& c, int n_lo, int n_hi) {
   a.q_scale = reinterpret_cast<const float*>(w + L.q_scale);
   a.out = c.o;
   a.lse = c.lse;
-  a.meta = reinterpret_cast<int*>(w + ps.meta);
+  a.splits = reinterpret_cast<PgSplit*>(w + ps.splits);
   a.part_lse = reinterpret_cast<float*>(w + ps.part_lse);
   a.part_o = reinterpret_cast<float*>(w + ps.part_o);
   a.n_lo = n_lo;
@@ -80,17 +97,15 @@ fa_status launch_paged(DeviceInfo& di, const PagedCall& c, int n_lo, int n_hi) {
         c.q, p.q_stride[0], p.q_stride[1], w + ps.q, reinterpret_cast<float*>(w + L.q_scale), p.T, p.H, di.status);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
   }
-  kern<<<grid, Cfg::kThreads, smem, c.stream>>>(mq, mk, mv, a);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
-  // few rows: a block per row, its four warps sharing the partial results; otherwise a warp per
-  // row and blocks of up to 32 rows
-  const unsigned units = static_cast<unsigned>(paged_units(p, n_hi, TQ));
-  const int rows = G * (n_hi < 2 * TQ ? n_hi : 2 * TQ);
+  if (!launch_after(Q8, kern, dim3(grid), Cfg::kThreads, smem, c.stream, mq, mk, mv, a)) return FA_ERR_LAUNCH;
+  // few rows: a block per row, its four warps sharing the partial results; otherwise eight blocks of
+  // eight warps, a row each at a time
+  bool ok;
   if constexpr (kFew)
-    fa_paged_merge_kernel<D, E, Cfg, 4><<<dim3(units, p.H_kv, rows), 128, 0, c.stream>>>(a);
+    ok = launch_after(true, fa_paged_merge_kernel<D, E, Cfg, 4, 128>, dim3(grid + p.B, G * TQ), 128, 0, c.stream, a, grid);
   else
-    fa_paged_merge_kernel<D, E, Cfg, 1><<<dim3(units, p.H_kv, (rows + 31) / 32), 128, 0, c.stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+    ok = launch_after(true, fa_paged_merge_kernel<D, E, Cfg, 1, 256>, dim3(grid + p.B, 8), 256, 0, c.stream, a, grid);
+  return ok ? FA_OK : FA_ERR_LAUNCH;
 }
 
 // Kernel attributes of one instantiation, before anything is enqueued.
@@ -109,14 +124,15 @@ bool paged_ready(DeviceInfo& di) {
 
 template <Elem E, bool Q8, int D>
 fa_status paged_call_d(DeviceInfo& di, const PagedCall& c) {
-  const PagedSplit s = paged_split(c.p);
+  const PagedKernels s = paged_kernels(c.p);
+  constexpr int kMost = Q8 ? 32 : 16;
   if (!(s.rows != 8 || paged_ready<D, E, Q8, 8>(di)) || !(s.rows != 16 || paged_ready<D, E, Q8, 16>(di)) ||
-      !(s.rows != 32 || paged_ready<D, E, Q8, 32>(di)) || !(!s.many || paged_ready<D, E, Q8, 0>(di)))
+      !(s.rows != 32 || paged_ready<D, E, Q8, kMost>(di)) || !(!s.many || paged_ready<D, E, Q8, 0>(di)))
     return FA_ERR_LAUNCH;
   fa_status st = FA_OK;
   if (s.rows == 8) st = launch_paged<D, E, Q8, 8>(di, c, 0, s.few_q);
   if (s.rows == 16) st = launch_paged<D, E, Q8, 16>(di, c, 0, s.few_q);
-  if (s.rows == 32) st = launch_paged<D, E, Q8, 32>(di, c, 0, s.few_q);
+  if (s.rows == 32) st = launch_paged<D, E, Q8, kMost>(di, c, 0, s.few_q);
   if (st == FA_OK && s.many) st = launch_paged<D, E, Q8, 0>(di, c, s.few_q, c.p.max_q);
   return st;
 }

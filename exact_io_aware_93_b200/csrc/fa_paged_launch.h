@@ -27,19 +27,22 @@ struct PagedCall {
 
 // Which kernels a call takes.  A key/value head's rows, (H / H_kv) * n for n new tokens, choose
 // per sequence: up to `rows` of them the few-rows kernel (n <= few_q), more the tiles of 128.
-//   all sequences few (max_q says so): that kernel alone, at the smallest of 8, 16, 32 rows
+//   all sequences few (max_q says so): that kernel alone, at the smallest of 8, 16 and, with e4m3
+//     pages, 32 rows.  (16 sequences of 16-32K tokens, 20 rows: 16-bit pages 270 us there and 262 us
+//     in tiles of 128; e4m3 pages 322 and 386 us.)
 //   all sequences max_q tokens long (T = B max_q): the tiles alone
 //   a mixture: both, one after the other, single tokens in the first at the smallest size
-struct PagedSplit {
+struct PagedKernels {
   int rows;   // 8, 16, 32, or 0: the few-rows kernel is not used
   int few_q;  // its most tokens per sequence
   bool many;
 };
-inline PagedSplit paged_split(const fa_paged_problem& p) {
+inline PagedKernels paged_kernels(const fa_paged_problem& p) {
   const int G = p.H / p.H_kv;
   const long long rows = static_cast<long long>(G) * p.max_q;
-  if (rows <= 32) return {rows <= 8 ? 8 : (rows <= 16 ? 16 : 32), p.max_q, false};
-  if (G > 32 || static_cast<long long>(p.B) * p.max_q == p.T) return {0, 0, true};
+  const int most = p.quant ? 32 : 16;
+  if (rows <= most) return {rows <= 8 ? 8 : (rows <= 16 ? 16 : 32), p.max_q, false};
+  if (G > most || static_cast<long long>(p.B) * p.max_q == p.T) return {0, 0, true};
   const int r = G <= 8 ? 8 : (G <= 16 ? 16 : 32);
   return {r, r / G, true};
 }
@@ -52,27 +55,27 @@ inline long long paged_units(const fa_paged_problem& p, int n, int TQ) {
   return each < all ? each : all;
 }
 
-// Workspace regions of each kernel used: the plan (total, work per CTA, unit and work prefixes),
-// the partial log-sums [rows, 2] and outputs [rows, d] (a CTA leaves at most two partial segments,
-// of `rows` or 256 rows), and with e4m3 pages the scaled queries (2 bytes per element); then a
-// factor per query row.
+// Workspace regions of each kernel used: the units that CTAs share (16 bytes per CTA), the partial
+// log-sums [rows, 2] and outputs [rows, d] (a CTA leaves at most two partial segments, of `rows` or
+// 256 rows), and with e4m3 pages the scaled queries (2 bytes per element); then a factor per query
+// row.
 struct PagedLayout {
   struct Pass {
-    size_t meta, part_lse, part_o, q;
+    size_t splits, part_lse, part_o, q;
   };
   Pass few, many;
   size_t q_scale, total;
 };
 inline PagedLayout paged_layout(const fa_paged_problem& p, int grid) {
   const auto round256 = [](size_t x) { return (x + 255) / 256 * 256; };
-  const PagedSplit s = paged_split(p);
+  const PagedKernels s = paged_kernels(p);
   const size_t q_rows = p.quant ? static_cast<size_t>(p.T) * p.H : 0;
   PagedLayout L{};
   size_t at = 0;
   const auto pass = [&](PagedLayout::Pass& x, size_t rows) {
     rows *= 2 * static_cast<size_t>(grid);
-    x.meta = at;
-    x.part_lse = x.meta + round256((2 + 2 * (static_cast<size_t>(p.B) + 1)) * 4);
+    x.splits = at;
+    x.part_lse = x.splits + round256(static_cast<size_t>(grid) * 16);
     x.part_o = x.part_lse + round256(rows * 2 * 4);
     x.q = x.part_o + round256(rows * static_cast<size_t>(p.d) * 4);
     at = x.q + round256(q_rows * p.d * 2);
