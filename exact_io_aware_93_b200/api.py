@@ -10,15 +10,18 @@ call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
 from . import build as _build
 
 _lib = None
+_HERE = contextlib.nullcontext()
 
 FA_STATUS = {
     0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_ALIGNMENT",
@@ -27,6 +30,7 @@ FA_STATUS = {
 }
 
 
+_SIXTEEN = (torch.bfloat16, torch.float16)
 FA_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
 
 
@@ -67,6 +71,24 @@ class FaPagedProblem(ctypes.Structure):
                 ("max_q", ctypes.c_int), ("P", ctypes.c_int), ("max_pages", ctypes.c_int), ("page", ctypes.c_int),
                 ("d", ctypes.c_int), ("scale", ctypes.c_float), ("causal", ctypes.c_int), ("window", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("quant", ctypes.c_int), ("q_stride", ctypes.c_longlong * 2)]
+
+
+def _packer(cls):
+    """Packs the fields of a descriptor, arrays flat, into its bytes (a ctypes object of nested
+    arrays takes microseconds to build)."""
+    kinds = {ctypes.c_int: "i", ctypes.c_float: "f"}
+    s = struct.Struct("@" + "".join(kinds.get(kind) or f"{kind._length_}q" for _, kind in cls._fields_))
+    assert s.size == ctypes.sizeof(cls)
+
+    def pack(*values) -> bytes:
+        try:
+            return s.pack(*values)
+        except struct.error as e:
+            raise ValueError(f"{cls.__name__}{values}: {e}") from None
+    return pack
+
+
+_pack_rope, _pack_cache, _pack_paged = map(_packer, (FaRopeProblem, FaCacheProblem, FaPagedProblem))
 
 
 class FAError(RuntimeError):
@@ -123,28 +145,30 @@ def lib() -> ctypes.CDLL:
     L.fa_decode_workspace_size.restype = ctypes.c_size_t
     L.fa_decode.argtypes = [ctypes.POINTER(FaDecodeProblem), vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
     L.fa_decode.restype = i
-    L.fa_rope.argtypes = [ctypes.POINTER(FaRopeProblem), vp, vp, vp, vp, vp, vp, vp]
+    L.fa_rope.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
     L.fa_rope.restype = i
-    L.fa_cache_append.argtypes = [ctypes.POINTER(FaCacheProblem)] + [vp] * 10
+    L.fa_cache_append.argtypes = [vp] + [vp] * 10
     L.fa_cache_append.restype = i
-    L.fa_cache_gather.argtypes = [ctypes.POINTER(FaCacheProblem)] + [vp] * 11
+    L.fa_cache_gather.argtypes = [vp] + [vp] * 11
     L.fa_cache_gather.restype = i
-    L.fa_paged_workspace_size.argtypes = [ctypes.POINTER(FaPagedProblem)]
+    L.fa_paged_workspace_size.argtypes = [vp]
     L.fa_paged_workspace_size.restype = ctypes.c_size_t
-    L.fa_paged.argtypes = [ctypes.POINTER(FaPagedProblem)] + [vp] * 11 + [ctypes.c_size_t, vp]
+    L.fa_paged.argtypes = [vp] + [vp] * 11 + [ctypes.c_size_t, vp]
     L.fa_paged.restype = i
     _lib = L
     return L
 
 
-def _stream_ptr(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+def _stream_ptr(t: torch.Tensor) -> int:
+    """The current stream of t's device.  (The raw handle: building a Stream object first costs
+    microseconds, which count beside kernels of a few.)"""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _on(t: torch.Tensor):
     """Make t's device current for a library call: the library takes its SM count, kernel
     set-up and status word from the current device, and launches on that device's stream."""
-    return torch.cuda.device(t.device)
+    return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
 def validate_inputs(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor) -> None:
@@ -347,9 +371,9 @@ def _check_heads(name: str, t: torch.Tensor, like: torch.Tensor | None = None) -
     strides), of ``like``'s type and device."""
     if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4):
         raise ValueError(f"{name} must be [tokens, heads, d] or [batch, seq_len, heads, d]")
-    if t.dtype not in (torch.bfloat16, torch.float16) or (like is not None and t.dtype != like.dtype):
+    if t.dtype not in _SIXTEEN or (like is not None and t.dtype != like.dtype):
         raise TypeError(f"{name} must be bfloat16 or float16, one type for all, got {t.dtype}")
-    if not t.is_cuda or (like is not None and t.device != like.device):
+    if not t.is_cuda or (like is not None and t.get_device() != like.get_device()):
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path), one device for all")
     if t.stride(-1) != 1 and t.shape[-1] != 1:
         raise ValueError(f"{name} must have contiguous columns")
@@ -380,6 +404,10 @@ def _check_rope_out(name: str, out: torch.Tensor, x: torch.Tensor, *others: torc
             raise ValueError(f"{name} must be its input itself or lie apart from the inputs")
 
 
+def _empty_like(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _strides3(t: torch.Tensor):
     return (t.stride(0) if t.dim() == 4 else 0, t.stride(-3), t.stride(-2))
 
@@ -392,18 +420,18 @@ def _rope(q, k, positions, inv_freq, interleaved, factor, q_out, k_out, inverse)
             raise ValueError(f"k {tuple(k.shape)} does not fit q {tuple(q.shape)}")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    lead = tuple(q.shape[:-2])
+    lead = q.shape[:-2]
     if (not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64)
-            or positions.device != q.device or tuple(positions.shape) not in (lead, lead[-1:])):
-        raise ValueError(f"positions must be int32 or int64 of shape {lead} or {lead[-1:]} on {q.device}")
+            or positions.device != q.device or (positions.shape != lead and positions.shape != lead[-1:])):
+        raise ValueError(f"positions must be int32 or int64 of shape {tuple(lead)} or {tuple(lead[-1:])} on {q.device}")
     if (not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1
             or inv_freq.device != q.device or not inv_freq.is_contiguous()
             or not 1 <= inv_freq.numel() <= q.shape[-1] // 2):
         raise ValueError(f"inv_freq must be a contiguous float64 vector of 1 to {q.shape[-1] // 2} entries on {q.device}")
     given = (q_out, k_out)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    q_out = _empty_like(q) if q_out is None else q_out
     if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = _empty_like(k)
     if given[0] is not None:
         _check_rope_out("q_out", q_out, q, k)
     if given[1] is not None:
@@ -412,13 +440,13 @@ def _rope(q, k, positions, inv_freq, interleaved, factor, q_out, k_out, inverse)
         return q_out, k_out
     B, N = (1, q.shape[0]) if q.dim() == 3 else (q.shape[0], q.shape[1])
     none = (0, 0, 0)
-    p = FaRopeProblem(B, N, q.shape[-2], 0 if k is None else k.shape[-2], q.shape[-1], 2 * inv_freq.numel(),
-                      int(bool(interleaved)), int(inverse), float(factor), FA_DTYPE[q.dtype],
-                      int(positions.dtype == torch.int64), _strides3(q), none if k is None else _strides3(k),
-                      _strides3(q_out), none if k is None else _strides3(k_out),
-                      (positions.stride(0) if positions.dim() == 2 else 0, positions.stride(-1)))
+    p = _pack_rope(B, N, q.shape[-2], 0 if k is None else k.shape[-2], q.shape[-1], 2 * inv_freq.numel(),
+                   int(bool(interleaved)), int(inverse), float(factor), FA_DTYPE[q.dtype],
+                      int(positions.dtype == torch.int64), *_strides3(q), *(none if k is None else _strides3(k)),
+                      *_strides3(q_out), *(none if k is None else _strides3(k_out)),
+                      positions.stride(0) if positions.dim() == 2 else 0, positions.stride(-1))
     with _on(q):
-        st = lib().fa_rope(ctypes.byref(p), q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+        st = lib().fa_rope(p, q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
                            None if k is None else k_out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
                            _stream_ptr(q))
     if st != 0:
@@ -455,8 +483,9 @@ _SCALE_TYPES = (torch.float8_e8m0fnu, torch.uint8)
 def _check_pages(k_pages, v_pages, page_table, seqlens, k_scales, v_scales, dtype) -> bool:
     """The tensors of a paged cache read or written as ``dtype``; True for an e4m3 pool."""
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4 or not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor [pages, kv_heads, page, d]")
+        if (not isinstance(t, torch.Tensor) or t.dim() != 4 or not t.is_cuda or not t.is_contiguous()
+                or 0 in t.shape):
+            raise ValueError(f"{name} must be a contiguous CUDA tensor [pages, kv_heads, page, d], none of them 0")
     if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or k_pages.device != v_pages.device:
         raise ValueError("k_pages and v_pages must have one shape, dtype and device")
     quant = k_pages.dtype == torch.float8_e4m3fn
@@ -503,10 +532,10 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     check_buffer("cu_q", cu_q, (B + 1,), torch.int32, k.device)
     if k.shape[0] == 0:
         return
-    p = FaCacheProblem(B, k.shape[0], H_kv, d, P, max_pages, page, FA_DTYPE[k.dtype], int(quant),
-                       (k.stride(0), k.stride(1)), (v.stride(0), v.stride(1)))
+    p = _pack_cache(B, k.shape[0], H_kv, d, P, max_pages, page, FA_DTYPE[k.dtype], int(quant),
+                       k.stride(0), k.stride(1), v.stride(0), v.stride(1))
     with _on(k):
-        st = lib().fa_cache_append(ctypes.byref(p), k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        st = lib().fa_cache_append(p, k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                                    _ptr(k_scales), _ptr(v_scales), page_table.data_ptr(), seqlens.data_ptr(),
                                    cu_q.data_ptr(), _stream_ptr(k))
     if st != 0:
@@ -543,9 +572,9 @@ def cache_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch
     check_buffer("v_out", v_out, shape, dtype, k_pages.device)
     if total == 0:
         return k_out, v_out
-    p = FaCacheProblem(B, total, H_kv, d, P, max_pages, page, FA_DTYPE[dtype], int(quant), (0, 0), (0, 0))
+    p = _pack_cache(B, total, H_kv, d, P, max_pages, page, FA_DTYPE[dtype], int(quant), 0, 0, 0, 0)
     with _on(k_pages):
-        st = lib().fa_cache_gather(ctypes.byref(p), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
+        st = lib().fa_cache_gather(p, k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
                                    _ptr(v_scales), page_table.data_ptr(), seqlens.data_ptr(), cu_k.data_ptr(),
                                    _ptr(starts), k_out.data_ptr(), v_out.data_ptr(), _stream_ptr(k_pages))
     if st != 0:
@@ -553,14 +582,14 @@ def cache_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch
     return k_out, v_out
 
 
-def _paged_problem(q, k_pages, page_table, max_q, causal, scale, window, quant) -> FaPagedProblem:
+def _paged_problem(q, k_pages, page_table, max_q, causal, scale, window, quant) -> bytes:
     T, H, d = q.shape
     P, H_kv, page, _ = k_pages.shape
     B, max_pages = page_table.shape
-    return FaPagedProblem(B, T, H, H_kv, int(max_q), P, max_pages, page, d,
+    return _pack_paged(B, T, H, H_kv, int(max_q), P, max_pages, page, d,
                           1.0 / math.sqrt(d) if scale is None else float(scale), int(bool(causal)),
                           -1 if window is None else int(window), FA_DTYPE[q.dtype], int(quant),
-                          (q.stride(0), q.stride(1)))
+                          q.stride(0), q.stride(1))
 
 
 def paged_workspace_size(q: torch.Tensor, k_pages: torch.Tensor, page_table: torch.Tensor, max_q: int) -> int:
@@ -568,7 +597,7 @@ def paged_workspace_size(q: torch.Tensor, k_pages: torch.Tensor, page_table: tor
     quant = k_pages.dtype == torch.float8_e4m3fn
     p = _paged_problem(q, k_pages, page_table, max_q, True, None, None, quant)
     with _on(q):
-        return int(lib().fa_paged_workspace_size(ctypes.byref(p)))
+        return int(lib().fa_paged_workspace_size(p))
 
 
 def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
@@ -593,19 +622,24 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
         raise ValueError(f"q {tuple(q.shape)} does not fit pages {tuple(k_pages.shape)} on {k_pages.device} "
                          "(key/value heads must divide the query heads)")
     check_buffer("cu_q", cu_q, (page_table.shape[0] + 1,), torch.int32, q.device)
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
-    lse = torch.empty((H, T), dtype=torch.float32, device=q.device) if lse is None else lse
-    check_buffer("out", out, q.shape, q.dtype, q.device)
-    check_buffer("lse", lse, (H, T), torch.float32, q.device)
+    if out is None:
+        out = _empty_like(q)
+    else:
+        check_buffer("out", out, q.shape, q.dtype, q.device)
+    if lse is None:
+        lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    else:
+        check_buffer("lse", lse, (H, T), torch.float32, q.device)
     if T == 0:
         return out, lse
     p = _paged_problem(q, k_pages, page_table, max_q, causal, scale, window, quant)
     with _on(q):
         if workspace is None:
-            need = int(lib().fa_paged_workspace_size(ctypes.byref(p)))
+            need = int(lib().fa_paged_workspace_size(p))
             workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-        check_scratch("workspace", workspace, q.device)
-        st = lib().fa_paged(ctypes.byref(p), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
+        else:
+            check_scratch("workspace", workspace, q.device)
+        st = lib().fa_paged(p, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
                             _ptr(v_scales), page_table.data_ptr(), seqlens.data_ptr(), cu_q.data_ptr(),
                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
                             workspace.numel() * workspace.element_size(), _stream_ptr(q))
