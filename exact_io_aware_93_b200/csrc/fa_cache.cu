@@ -57,6 +57,18 @@ fa::CacheArgs cache_args(const fa_cache_problem& p, const void* k_pages, const v
   return a;
 }
 
+// A warp takes as many rows, up to 8, as fill the 2048 elements that its four passes have in flight,
+// fewer while that leaves an SM less than 16 warps: what comes before its first load of the cache
+// (sequence, length, page number) is a chain of four loads.  1 / 2 / 4 / 8 rows:
+// 8K appended and 45K gathered rows of 640 elements, e4m3 pages: 37.7 / 29.0 / 28.1 / 32.2 us; 32K and
+// 32K of 2048 elements: 91.2 / 93.0 / 97.6 / 101.3 us; 64 and 64: 9.2 / 12.2 / 18.4 / 30.1 us.
+unsigned cache_blocks(fa::CacheArgs* a, int d, int sms) {
+  a->lg = 0;
+  while (a->lg < 3 && (2ll * a->H_kv * d) << a->lg < 2048 && a->T >> (a->lg + 1) >= 16 * sms) ++a->lg;
+  const unsigned warps = (static_cast<unsigned>(a->T) + (1u << a->lg) - 1) >> a->lg;
+  return (warps + 3) / 4;
+}
+
 template <Elem E, int D>
 void launch_append(const fa::CacheArgs& a, bool quant, unsigned blocks, cudaStream_t s) {
   quant ? fa::fa_cache_append_kernel<E, D, true><<<blocks, 128, 0, s>>>(a)
@@ -120,12 +132,19 @@ fa_status fa_rope(const fa_rope_problem* problem, const void* q, const void* k, 
   const fa_status st = fa::current_device(&di);
   if (st != FA_OK) return st;
   a.status = di->status;
-  // A block takes all heads of 4 tokens, so that one row of cosines serves every head; when
-  // that leaves SMs without a block, one token, and then a part of its heads.
+  // A block takes all heads of as many tokens, up to 16, as give each of its threads four items
+  // (what it has in flight at a time), so that one row of cosines serves every head; fewer while
+  // that leaves less than four blocks per SM, and of a single token a part of its heads when there
+  // are not two per SM.
+  // (5 heads of 128 x 16384 tokens, 4 / 16 tokens a block: 22.9 / 16.6 us; 32 heads, 4 / 8: 96.8 / 112.7.)
   const long long tokens = static_cast<long long>(p.B) * p.N;
   const int heads = p.H + p.H_k;
   const long long want = 2ll * di->sm_count;
-  a.tokens_per_block = tokens >= 4 * want ? 4 : 1;
+  const long long items = static_cast<long long>(heads) * (p.d >= 16 ? p.d / 16 : 1);
+  int tpb = 1;
+  while (tpb < 16 && tpb * items < 4 * fa::kRopeThreads && 2 * tpb * p.rotary_dim <= 8192 && tokens >= 4 * tpb * want)
+    tpb *= 2;
+  a.tokens_per_block = tpb;
   const long long bx = (tokens + a.tokens_per_block - 1) / a.tokens_per_block;
   long long by = bx >= want ? 1 : (want + bx - 1) / bx;
   by = by > heads ? heads : by;
@@ -164,7 +183,7 @@ fa_status fa_cache_append(const fa_cache_problem* problem, const void* k, const 
     a.ks[i] = p.k_stride[i];
     a.vs[i] = p.v_stride[i];
   }
-  const unsigned blocks = (static_cast<unsigned>(p.T) + 3) / 4;
+  const unsigned blocks = cache_blocks(&a, p.d, di->sm_count);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.dtype == FA_DTYPE_F16)
     p.d == 128 ? launch_append<Elem::kF16, 128>(a, p.quant, blocks, s)
@@ -194,7 +213,7 @@ fa_status fa_cache_gather(const fa_cache_problem* problem, const void* k_pages, 
   a.k_out = k_out;
   a.v_out = v_out;
   a.starts = starts;
-  const unsigned blocks = (static_cast<unsigned>(p.T) + 3) / 4;
+  const unsigned blocks = cache_blocks(&a, p.d, di->sm_count);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.dtype == FA_DTYPE_F16)
     p.d == 128 ? launch_gather<Elem::kF16, 128>(a, p.quant, blocks, s)

@@ -74,20 +74,41 @@ __device__ __forceinline__ float2 rope_pair(float x0, float x1, float c, float s
   return make_float2(fmaf(x0, c, -__fmul_rn(x1, s)), fmaf(x1, c, __fmul_rn(x0, s)));
 }
 
-// Element offset of (token t, head h) in q (h < H) or k; *which says which.
-__device__ __forceinline__ int64_t rope_offset(const RopeArgs& a, const int64_t (&st)[2][3], int64_t t, int h,
-                                               int* which) {
-  const int w = h >= a.H;
-  *which = w;
-  return (t / a.N) * st[w][0] + (t % a.N) * st[w][1] + (h - (w ? a.H : 0)) * st[w][2];
-}
+// The rows (token, head) of a block in order, `step` apart: a thread divides once and then adds,
+// since two divisions per row, 64 bits wide for the batch, took as many instructions as the rotation.
+struct RopeRow {
+  int b, n;   // the block's first token: batch row and place in it
+  int tk, h;  // this row's token, from that one on, and head among the block's
+  int dt, dh; // what a step adds
+  __device__ __forceinline__ RopeRow(const RopeArgs& a, int64_t t0, int nh, int row, int step)
+      : b(static_cast<int>(t0 / a.N)), n(static_cast<int>(t0 - static_cast<int64_t>(b) * a.N)), tk(row / nh),
+        h(row - tk * nh), dt(step / nh), dh(step - dt * nh) {}
+  __device__ __forceinline__ void next(int nh) {
+    tk += dt;
+    h += dh;
+    if (h >= nh) {
+      h -= nh;
+      ++tk;
+    }
+  }
+  // Element offset of head `head` of all (q's, then k's); w says which.
+  __device__ __forceinline__ int64_t offset(const RopeArgs& a, const int64_t (&st)[2][3], int head, int w) const {
+    int bb = b;
+    unsigned nn = static_cast<unsigned>(n) + tk;
+    if (nn >= static_cast<unsigned>(a.N)) {
+      bb += static_cast<int>(nn / a.N);
+      nn %= a.N;
+    }
+    return bb * st[w][0] + nn * st[w][1] + (head - (w ? a.H : 0)) * st[w][2];
+  }
+};
 
 // Rows of whole 16-element items (R and d multiples of 16, 16-byte aligned rows): a thread
 // owns one item of a head for several rows, 32 bytes in and out per row, and issues four
 // rows' loads before it needs the first.  The block's cos/sin are computed once per token and
 // serve all its heads.
 template <Elem E, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 4) fa_rope_kernel(const RopeArgs a) {
   using T = typename ElemOps<E>::T;
   extern __shared__ __align__(16) float tab[];
   constexpr int U = 4;
@@ -107,19 +128,18 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeArgs a)
   const int c0 = (turned && !INTERLEAVED) ? item * 8 : item * 16;
   const int c1 = (turned && !INTERLEAVED) ? half + item * 8 : item * 16 + 8;
   uint4 v0[U], v1[U];
+  RopeRow in(a, t0, nh, r0, step), out = in;
   auto load = [&](int base) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int row = base + u * step;
-      if (r0 < step && row < rows) {
-        int w;
-        const int tk = row / nh;
-        const int64_t off = rope_offset(a, a.xs, t0 + tk, h0 + row - tk * nh, &w);
-        const T* x = static_cast<const T*>(a.x[w]) + off;
-        if (FA_IN_BOUNDS(t0 + tk < static_cast<int64_t>(a.B) * a.N && c1 + 8 <= a.d, a.status, 401)) {
+      if (r0 < step && base + u * step < rows) {
+        const int w = h0 + in.h >= a.H;
+        const T* x = static_cast<const T*>(a.x[w]) + in.offset(a, a.xs, h0 + in.h, w);
+        if (FA_IN_BOUNDS(t0 + in.tk < static_cast<int64_t>(a.B) * a.N && c1 + 8 <= a.d, a.status, 401)) {
           v0[u] = *reinterpret_cast<const uint4*>(x + c0);  // plain loads: y may be x
           v1[u] = *reinterpret_cast<const uint4*>(x + c1);
         }
+        in.next(nh);
       }
     }
   };
@@ -130,9 +150,8 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeArgs a)
     if (base != r0) load(base);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int row = base + u * step;
-      if (row >= rows) break;
-      const int tk = row / nh;
+      if (base + u * step >= rows) break;
+      const int tk = out.tk;
       uint32_t* p0 = &v0[u].x;
       uint32_t* p1 = &v1[u].x;
       if (turned) {
@@ -160,13 +179,13 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeArgs a)
           }
         }
       }
-      int w;
-      const int64_t off = rope_offset(a, a.ys, t0 + tk, h0 + row - tk * nh, &w);
-      T* y = static_cast<T*>(a.y[w]) + off;
+      const int w = h0 + out.h >= a.H;
+      T* y = static_cast<T*>(a.y[w]) + out.offset(a, a.ys, h0 + out.h, w);
       if (FA_IN_BOUNDS(t0 + tk < static_cast<int64_t>(a.B) * a.N && c1 + 8 <= a.d, a.status, 402)) {
         *reinterpret_cast<uint4*>(y + c0) = v0[u];
         *reinterpret_cast<uint4*>(y + c1) = v1[u];
       }
+      out.next(nh);
     }
   }
 }
@@ -186,15 +205,15 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_any_kernel(const RopeArg
   __syncthreads();
   const int per = a.d - half;  // pairs, then copied columns
   const int rows = nt * nh;
+  RopeRow at(a, t0, nh, 0, 1);
   for (int i = threadIdx.x; i < rows * per; i += kRopeThreads) {
     const int row = i / per;
     const int e = i - row * per;
     const int tk = row / nh;
-    int w;
-    const int64_t xo = rope_offset(a, a.xs, t0 + tk, h0 + row - tk * nh, &w);
-    const int64_t yo = rope_offset(a, a.ys, t0 + tk, h0 + row - tk * nh, &w);
-    const T* x = static_cast<const T*>(a.x[w]) + xo;
-    T* y = static_cast<T*>(a.y[w]) + yo;
+    const int head = h0 + row - tk * nh, w = head >= a.H;
+    at.tk = tk;
+    const T* x = static_cast<const T*>(a.x[w]) + at.offset(a, a.xs, head, w);
+    T* y = static_cast<T*>(a.y[w]) + at.offset(a, a.ys, head, w);
     if (!FA_IN_BOUNDS(t0 + tk < static_cast<int64_t>(a.B) * a.N && half + e < a.d, a.status, 403)) continue;
     if (e >= half) {
       y[half + e] = x[half + e];
@@ -225,6 +244,7 @@ struct CacheArgs {
   const int* cu;          // [B + 1] offsets of the batch's rows
   const int* starts;      // gather: first position of each sequence, or null (0)
   int B, T, H_kv, max_pages, page, P;
+  int lg;                 // log2 of a warp's rows
   int* status;
 };
 
@@ -243,15 +263,30 @@ __device__ __forceinline__ int find_seq(const int* cu, int B, int t, int lane) {
   return lo;
 }
 
+// The sequence of row t + lane, `first` being row t's.
+__device__ __forceinline__ int find_seq_from(const int* cu, int B, int first, int t) {
+  int lo = first, hi = B;  // cu[lo] <= t < cu[hi + 1], if hi < B
+  while (lo < hi && __ldg(cu + lo + 1) <= t) {
+    const int mid = lo + 1 + (hi - lo - 1) / 2;
+    if (__ldg(cu + mid) <= t) {
+      lo = mid;
+    } else {
+      hi = mid - 1;
+      ++lo;
+    }
+  }
+  return lo;
+}
+
 // Where position `pos` of sequence b lies: the row index (page * H_kv) * slots + slot of head
 // 0, or -1 (recorded) for a position or page number out of range.
-__device__ __forceinline__ int64_t cache_row(const CacheArgs& a, int b, int64_t pos, int lane, int site) {
+__device__ __forceinline__ int64_t cache_row(const CacheArgs& a, int b, int64_t pos, int site) {
   int64_t at = -1;
   if (pos >= 0 && pos < static_cast<int64_t>(a.max_pages) * a.page) {
     const int pg = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + pos / a.page);
     if (pg >= 0 && pg < a.P) at = (static_cast<int64_t>(pg) * a.H_kv) * a.page + pos % a.page;
   }
-  if (at < 0 && lane == 0) plan_fail(a.status, site);
+  if (at < 0) plan_fail(a.status, site);
   return at;
 }
 
@@ -278,28 +313,31 @@ __device__ __forceinline__ int e4m3_exponent(float amax) {
   return E == Elem::kF16 ? min(max(e, -15), 8) : min(max(e, -126), 119);
 }
 
-// Appends row t (one warp per row) of the new keys and values at its position: the last
-// position of its sequence is seqlens[b] - 1.  Lanes own 16 elements of a head; up to four
-// heads' rows per lane are loaded before the position is known.
+// Appends rows of the new keys and values at their positions: the last position of a sequence is
+// seqlens[b] - 1.  A warp takes 2^lg rows (a lane finds where one lies) and its lanes 16 elements of
+// a head each, the rows of one head side by side: their slots, and the scales, are neighbours in a
+// page.  The first four passes' elements are loaded before the positions are known.
 template <Elem E, int D, bool Q8>
 __global__ void __launch_bounds__(128) fa_cache_append_kernel(const CacheArgs a) {
   using T = typename ElemOps<E>::T;
   constexpr int L = D / 16;    // lanes per row
   constexpr int RW = 32 / L;   // rows per pass
   constexpr int U = 4;
+  constexpr unsigned kFull = 0xffffffffu;
   const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (t >= a.T) return;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5)) << a.lg;
+  if (t0 >= a.T) return;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(1) << a.lg, a.T - t0));
   const int item = lane % L;
-  const int rows = 2 * a.H_kv;  // the keys' heads, then the values'
+  const int rows = (2 * a.H_kv) << a.lg;  // the keys' heads, then the values', each of all tokens
   uint4 x0[U], x1[U];
   auto load = [&](int base) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r = base + u * RW;
-      if (r < rows) {
+      const int row = base + u * RW, tk = row & ((1 << a.lg) - 1), r = row >> a.lg;
+      if (row < rows && tk < nt) {
         const bool isv = r >= a.H_kv;
-        const T* src = static_cast<const T*>(isv ? a.v : a.k) + t * (isv ? a.vs[0] : a.ks[0]) +
+        const T* src = static_cast<const T*>(isv ? a.v : a.k) + (t0 + tk) * (isv ? a.vs[0] : a.ks[0]) +
                        (isv ? r - a.H_kv : r) * (isv ? a.vs[1] : a.ks[1]) + item * 16;
         x0[u] = __ldg(reinterpret_cast<const uint4*>(src));
         x1[u] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
@@ -307,20 +345,28 @@ __global__ void __launch_bounds__(128) fa_cache_append_kernel(const CacheArgs a)
     }
   };
   load(lane / L);
-  const int b = find_seq(a.cu, a.B, static_cast<int>(t), lane);
-  if (b >= a.B) return;  // behind the last sequence
-  const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
-  const int64_t pos = static_cast<int64_t>(__ldg(a.seqlens + b)) - (static_cast<int64_t>(c1) - c0) + (t - c0);
-  const int64_t at = t < c0 ? -1 : cache_row(a, b, pos, lane, 41);
-  if (at < 0) return;
+  const int first = find_seq(a.cu, a.B, static_cast<int>(t0), lane);
+  int64_t mine = -1;  // of row t0 + lane
+  if (lane < nt) {
+    const int t = static_cast<int>(t0) + lane;
+    const int b = find_seq_from(a.cu, a.B, first, t);
+    if (b < a.B) {  // else behind the last sequence
+      const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
+      const int64_t pos = static_cast<int64_t>(__ldg(a.seqlens + b)) - (static_cast<int64_t>(c1) - c0) + (t - c0);
+      if (t >= c0) mine = cache_row(a, b, pos, 41);
+    }
+  }
+  if (__all_sync(kFull, mine < 0)) return;
   for (int base = 0; base < rows; base += U * RW) {
     if (base != 0) load(base + lane / L);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (base + u * RW >= rows) break;  // the same for the whole warp: all lanes shuffle
-      const int r = base + u * RW + lane / L;
-      const bool live = r < rows;
+      const int idx = base + u * RW + lane / L;
+      const int tk = idx & ((1 << a.lg) - 1), r = idx >> a.lg;
       const bool isv = r >= a.H_kv;
+      const int64_t at = __shfl_sync(kFull, mine, tk);
+      const bool live = idx < rows && at >= 0;
       const int64_t row = at + static_cast<int64_t>(isv ? r - a.H_kv : r) * a.page;
       const bool in = live && FA_IN_BOUNDS(row >= 0 && row < static_cast<int64_t>(a.P) * a.H_kv * a.page, a.status, 404);
       if constexpr (!Q8) {
@@ -370,37 +416,47 @@ __global__ void __launch_bounds__(128) fa_cache_append_kernel(const CacheArgs a)
   }
 }
 
-// Reads row t (one warp per row) of a ragged batch back from the cache: row cu[b] + i is
-// position starts[b] + i of sequence b.  Rows whose position is at or past the sequence's
-// length, and rows behind the last sequence, are left as they were.
+// Reads rows of a ragged batch back from the cache: row cu[b] + i is position starts[b] + i of
+// sequence b.  Rows whose position is at or past the sequence's length, and rows behind the last
+// sequence, are left as they were.  Warps and lanes as in the append.
 template <Elem E, int D, bool Q8>
 __global__ void __launch_bounds__(128) fa_cache_gather_kernel(const CacheArgs a) {
   using T = typename ElemOps<E>::T;
   constexpr int L = D / 16;
   constexpr int RW = 32 / L;
   constexpr int U = 4;
+  constexpr unsigned kFull = 0xffffffffu;
   const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (t >= a.T) return;
-  const int b = find_seq(a.cu, a.B, static_cast<int>(t), lane);
-  if (b >= a.B) return;
-  const int c0 = __ldg(a.cu + b);
-  const int64_t pos = (a.starts ? static_cast<int64_t>(__ldg(a.starts + b)) : 0) + (t - c0);
-  if (t < c0 || pos >= __ldg(a.seqlens + b)) return;
-  const int64_t at = cache_row(a, b, pos, lane, 42);
-  if (at < 0) return;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5)) << a.lg;
+  if (t0 >= a.T) return;
+  const int first = find_seq(a.cu, a.B, static_cast<int>(t0), lane);
+  int64_t mine = -1;
+  if (lane < 1 << a.lg && t0 + lane < a.T) {
+    const int t = static_cast<int>(t0) + lane;
+    const int b = find_seq_from(a.cu, a.B, first, t);
+    if (b < a.B) {
+      const int c0 = __ldg(a.cu + b);
+      const int64_t pos = (a.starts ? static_cast<int64_t>(__ldg(a.starts + b)) : 0) + (t - c0);
+      if (t >= c0 && pos < __ldg(a.seqlens + b)) mine = cache_row(a, b, pos, 42);
+    }
+  }
+  if (__all_sync(kFull, mine < 0)) return;
   const int item = lane % L;
-  const int rows = 2 * a.H_kv;
-  for (int base = lane / L; base < rows; base += U * RW) {
+  const int rows = (2 * a.H_kv) << a.lg;
+  for (int base = 0; base < rows; base += U * RW) {
     uint4 x0[U], x1[U];
     uint32_t sc[U];
+    bool live[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r = base + u * RW;
-      if (r >= rows) break;
+      const int idx = base + u * RW + lane / L;
+      const int r = idx >> a.lg;
+      const int64_t at = __shfl_sync(kFull, mine, idx & ((1 << a.lg) - 1));
       const bool isv = r >= a.H_kv;
       const int64_t row = at + static_cast<int64_t>(isv ? r - a.H_kv : r) * a.page;
-      if (!FA_IN_BOUNDS(row >= 0 && row < static_cast<int64_t>(a.P) * a.H_kv * a.page, a.status, 405)) continue;
+      live[u] = idx < rows && at >= 0 &&
+                FA_IN_BOUNDS(row >= 0 && row < static_cast<int64_t>(a.P) * a.H_kv * a.page, a.status, 405);
+      if (!live[u]) continue;
       if constexpr (Q8) {
         x0[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(isv ? a.v_pages : a.k_pages) +
                                                      row * D + item * 16));
@@ -414,8 +470,10 @@ __global__ void __launch_bounds__(128) fa_cache_gather_kernel(const CacheArgs a)
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r = base + u * RW;
-      if (r >= rows) break;
+      if (!live[u]) continue;
+      const int idx = base + u * RW + lane / L;
+      const int r = idx >> a.lg;
+      const int64_t t = t0 + (idx & ((1 << a.lg) - 1));
       const bool isv = r >= a.H_kv;
       if constexpr (Q8) {
         const float f = e8m0_to_float(sc[u]);
