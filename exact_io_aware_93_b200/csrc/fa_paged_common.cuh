@@ -568,16 +568,23 @@ __global__ void __launch_bounds__(256) fa_paged_scale_q_kernel(const void* q, in
 // ---------------------------------------------------------------- joining the partial results
 // Per row: LSE = log sum_s exp(lse_s) and O = sum_s exp(lr_s - LR) O_s with LR = log sum_s
 // exp(lr_s), the convex combination one CTA would have formed.  Blocks (c, y) with c < `ctas` take
-// the unit that CTA c began and did not finish, W warps per row; further blocks c = ctas + b give
-// the rows of sequence b's units without keys O = 0, LSE = -inf.  All other rows were written by
-// their CTA.
-template <int D, Elem E, typename Cfg, int W, int kThreads>
+// the unit that CTA c began and did not finish; further blocks c = ctas + b give the rows of
+// sequence b's units without keys O = 0, LSE = -inf.  All other rows were written by their CTA.
+//
+// A warp takes 32 / L rows at a time: L lanes form the weights of a row's next L partial results,
+// then all 32 lanes share each row's columns.  Tiles of 128 leave many rows of two or three partial
+// results: L = 16 has two rows' loads in flight per chain of dependent loads (L = 8 / 16 / 32: a call
+// with 2048 tokens at 32K 1042 / 1044 / 1098 us, one of 24 sequences of 30 rows 70.5 / 68.0 / 66.6).
+// Few rows leave up to a hundred partial results: L = 32, and W warps share a row's.
+template <int D, Elem E, typename Cfg, int L, int W, int kThreads>
 __global__ void __launch_bounds__(kThreads) fa_paged_merge_kernel(const PgArgs a, int ctas) {
   using T = typename ElemOps<E>::T;
   constexpr unsigned kFull = 0xffffffffu;
-  constexpr int V = D / 32;  // columns per lane
-  constexpr int kRowsAtOnce = kThreads / 32 / W;
-  __shared__ float acc_sh[W > 1 ? W : 1][D];
+  constexpr int V = D / 32;       // columns per lane
+  constexpr int R = 32 / L;       // rows per warp
+  constexpr int kRowsAtOnce = kThreads / 32 / W * R;
+  static_assert(W == 1 || (R == 1 && kThreads == 32 * W), "warps that share a row are a block");
+  __shared__ float acc_sh[W][D];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int G = a.H / a.H_kv;
@@ -605,96 +612,113 @@ __global__ void __launch_bounds__(kThreads) fa_paged_merge_kernel(const PgArgs a
   const PgSplit sp = a.splits[blockIdx.x];
   const int rows = G * sp.ntok;
   if (sp.parts == 0) return;
-  for (int row = blockIdx.y * kRowsAtOnce + warp / W; row < rows; row += gridDim.y * kRowsAtOnce) {
+  const int share = W > 1 ? warp : 0;
+  // where a row lies in each partial result, and partial result i: the beginning is in its CTA's
+  // second slot
+  auto in_part = [&](int row) -> int {
     const int tile = row / (G * a.TQ);
-    const int rc = row - tile * G * a.TQ;
-    const int iq = row / G, h = sp.kvh * G + (row - iq * G);
-    const int64_t token = static_cast<int64_t>(sp.q0) + iq;
-    // index of partial result i of this row: the beginning lies in its CTA's second slot
-    auto at = [&](int i) -> int64_t {
-      const int slot = 2 * (static_cast<int>(blockIdx.x) + i) + (i == 0);
-      return (static_cast<int64_t>(slot) * Cfg::kSubs + tile) * Cfg::kRows + rc;
-    };
+    return tile * Cfg::kRows + row - tile * G * a.TQ;
+  };
+  auto part = [&](int i) -> int64_t {
+    return static_cast<int64_t>(2 * (static_cast<int>(blockIdx.x) + i) + (i == 0)) * (Cfg::kSubs * Cfg::kRows);
+  };
+  for (int row0 = blockIdx.y * kRowsAtOnce + (W > 1 ? 0 : warp * R); row0 < rows; row0 += gridDim.y * kRowsAtOnce) {
+    // this lane's row and partial results sl, sl + L, ..; behind the last row the last again, not stored
+    const int mine_at = in_part(min(row0 + lane / L, rows - 1)), sl = lane % L;
+    const float* po[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      po[r] = a.part_o + static_cast<int64_t>(__shfl_sync(kFull, mine_at, r * L)) * D + lane * V;
     float mx_l = -INFINITY, mx_r = -INFINITY, s_l = 0.f, s_r = 0.f;
     float2 mine = make_float2(-INFINITY, -INFINITY);  // of the lane's last partial result
-    for (int i = lane; i < sp.parts; i += 32) {
-      const int64_t x = at(i);
+    for (int i = sl; i < sp.parts; i += L) {
+      const int64_t x = part(i) + mine_at;
       if (!FA_IN_BOUNDS(x >= 0 && x < a.slots * Cfg::kSubs * Cfg::kRows, a.status, 508)) continue;
       mine = *reinterpret_cast<const float2*>(a.part_lse + x * 2);
       mx_l = fmaxf(mx_l, mine.x);
       mx_r = fmaxf(mx_r, mine.y);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = L / 2; o > 0; o >>= 1) {
       mx_l = fmaxf(mx_l, __shfl_xor_sync(kFull, mx_l, o));
       mx_r = fmaxf(mx_r, __shfl_xor_sync(kFull, mx_r, o));
     }
     if (mx_l == -INFINITY) mx_l = 0.f;  // no key, or NaN only: the sums decide
     if (mx_r == -INFINITY) mx_r = 0.f;
-    for (int i = lane; i < sp.parts; i += 32) {
-      if (sp.parts > 32) mine = *reinterpret_cast<const float2*>(a.part_lse + at(i) * 2);
+    for (int i = sl; i < sp.parts; i += L) {
+      if (sp.parts > L) mine = *reinterpret_cast<const float2*>(a.part_lse + (part(i) + mine_at) * 2);
       s_l += expf(mine.x - mx_l);
       s_r += expf(mine.y - mx_r);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = L / 2; o > 0; o >>= 1) {
       s_l += __shfl_xor_sync(kFull, s_l, o);
       s_r += __shfl_xor_sync(kFull, s_r, o);
     }
-    float acc[V];
+    float acc[R][V];
 #pragma unroll
-    for (int x = 0; x < V; ++x) acc[x] = 0.f;
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int x = 0; x < V; ++x) acc[r][x] = 0.f;
     const float inv = s_r == 0.f ? 0.f : 1.0f / s_r;
-    // 32 partial results at a time: a lane forms one weight, then the warp sums the rows with
-    // the weights broadcast; a partial result without keys was not written and is not read
-    for (int base = (W > 1 ? (warp % W) * 32 : 0); base < sp.parts; base += 32 * W) {
+    for (int base = share * L; base < sp.parts; base += L * W) {
+      // a partial result without keys was not written and is not read
       float wl = 0.f;
-      if (base + lane < sp.parts) {
-        const float v = sp.parts > 32 ? a.part_lse[at(base + lane) * 2 + 1] : mine.y;
+      if (base + sl < sp.parts) {
+        const float v = sp.parts > L ? a.part_lse[(part(base + sl) + mine_at) * 2 + 1] : mine.y;
         wl = v == -INFINITY ? 0.f : expf(v - mx_r) * inv;
       }
-      const int cnt = min(32, sp.parts - base);
-#pragma unroll 4
+      const int cnt = min(L, sp.parts - base);
+#pragma unroll(R > 1 ? 1 : 4)
       for (int t = 0; t < cnt; ++t) {
-        const float wgt = __shfl_sync(kFull, wl, t);
-        if (wgt == 0.f) continue;
-        const float* po = a.part_o + at(base + t) * D + lane * V;
-        if constexpr (V == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(po);
-          acc[0] = fmaf(wgt, v.x, acc[0]);
-          acc[1] = fmaf(wgt, v.y, acc[1]);
-          acc[2] = fmaf(wgt, v.z, acc[2]);
-          acc[3] = fmaf(wgt, v.w, acc[3]);
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(po);
-          acc[0] = fmaf(wgt, v.x, acc[0]);
-          acc[1] = fmaf(wgt, v.y, acc[1]);
+        const int64_t from = part(base + t) * D;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float wgt = __shfl_sync(kFull, wl, r * L + t);
+          if (wgt == 0.f) continue;
+          if constexpr (V == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(po[r] + from);
+            acc[r][0] = fmaf(wgt, v.x, acc[r][0]);
+            acc[r][1] = fmaf(wgt, v.y, acc[r][1]);
+            acc[r][2] = fmaf(wgt, v.z, acc[r][2]);
+            acc[r][3] = fmaf(wgt, v.w, acc[r][3]);
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(po[r] + from);
+            acc[r][0] = fmaf(wgt, v.x, acc[r][0]);
+            acc[r][1] = fmaf(wgt, v.y, acc[r][1]);
+          }
         }
       }
     }
-    if constexpr (W > 1) {  // one row per block at a time
+    if constexpr (W > 1) {
 #pragma unroll
-      for (int x = 0; x < V; ++x) acc_sh[warp][lane * V + x] = acc[x];
+      for (int x = 0; x < V; ++x) acc_sh[warp][lane * V + x] = acc[0][x];
       __syncthreads();
       if (warp == 0) {
 #pragma unroll
         for (int x = 0; x < V; ++x) {
-          acc[x] = 0.f;
+          acc[0][x] = 0.f;
 #pragma unroll
-          for (int y = 0; y < W; ++y) acc[x] += acc_sh[y][lane * V + x];
+          for (int y = 0; y < W; ++y) acc[0][x] += acc_sh[y][lane * V + x];
         }
       }
       __syncthreads();
       if (warp != 0) continue;
     }
-    if (FA_IN_BOUNDS(token >= 0 && token < a.T && h < a.H, a.status, 509)) {
-      T* orow = static_cast<T*>(a.out) + (token * a.H + h) * D + lane * V;
-      if constexpr (V == 4)
-        *reinterpret_cast<uint2*>(orow) =
-            make_uint2(ElemOps<E>::pack(acc[0], acc[1]), ElemOps<E>::pack(acc[2], acc[3]));
-      else
-        *reinterpret_cast<uint32_t*>(orow) = ElemOps<E>::pack(acc[0], acc[1]);
-      if (lane == 0) a.lse[static_cast<int64_t>(h) * a.T + token] = s_l == 0.f ? -INFINITY : mx_l + logf(s_l);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (row0 + r >= rows) break;
+      const int iq = (row0 + r) / G, h = sp.kvh * G + row0 + r - iq * G;
+      const int64_t token = static_cast<int64_t>(sp.q0) + iq;
+      if (FA_IN_BOUNDS(token >= 0 && token < a.T && h < a.H, a.status, 509)) {
+        T* orow = static_cast<T*>(a.out) + (token * a.H + h) * D + lane * V;
+        if constexpr (V == 4)
+          *reinterpret_cast<uint2*>(orow) =
+              make_uint2(ElemOps<E>::pack(acc[r][0], acc[r][1]), ElemOps<E>::pack(acc[r][2], acc[r][3]));
+        else
+          *reinterpret_cast<uint32_t*>(orow) = ElemOps<E>::pack(acc[r][0], acc[r][1]);
+        if (lane == r * L) a.lse[static_cast<int64_t>(h) * a.T + token] = s_l == 0.f ? -INFINITY : mx_l + logf(s_l);
+      }
     }
   }
 }

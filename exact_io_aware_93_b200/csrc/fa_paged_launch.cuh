@@ -98,13 +98,12 @@ fa_status launch_paged(DeviceInfo& di, const PagedCall& c, int n_lo, int n_hi) {
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
   }
   if (!launch_after(Q8, kern, dim3(grid), Cfg::kThreads, smem, c.stream, mq, mk, mv, a)) return FA_ERR_LAUNCH;
-  // few rows: a block per row, its four warps sharing the partial results; otherwise eight blocks of
-  // eight warps, a row each at a time
+  // few rows: a block of four warps per row; otherwise eight blocks of eight warps, two rows each
   bool ok;
   if constexpr (kFew)
-    ok = launch_after(true, fa_paged_merge_kernel<D, E, Cfg, 4, 128>, dim3(grid + p.B, G * TQ), 128, 0, c.stream, a, grid);
+    ok = launch_after(true, fa_paged_merge_kernel<D, E, Cfg, 32, 4, 128>, dim3(grid + p.B, G * TQ), 128, 0, c.stream, a, grid);
   else
-    ok = launch_after(true, fa_paged_merge_kernel<D, E, Cfg, 1, 256>, dim3(grid + p.B, 8), 256, 0, c.stream, a, grid);
+    ok = launch_after(true, fa_paged_merge_kernel<D, E, Cfg, 16, 1, 256>, dim3(grid + p.B, 8), 256, 0, c.stream, a, grid);
   return ok ? FA_OK : FA_ERR_LAUNCH;
 }
 
