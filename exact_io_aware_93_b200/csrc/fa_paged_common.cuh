@@ -497,12 +497,12 @@ __device__ __forceinline__ void pg_clean(const PgSeg& g, int j, uint8_t* tile, i
 
 // ---------------------------------------------------------------- queries for e4m3 pages
 // Every query row is scaled by a power of two, 2^e the smallest with max|row| <= 448 * 2^e, and
-//   kPieces   cut into two e4m3 pieces: the rounding of q / 2^e and that of the rest; exact for
-//             bf16, 8 significant bits of an fp16's 11, down to 2^-18 of the row's largest
-//   otherwise written as fp16: exact for both types, down to 2^-33 of the row's largest
+//   kPieces   cut into that many e4m3 pieces, each the rounding of what the ones before it left:
+//             two hold a bf16, three an fp16, exactly, down to 2^-18 of the row's largest
+//   0         written as fp16: exact for both types, down to 2^-33 of the row's largest
 // Piece i of (token, head) lies at out[((i T + token) H + head) D], fp16 rows likewise; factors
 // 2^e at q_scale[token H + head].  D / 16 lanes per row.
-template <int D, Elem E, bool kPieces>
+template <int D, Elem E, int kPieces>
 __global__ void __launch_bounds__(256) fa_paged_scale_q_kernel(const void* q, int64_t token_stride, int64_t head_stride,
                                                                uint8_t* out, float* q_scale, int T, int H,
                                                                int* status) {
@@ -538,9 +538,9 @@ __global__ void __launch_bounds__(256) fa_paged_scale_q_kernel(const void* q, in
   if (!live || !FA_IN_BOUNDS(token < T && h < H && item * 16 + 16 <= D, status, 510)) return;
 #pragma unroll
   for (int i = 0; i < 16; ++i) f[i] *= inv;
-  if constexpr (kPieces) {
+  if constexpr (kPieces > 0) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
+    for (int p = 0; p < kPieces; ++p) {
       uint32_t c[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

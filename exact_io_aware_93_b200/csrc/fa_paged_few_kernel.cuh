@@ -19,12 +19,13 @@
 //
 // e4m3 pages.  The codes are operands as they are (kind::f8f6f4): a tile moves half the bytes and
 // nothing is converted.
-//   Q   two e4m3 pieces per row (fa_paged_scale_q_kernel), as rows r and RW + r of the tile: the
-//       two score columns are added by the key's thread
-//   P   the weight, an fp16 value rounded to 9 bits, is the sum of three e5m2 pieces (e5m2 is the
-//       upper byte of an fp16): relative error 2^-9 down to 2^-23 of the largest weight.  e5m2
-//       and not e4m3 for its range: a long tail of small weights beside a large one keeps its
-//       mass.  The pieces are rows of P^T, their products columns of O^T, added at the end.
+//   Q   e4m3 pieces per row (fa_paged_scale_q_kernel), two of a bf16 and three of an fp16 row, as
+//       rows r, RW + r, .. of the tile: the score columns are added by the key's thread
+//   P   the weight, an fp16 value, is the sum of e5m2 pieces (e5m2 is the upper byte of an fp16):
+//       three hold 9 bits, one more than bf16, and four all 11, for fp16 outputs; down to 2^-23 of
+//       the largest weight.  e5m2 and not e4m3 for its range: a long tail of small weights beside
+//       a large one keeps its mass.  The pieces are rows of P^T, their products columns of O^T,
+//       added at the end.
 //   scales  a key's 2^ek and 2^(ev - E) are one number each for its thread; E is the largest
 //       value exponent of the group's tiles so far (O^T is rescaled when it grows).  The bytes
 //       come with the K tile, into a ring of their own that the softmax groups free.
@@ -37,14 +38,16 @@
 #pragma once
 
 #include "fa_paged_common.cuh"
+#include "fa_paged_launch.h"
 
 namespace fa {
 
-constexpr int kPPieces = 3;      // e5m2 pieces of a weight
 constexpr float kPShift = 7.0f;  // weights cut into pieces are 2^(x - m + 7) <= 2^15
 
-template <int D, bool Q8, int RW>
+template <int D, Elem E, bool Q8, int RW>
 struct PfCfg {
+  static constexpr int kQPieces = paged_q_pieces(E == Elem::kF16);  // e4m3 pieces of a query
+  static constexpr int kPPieces = E == Elem::kF16 ? 4 : 3;  // e5m2 pieces of a weight
   static constexpr int kRows = RW;      // rows of a tile and of a partial result
   static constexpr int kSubs = 1;
   static constexpr int kPairCost = 1;   // units are single tiles
@@ -58,15 +61,15 @@ struct PfCfg {
   static constexpr int kChunks = Q8 ? 1 : D / 64;
   static constexpr int kChunkBytes = 128 * kRowBytes;
   static constexpr int kTileBytes = kChunks * kChunkBytes;
-  // N of the products: rows, or two pieces of each; and three pieces, in whole 16s
-  static constexpr int kNS = Q8 ? 2 * RW : (RW < 16 ? 16 : RW);
-  static constexpr int kNO = Q8 ? (3 * RW + 15) / 16 * 16 : (RW < 16 ? 16 : RW);
+  // N of the products: rows, or all pieces of each, in whole 16s
+  static constexpr int kNS = ((Q8 ? kQPieces : 1) * RW + 15) / 16 * 16;
+  static constexpr int kNO = ((Q8 ? kPPieces : 1) * RW + 15) / 16 * 16;
   static constexpr int kQPartBytes = kNS * kRowBytes;
   static constexpr int kQBytes = kChunks * kQPartBytes;
   static constexpr int kPChunks = Q8 ? 1 : 2;         // 128 keys of a row in 128-byte chunks
   static constexpr int kPChunkBytes = kNO * 128;
   static constexpr int kPBytes = kPChunks * kPChunkBytes;
-  static constexpr int kStages = (Q8 ? (RW == 32 ? 10 : 12) : (RW == 32 ? 5 : 6)) * (128 / D);
+  static constexpr int kStages = (Q8 ? (RW == 32 ? 10 : (RW == 16 && E == Elem::kF16 ? 11 : 12)) : 6) * (128 / D);
   static constexpr int kScaleRing = 8;  // key tiles
   static constexpr int kSegRing = 4;
   static constexpr int kSegReaders = 10;  // warps
@@ -76,9 +79,9 @@ struct PfCfg {
   static_assert(kCols <= 512 && RW % 8 == 0, "tensor memory");
 };
 
-template <int D, bool Q8, int RW>
+template <int D, Elem E, bool Q8, int RW>
 struct __align__(1024) PfSmem {
-  using Cfg = PfCfg<D, Q8, RW>;
+  using Cfg = PfCfg<D, E, Q8, RW>;
   uint8_t kv[Cfg::kStages][Cfg::kTileBytes];
   uint8_t q[2][Cfg::kQBytes];
   uint8_t p[2][Cfg::kPBytes];               // each group's P^T
@@ -136,7 +139,7 @@ template <int D, Elem E, bool Q8, int RW>
 __global__ void __launch_bounds__(384, 1)
     fa_paged_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const PgArgs a) {
-  using Cfg = PfCfg<D, Q8, RW>;
+  using Cfg = PfCfg<D, E, Q8, RW>;
   using T = typename ElemOps<E>::T;
   constexpr int NS = Cfg::kStages;
   constexpr int NSC = Cfg::kScaleRing;
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(384, 1)
   constexpr unsigned kFull = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
   // aligned by an offset and not through an integer: the compiler keeps seeing shared memory
-  PfSmem<D, Q8, RW>& sm = *reinterpret_cast<PfSmem<D, Q8, RW>*>(smem_raw + (1024u - (smem_u32(smem_raw) & 1023u)) % 1024u);
+  PfSmem<D, E, Q8, RW>& sm = *reinterpret_cast<PfSmem<D, E, Q8, RW>*>(smem_raw + (1024u - (smem_u32(smem_raw) & 1023u)) % 1024u);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int G = a.H / a.H_kv;
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(384, 1)
       ok = pg_wait(&sm.q_empty[qs], (qcnt[qs] & 1) ^ 1, wc);
       if (!ok) break;
       // a box of G heads x TQ tokens per chunk, or per piece
-      constexpr int kBoxes = Q8 ? 2 : Cfg::kChunks;
+      constexpr int kBoxes = Q8 ? Cfg::kQPieces : Cfg::kChunks;
       if (lane == 0)
         mbar_arrive_expect_tx(&sm.q_full[qs], static_cast<uint32_t>(kBoxes * Cfg::kRowBytes * G * a.TQ));
       __syncwarp();
@@ -488,15 +491,18 @@ __global__ void __launch_bounds__(384, 1)
         }
         float x[RW];  // scores in log2 units
         {
-          uint32_t s[Q8 ? 2 * RW : RW];
+          uint32_t s[Q8 ? Cfg::kQPieces * RW : RW];
           tmem_ld_cols(tbase + buf * Cfg::kNS + lane_off, s);
           tmem_wait_ld();
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
-            if constexpr (Q8)
-              x[r] = (__uint_as_float(s[r]) + __uint_as_float(s[RW + r])) * kf * c_row[r];
-            else
+            if constexpr (Q8) {
+              float sum = __uint_as_float(s[r]) + __uint_as_float(s[RW + r]);
+              if constexpr (Cfg::kQPieces == 3) sum += __uint_as_float(s[2 * RW + r]);
+              x[r] = sum * kf * c_row[r];
+            } else {
               x[r] = __uint_as_float(s[r]) * a.scale_log2;
+            }
           }
         }
         const int k0 = (kt0 + t) << 7;
@@ -550,7 +556,7 @@ __global__ void __launch_bounds__(384, 1)
           }
           if (!first) {
 #pragma unroll
-            for (int c = 0; c < (Q8 ? 3 * RW : RW); c += 8) {
+            for (int c = 0; c < (Q8 ? Cfg::kPPieces * RW : RW); c += 8) {
               uint32_t o[8];
               tmem_ld8(tO + c, o);
               tmem_wait_ld();
@@ -576,16 +582,16 @@ __global__ void __launch_bounds__(384, 1)
               l[r + y] += p;
               w[y] = p * vf;
             }
-            // fp16, rounded to 9 significant bits; its upper byte is the e5m2 truncation, and each
-            // remainder is exact in fp16
-            uint32_t v = pack_f16x2(w[0], w[1]) + 0x00020002u;
+            // fp16, with three pieces rounded to 9 significant bits; its upper byte is the e5m2
+            // truncation, and each remainder is exact in fp16
+            uint32_t v = pack_f16x2(w[0], w[1]) + (Cfg::kPPieces == 3 ? 0x00020002u : 0u);
 #pragma unroll
-            for (int piece = 0; piece < kPPieces; ++piece) {
+            for (int piece = 0; piece < Cfg::kPPieces; ++piece) {
 #pragma unroll
               for (int y = 0; y < 2; ++y)
                 prow[(piece * RW + r + y) * 128 + ((unit ^ ((r + y) & 7)) << 4) + at] =
                     static_cast<uint8_t>(v >> (8 + 16 * y));
-              if (piece + 1 < kPPieces)
+              if (piece + 1 < Cfg::kPPieces)
                 asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v) : "r"(v), "r"(v & 0xff00ff00u));
             }
           }
@@ -675,7 +681,7 @@ __global__ void __launch_bounds__(384, 1)
         for (int y = 0; y < 8; ++y) v[y] = 0.f;
         if (has) {
 #pragma unroll
-          for (int piece = 0; piece < (Q8 ? kPPieces : 1); ++piece) {
+          for (int piece = 0; piece < (Q8 ? Cfg::kPPieces : 1); ++piece) {
             uint32_t o[8];
             tmem_ld8(tO + piece * RW + r0, o);
             tmem_wait_ld();

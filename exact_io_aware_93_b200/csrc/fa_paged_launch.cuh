@@ -32,14 +32,15 @@ bool launch_after(bool early, void (*kern)(P...), dim3 grid, int threads, int sm
 template <int D, Elem E, bool Q8, int RW>
 fa_status launch_paged(DeviceInfo& di, const PagedCall& c, int n_lo, int n_hi) {
   constexpr bool kFew = RW > 0;
-  using Cfg = std::conditional_t<kFew, PfCfg<D, Q8, kFew ? RW : 8>, PgCfg<D, E, Q8>>;
-  using Smem = std::conditional_t<kFew, PfSmem<D, Q8, kFew ? RW : 8>, PgSmem<D, E, Q8>>;
+  using Cfg = std::conditional_t<kFew, PfCfg<D, E, Q8, kFew ? RW : 8>, PgCfg<D, E, Q8>>;
+  using Smem = std::conditional_t<kFew, PfSmem<D, E, Q8, kFew ? RW : 8>, PgSmem<D, E, Q8>>;
   static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory of one CTA");
   const fa_paged_problem& p = c.p;
   auto kern = [] {
     if constexpr (kFew) return fa_paged_few_kernel<D, E, Q8, RW>;
     else return fa_paged_kernel<D, E, Q8>;
   }();
+  constexpr int kPieces = kFew ? paged_q_pieces(E == Elem::kF16) : 0;
   const int smem = static_cast<int>(sizeof(Smem)) + 1024;
   const int G = p.H / p.H_kv;
   const int TQ = kFew ? n_hi : 128 / G;
@@ -55,7 +56,7 @@ fa_status launch_paged(DeviceInfo& di, const PagedCall& c, int n_lo, int n_hi) {
   const bool q_ok =
       !Q8 ? make_ragged_q_map(&mq, c.q, p.T, p.H_kv, G, D, p.q_stride[0], p.q_stride[1], TQ, me)
       // the e4m3 pieces, one batch of tokens after the other, or the fp16 queries
-      : kFew ? make_ragged_q_map(&mq, w + ps.q, 2ll * p.T, p.H_kv, G, D, static_cast<long long>(p.H) * D, D, TQ,
+      : kFew ? make_ragged_q_map(&mq, w + ps.q, static_cast<long long>(kPieces) * p.T, p.H_kv, G, D, static_cast<long long>(p.H) * D, D, TQ,
                                  MapElem::kE4M3)
              : make_ragged_q_map(&mq, w + ps.q, p.T, p.H_kv, G, D, static_cast<long long>(p.H) * D, D, TQ,
                                  MapElem::kF16);
@@ -93,7 +94,7 @@ fa_status launch_paged(DeviceInfo& di, const PagedCall& c, int n_lo, int n_hi) {
   a.status = di.status;
   if constexpr (Q8) {
     const long long threads = static_cast<long long>(p.T) * p.H * (D / 16);
-    fa_paged_scale_q_kernel<D, E, kFew><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, c.stream>>>(
+    fa_paged_scale_q_kernel<D, E, kPieces><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, c.stream>>>(
         c.q, p.q_stride[0], p.q_stride[1], w + ps.q, reinterpret_cast<float*>(w + L.q_scale), p.T, p.H, di.status);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
   }
@@ -113,7 +114,7 @@ bool paged_ready(DeviceInfo& di) {
   return once_per_device(di.paged_attr[E == Elem::kF16][Q8][D == 128][RW / 8 < 4 ? RW / 8 : 3], [&] {
     if constexpr (RW > 0)
       return cudaFuncSetAttribute(fa_paged_few_kernel<D, E, Q8, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(sizeof(PfSmem<D, Q8, RW>)) + 1024) == cudaSuccess;
+                                  static_cast<int>(sizeof(PfSmem<D, E, Q8, RW>)) + 1024) == cudaSuccess;
     else
       return launch_regs_ok(fa_paged_kernel<D, E, Q8>, PgCfg<D, E, Q8>::kLaunch) &&
              cudaFuncSetAttribute(fa_paged_kernel<D, E, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -124,7 +125,7 @@ bool paged_ready(DeviceInfo& di) {
 template <Elem E, bool Q8, int D>
 fa_status paged_call_d(DeviceInfo& di, const PagedCall& c) {
   const PagedKernels s = paged_kernels(c.p);
-  constexpr int kMost = Q8 ? 32 : 16;
+  constexpr int kMost = paged_most_rows(Q8, E == Elem::kF16);
   if (!(s.rows != 8 || paged_ready<D, E, Q8, 8>(di)) || !(s.rows != 16 || paged_ready<D, E, Q8, 16>(di)) ||
       !(s.rows != 32 || paged_ready<D, E, Q8, kMost>(di)) || !(!s.many || paged_ready<D, E, Q8, 0>(di)))
     return FA_ERR_LAUNCH;

@@ -25,10 +25,16 @@ struct PagedCall {
   cudaStream_t stream;
 };
 
+// With e4m3 pages, the e4m3 pieces of a query in the few-rows kernel: all bits of a bf16 (8), or of
+// an fp16 (11), four to a piece.
+constexpr int paged_q_pieces(bool f16) { return f16 ? 3 : 2; }
+// Most rows of the few-rows kernel; 32 of fp16 with e4m3 pages would not fit into tensor memory.
+constexpr int paged_most_rows(bool quant, bool f16) { return quant && !f16 ? 32 : 16; }
+
 // Which kernels a call takes.  A key/value head's rows, (H / H_kv) * n for n new tokens, choose
 // per sequence: up to `rows` of them the few-rows kernel (n <= few_q), more the tiles of 128.
-//   all sequences few (max_q says so): that kernel alone, at the smallest of 8, 16 and, with e4m3
-//     pages, 32 rows.  (16 sequences of 16-32K tokens, 20 rows: 16-bit pages 270 us there and 262 us
+//   all sequences few (max_q says so): that kernel alone, at the smallest of 8, 16 and, bf16 with
+//     e4m3 pages, 32 rows.  (16 sequences of 16-32K tokens, 20 rows: 16-bit pages 270 us there and 262 us
 //     in tiles of 128; e4m3 pages 322 and 386 us.)
 //   all sequences max_q tokens long (T = B max_q): the tiles alone
 //   a mixture: both, one after the other, single tokens in the first at the smallest size
@@ -40,7 +46,7 @@ struct PagedKernels {
 inline PagedKernels paged_kernels(const fa_paged_problem& p) {
   const int G = p.H / p.H_kv;
   const long long rows = static_cast<long long>(G) * p.max_q;
-  const int most = p.quant ? 32 : 16;
+  const int most = paged_most_rows(p.quant, p.dtype == FA_DTYPE_F16);
   if (rows <= most) return {rows <= 8 ? 8 : (rows <= 16 ? 16 : 32), p.max_q, false};
   if (G > most || static_cast<long long>(p.B) * p.max_q == p.T) return {0, 0, true};
   const int r = G <= 8 ? 8 : (G <= 16 ? 16 : 32);
@@ -57,8 +63,8 @@ inline long long paged_units(const fa_paged_problem& p, int n, int TQ) {
 
 // Workspace regions of each kernel used: the units that CTAs share (16 bytes per CTA), the partial
 // log-sums [rows, 2] and outputs [rows, d] (a CTA leaves at most two partial segments, of `rows` or
-// 256 rows), and with e4m3 pages the scaled queries (2 bytes per element); then a factor per query
-// row.
+// 256 rows), and with e4m3 pages the queries' pieces (2 or 3 bytes per element) or fp16 form; then a
+// factor per query row.
 struct PagedLayout {
   struct Pass {
     size_t splits, part_lse, part_o, q;
@@ -72,16 +78,16 @@ inline PagedLayout paged_layout(const fa_paged_problem& p, int grid) {
   const size_t q_rows = p.quant ? static_cast<size_t>(p.T) * p.H : 0;
   PagedLayout L{};
   size_t at = 0;
-  const auto pass = [&](PagedLayout::Pass& x, size_t rows) {
+  const auto pass = [&](PagedLayout::Pass& x, size_t rows, int q_bytes) {
     rows *= 2 * static_cast<size_t>(grid);
     x.splits = at;
     x.part_lse = x.splits + round256(static_cast<size_t>(grid) * 16);
     x.part_o = x.part_lse + round256(rows * 2 * 4);
     x.q = x.part_o + round256(rows * static_cast<size_t>(p.d) * 4);
-    at = x.q + round256(q_rows * p.d * 2);
+    at = x.q + round256(q_rows * p.d * q_bytes);
   };
-  if (s.rows) pass(L.few, s.rows);
-  if (s.many) pass(L.many, 256);
+  if (s.rows) pass(L.few, s.rows, paged_q_pieces(p.dtype == FA_DTYPE_F16));
+  if (s.many) pass(L.many, 256, 2);
   L.q_scale = at;
   L.total = at + q_rows * 4;
   return L;
