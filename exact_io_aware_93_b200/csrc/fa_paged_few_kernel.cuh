@@ -14,7 +14,7 @@
 //
 // The two softmax groups take alternate key tiles, each with its own accumulator.  A group's
 // rows share one reference maximum per row over its 128 threads: per tile each warp posts whether
-// one of its scores exceeds the reference by 2^8; only then do the four warps exchange maxima and
+// one of its scores exceeds the reference by a threshold; only then do the four warps exchange maxima and
 // rescale O^T.  Weights P^T go to shared memory as the next product's B operand.
 //
 // e4m3 pages.  The codes are operands as they are (kind::f8f6f4): a tile moves half the bytes and
@@ -22,9 +22,9 @@
 //   Q   e4m3 pieces per row (fa_paged_scale_q_kernel), two of a bf16 and three of an fp16 row, as
 //       rows r, RW + r, .. of the tile: the score columns are added by the key's thread
 //   P   the weight, an fp16 value, is the sum of e5m2 pieces (e5m2 is the upper byte of an fp16):
-//       three hold 9 bits, one more than bf16, and four all 11, for fp16 outputs; down to 2^-23 of
-//       the largest weight.  e5m2 and not e4m3 for its range: a long tail of small weights beside
-//       a large one keeps its mass.  The pieces are rows of P^T, their products columns of O^T,
+//       three hold 9 bits, one more than bf16, and four all 11, for fp16 outputs.  e5m2 and not
+//       e4m3 for its range: a long tail of small weights beside a large one keeps its mass.  The
+//       pieces are rows of P^T, their products columns of O^T,
 //       added at the end.
 //   scales  a key's 2^ek and 2^(ev - E) are one number each for its thread; E is the largest
 //       value exponent of the group's tiles so far (O^T is rescaled when it grows).  The bytes
@@ -42,7 +42,11 @@
 
 namespace fa {
 
-constexpr float kPShift = 7.0f;  // weights cut into pieces are 2^(x - m + 7) <= 2^15
+// Over e4m3 pages a score may exceed its row's reference maximum m by 2^2 (16-bit pages: kTau, 2^8)
+// before m is raised, and weights are 2^(x - m + 13) <= 2^15: they are cut off at e5m2's 2^-16,
+// 2^-29 of the reference weight, far below what a long tail of small weights adds up to.
+constexpr float kTauCodes = 2.0f;
+constexpr float kPShift = 13.0f;
 
 template <int D, Elem E, bool Q8, int RW>
 struct PfCfg {
@@ -146,6 +150,7 @@ __global__ void __launch_bounds__(384, 1)
   constexpr int NSEG = Cfg::kSegRing;
   constexpr int NB = Cfg::kSBufs;
   constexpr unsigned kFull = 0xffffffffu;
+  constexpr float kRaise = Q8 ? kTauCodes : kTau;
   extern __shared__ uint8_t smem_raw[];
   // aligned by an offset and not through an integer: the compiler keeps seeing shared memory
   PfSmem<D, E, Q8, RW>& sm = *reinterpret_cast<PfSmem<D, E, Q8, RW>*>(smem_raw + (1024u - (smem_u32(smem_raw) & 1023u)) % 1024u);
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         bool raise = false;
 #pragma unroll
-        for (int r = 0; r < RW; ++r) raise = raise || (r < M && x[r] > ref[r] + kTau);
+        for (int r = 0; r < RW; ++r) raise = raise || (r < M && x[r] > ref[r] + kRaise);
         const bool any = __any_sync(kFull, raise);
         if (lane == 0) sm.flag[grp][mine & 1][wq] = e * 2 + any;
         ok = sync4();
@@ -547,7 +552,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int r = 0; r < RW; ++r) {
             const float m = fmaxf(fmaxf(sm.top[grp][0][r], sm.top[grp][1][r]),
                                   fmaxf(sm.top[grp][2][r], sm.top[grp][3][r]));
-            const bool up = m > ref[r] + kTau;
+            const bool up = m > ref[r] + kRaise;
             alpha[r] = up ? ex2_approx(ref[r] - m) : 1.f;
             l[r] *= alpha[r];
             lr[r] *= alpha[r];

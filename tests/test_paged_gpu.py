@@ -9,10 +9,11 @@ sum: (u + eta) sum_j w_j |v_j|, plus 2^-25 per key.  Then the output rounds (u |
 over the keys add at most 2^-17 max|v|.  LSE: eta, and 2^-20 relative.
 
 e4m3 pages: a weight is an fp16 value, kept to 9 bits for bf16 queries (u = 2^-9) and whole for
-fp16 (u = 2^-11), and loses what lies under 2^-16 / 2^7 = 2^-23 of the largest weight (times a
-value of up to 2 max|v|, by the scales' powers of two); the fp32 sum divides.  Query pieces end
-at 2^-10 with a row maximum of at least 224: 2^-17.8 of it per element, which moves a score by up
-to 2^-17.8 scale max|q| sum|k| < 2^-12.5 at these sizes, so eta = 2^-12."""
+fp16 (u = 2^-11).  It is cut off at 2^-16 / 2^13 = 2^-29 of the reference weight, which is at most
+the largest, with few rows, and rounded by fp16's smallest step at 2^-25 of it in tiles of 128 (times
+a value of up to 2 max|v|, by the scales' powers of two); the fp32 sum divides.  Query pieces end at
+2^-10 with a row maximum of at least 224: 2^-17.8 of it per element, which moves a score by up to
+2^-17.8 scale max|q| sum|k| < 2^-12.5 at these sizes, so eta = 2^-12."""
 import math
 
 import pytest
@@ -107,7 +108,7 @@ def check(s, o, lse, causal=True, scale=None, q=None):
             for r in range(0, n, 64):                        # sum_j w_j |v_j - O|, a block of rows at a time
                 wr = w[:, r:r + 64]
                 if quant or dtype == torch.float16:
-                    lost = m * (2.0 ** -22 if quant else 2.0 ** -25) * top
+                    lost = m * (2.0 ** -24 if quant else 2.0 ** -25) * top
                     tol[:, r:r + 64] = torch.matmul(wr, v.abs()) + lost / u
                 else:
                     for c in range(0, d, 16):
@@ -169,3 +170,266 @@ def test_paged_attention(new, lens, h, hk, d, page, dtype, quant, causal, window
     torch.cuda.synchronize()
     assert api.get_status_site() == (0, 0)
     check(s, o, lse, causal)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_batches(seed):
+    """Random shapes, kinds and lengths of everything the entry point takes."""
+    import random
+    rng = random.Random(4000 + seed)
+    hk = rng.choice([1, 1, 2, 3, 4])
+    h = hk * rng.choice([1, 2, 3, 4, 5, 7, 8, 12])
+    kind = rng.choice(["one", "few", "chunk", "mixed"])
+    page = rng.choice([16, 32, 64, 128, 256])
+    new, lens = [], []
+    for _ in range(rng.randint(1, 9)):
+        n = {"one": 1, "few": rng.randint(1, 7), "chunk": rng.randint(1, 300),
+             "mixed": rng.choice([0, 1, 1, 2, rng.randint(1, 200)])}[kind]
+        m = rng.choice([n, rng.randint(1, 1500), rng.randint(1, 1500), page * rng.randint(1, 4)])
+        new.append(n)
+        lens.append(m)
+    if sum(new) == 0:
+        new[0], lens[0] = 1, max(lens[0], 1)
+    causal = rng.random() < 0.8
+    window = rng.choice([-1, -1, 0, 17, 127, 400]) if causal else -1
+    s = build(new, lens, h, hk, rng.choice([64, 128]), page, rng.choice([BF, FP]), rng.random() < 0.5, seed=seed,
+              window=window)
+    o, lse = attend(s, causal, max_q=max(new) + rng.choice([0, 0, 1, 60]))
+    torch.cuda.synchronize()
+    assert api.get_status_site() == (0, 0)
+    check(s, o, lse, causal)
+
+
+KINDS = [  # batches that take the few-rows kernel, the tiles, and both
+    ([1] * 6, [700, 30, 129, 1500, 64, 1]),
+    ([50, 41], [300, 900]),
+    ([1, 130, 1, 1], [700, 300, 129, 2000]),
+]
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("new,lens", KINDS)
+def test_strides_given_buffers_and_padding(new, lens, quant):
+    """q as a slice of a fused projection, buffers of the caller's, rows behind the last sequence
+    and guard zones around everything that is written."""
+    s = build(new, lens, 8, 2, 128, 32, BF, quant, seed=5)
+    want, want_l = attend(s)
+    T, pad = sum(new), 37
+    fused = torch.full((T + pad, 12, 128), float("nan"), dtype=BF, device="cuda")
+    fused[:T, 2:10] = s["q"]
+    guard = 1024
+    nbytes = api.paged_workspace_size(fused[:, 2:10], s["pages"][0], s["table"], max(new))
+    flat = torch.full((2 * guard + (T + pad) * 1024,), 3.0, dtype=BF, device="cuda")
+    flat_l = torch.full((2 * guard + 8 * (T + pad),), 5.0, device="cuda")
+    ws = torch.full((2 * guard + nbytes,), 0xFF, dtype=torch.uint8, device="cuda")     # NaN everywhere
+    out = flat[guard:-guard].view(T + pad, 8, 128)
+    lse = flat_l[guard:-guard].view(8, T + pad)
+    o2, l2 = attend(s, q=fused[:, 2:10], out=out, lse=lse, workspace=ws[guard:guard + nbytes])
+    torch.cuda.synchronize()
+    assert api.get_status_site() == (0, 0) and o2 is out and l2 is lse
+    assert torch.equal(out[:T], want) and torch.equal(lse[:, :T], want_l)
+    assert torch.all(out[T:] == 3.0) and torch.all(lse[:, T:] == 5.0)
+    for t, v in ((flat, 3.0), (flat_l, 5.0), (ws, 0xFF)):
+        assert torch.all(t[:guard] == v) and torch.all(t[-guard:] == v)
+    with pytest.raises(api.FAError) as e:
+        attend(s, workspace=ws[guard:guard + nbytes // 512 * 256])
+    assert e.value.status == 7
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("new,lens", KINDS)
+def test_same_bits_again(new, lens, quant):
+    s = build(new, lens, 8, 2, 64, 64, FP, quant, seed=6)
+    o, lse = attend(s)
+    for fill in (0x00, 0x7F, 0xFF):
+        ws = torch.full((api.paged_workspace_size(s["q"], s["pages"][0], s["table"], max(new)),), fill, dtype=torch.uint8,
+                        device="cuda")
+        o2, l2 = attend(s, workspace=ws)
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+    assert api.get_status() == 0
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_captured_graph_replayed_as_the_batch_changes(quant):
+    """One capture serves other lengths, other tokens per sequence and other pages, within B, T and
+    max_q; a second graph with the same workspace replays after it."""
+    batches = [build(n, m, 8, 2, 128, 32, BF, quant, seed=7) for n, m in
+               (([1, 60, 3], [900, 300, 200]), ([64, 0, 0], [1000, 3, 2]), ([0, 1, 1], [0, 1200, 5]))]
+    pool = max(b["pages"][0].shape[0] for b in batches)
+    width = max(b["table"].shape[1] for b in batches)
+    first = batches[0]
+    live = dict(first)
+    live["pages"] = [torch.zeros((pool, *first["pages"][0].shape[1:]), dtype=first["pages"][0].dtype, device="cuda")
+                     for _ in "kv"]
+    if quant:
+        live["scales"] = [torch.zeros((pool, *first["scales"][0].shape[1:]), dtype=torch.uint8, device="cuda")
+                          .view(torch.float8_e8m0fnu) for _ in "kv"]
+    live["table"] = torch.full((3, width), -1, dtype=torch.int32, device="cuda")
+    live["q"] = torch.zeros(64, 8, 128, dtype=BF, device="cuda")
+    live["seqlens"], live["cu"] = first["seqlens"].clone(), first["cu"].clone()
+    ws = torch.empty(api.paged_workspace_size(live["q"], live["pages"][0], live["table"], 64), dtype=torch.uint8,
+                     device="cuda")
+    out = [torch.empty(64, 8, 128, dtype=BF, device="cuda") for _ in range(2)]
+    lse = [torch.empty(8, 64, device="cuda") for _ in range(2)]
+
+    def fill(b):
+        for x, y in zip(live["pages"], b["pages"]):
+            x[:y.shape[0]].view(torch.uint8).copy_(y.view(torch.uint8))
+        if quant:
+            for x, y in zip(live["scales"], b["scales"]):
+                x[:y.shape[0]].view(torch.uint8).copy_(y.view(torch.uint8))
+        live["table"].fill_(-1)
+        live["table"][:, :b["table"].shape[1]] = b["table"]
+        live["q"].fill_(float("nan"))
+        live["q"][:b["q"].shape[0]] = b["q"]
+        live["seqlens"].copy_(b["seqlens"])
+        live["cu"].copy_(b["cu"])
+    fill(first)
+    graphs = []
+    for i in range(2):
+        attend(live, max_q=64, out=out[i], lse=lse[i], workspace=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            attend(live, max_q=64, out=out[i], lse=lse[i], workspace=ws)
+        graphs.append(g)
+    for b in batches[1:] + batches[:1]:
+        fill(b)
+        for i in range(2):
+            out[i].fill_(-2.0)
+            lse[i].fill_(-2.0)
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert api.get_status_site() == (0, 0)
+        T = sum(b["new"])
+        check(b, out[0], lse[0])
+        assert torch.all(out[0][T:] == -2.0) and torch.all(lse[0][:, T:] == -2.0)
+        assert torch.equal(out[0], out[1]) and torch.equal(lse[0], lse[1])
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams, and on one that is not the tensors' own, each with its own
+    workspace."""
+    a = build([1] * 8, [3000 + 100 * i for i in range(8)], 16, 4, 128, 64, BF, True, seed=8)
+    b = build([200, 1, 1], [2500, 1900, 40], 16, 4, 128, 16, FP, True, seed=9)
+    want = [attend(a), attend(b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(attend(s))
+    torch.cuda.synchronize()
+    assert api.get_status_site() == (0, 0)
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_shared_pages_and_uint8_scales():
+    """Sequences that share the pages of a prefix give what copies of it give; scales may be uint8."""
+    s = build([2, 2, 2], [300, 300, 300], 4, 2, 64, 16, BF, True, seed=10)
+    s["q"][2:4] = s["q"][0:2]
+    s["q"][4:6] = s["q"][0:2]
+    s["table"][1] = s["table"][0]
+    s["table"][2] = s["table"][0]
+    o, lse = attend(s, k_scales=s["scales"][0].view(torch.uint8), v_scales=s["scales"][1].view(torch.uint8))
+    assert api.get_status() == 0
+    assert torch.equal(o[0:2], o[2:4]) and torch.equal(o[0:2], o[4:6]) and torch.equal(lse[:, :2], lse[:, 4:])
+
+
+@pytest.mark.parametrize("dtype,quant,rows", [(BF, True, 1), (FP, True, 1), (BF, True, 40), (FP, True, 40), (FP, False, 1)])
+def test_long_tail_of_small_weights(dtype, quant, rows):
+    """One key takes nearly all of the softmax; thousands of others, 2^-18 of it each, still add up:
+    with values 0 for it and 1 for them O is their share."""
+    m, c = 16384, 18.0 * math.log(2.0)
+    s = build([rows], [m], 1, 1, 64, 64, dtype, quant, seed=11)
+    k = torch.zeros(m, 1, 64, dtype=dtype, device="cuda")
+    k[:, 0, 0] = -1.0
+    k[3, 0, 0] = 0.0
+    v = torch.ones(m, 1, 64, dtype=dtype, device="cuda")
+    v[3] = 0.0
+    api.cache_append(k, v, *s["pages"], s["table"], s["seqlens"], torch.tensor([0, m], dtype=torch.int32, device="cuda"),
+                     k_scales=s["scales"][0], v_scales=s["scales"][1])
+    s["q"].zero_()
+    s["q"][:, 0, 0] = 16.0
+    o, lse = attend(s, causal=False, scale=c / 16.0)
+    assert api.get_status() == 0
+    share = (m - 1) * math.exp(-c) / (1.0 + (m - 1) * math.exp(-c))       # 0.0588
+    # a weight: 2^-9 (bf16) or 2^-11 of itself, or 2^-25 of the largest, 2^-7 of itself, and equal
+    # weights round alike; fp32 scores of 12.5: 2^-20; then the output's rounding
+    rel = (2.0 ** -7 if rows > 32 or not quant else 2.0 ** -9) + 2.0 ** -20 + torch.finfo(dtype).eps / 2
+    assert (o.double() / share - 1.0).abs().max().item() <= rel
+    assert (lse.double() - math.log1p((m - 1) * math.exp(-c))).abs().max().item() <= 2.0 ** -14
+
+
+def test_bad_plans_are_reported_and_skip_their_access():
+    """Offsets, lengths and page numbers out of range: recorded, and everything else computed."""
+    s = build([1, 1, 1], [500, 400, 300], 8, 2, 128, 32, BF, False, seed=12)
+    good_o, good_l = attend(s)
+    table, lens, cu = s["table"].clone(), s["seqlens"].clone(), s["cu"].clone()
+    for bad in (-1, -2 ** 31, s["pages"][0].shape[0], 2 ** 31 - 1):
+        s["table"].copy_(table)
+        s["table"][1, 3] = bad
+        o, lse = attend(s)
+        assert api.get_status_site() == (9, 44)
+        assert torch.equal(o[[0, 2]], good_o[[0, 2]]) and torch.equal(lse[:, [0, 2]], good_l[:, [0, 2]])
+    s["table"].copy_(table)
+    for bad in (-5, 10 ** 6, 2 ** 31 - 1):
+        s["seqlens"].copy_(lens)
+        s["seqlens"][1] = bad
+        o, lse = attend(s)
+        assert api.get_status() == 9
+        assert torch.equal(o[[0, 2]], good_o[[0, 2]])
+    s["seqlens"].copy_(lens)
+    for bad in ([0, 2, 1, 3], [0, 1, 2, 9], [-4, 1, 2, 3], [0, 2 ** 31 - 1, 2, 3], [5, 5, 5, 5]):
+        s["cu"].copy_(torch.tensor(bad, dtype=torch.int32))
+        flat = torch.full((5, 8, 128), 3.0, dtype=BF, device="cuda")
+        attend(s, out=flat[1:4])
+        st = api.get_status_site()
+        assert st == (9, 43) and torch.all(flat[0] == 3.0) and torch.all(flat[4] == 3.0)
+    s["cu"].copy_(cu)
+    o, lse = attend(s)
+    assert torch.equal(o, good_o) and api.get_status() == 0
+
+
+def test_refusals():
+    s = build([2, 1], [50, 20], 4, 2, 64, 16, BF, True, seed=13)
+    for kw, err in ((dict(q=s["q"].float()), TypeError), (dict(q=s["q"][0]), ValueError), (dict(q=s["q"].cpu()), ValueError),
+                    (dict(q=s["q"][:, :3]), ValueError), (dict(q=s["q"][..., :32]), ValueError),
+                    (dict(q=s["q"].transpose(1, 2)), ValueError), (dict(k_scales=None), ValueError),
+                    (dict(v_scales=s["scales"][1][:1]), ValueError), (dict(page_table=s["table"][:1]), ValueError),
+                    (dict(cu_q=s["cu"].long()), ValueError), (dict(seqlens=s["seqlens"][:1]), ValueError),
+                    (dict(out=s["q"][:2]), ValueError), (dict(lse=torch.empty(4, 4, device="cuda")), ValueError),
+                    (dict(workspace=torch.empty(1 << 20)), ValueError), (dict(max_q=2 ** 40), ValueError),
+                    (dict(max_q=0), api.FAError), (dict(window=-3), api.FAError), (dict(scale=-1.0), api.FAError),
+                    (dict(causal=False, window=5), api.FAError),
+                    (dict(k_pages=s["pages"][0][:0], v_pages=s["pages"][1][:0]), ValueError)):
+        with pytest.raises(err):
+            attend(s, **kw)
+    with pytest.raises(TypeError):
+        attend(build([2], [50], 4, 2, 64, 16, BF, False, seed=13), q=s["q"][:2].half())
+    o, lse = attend(s, q=s["q"][:0])                                   # no tokens: nothing to do
+    assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
+    torch.cuda.synchronize()
+    assert api.get_status() == 0
+
+
+def test_offsets_past_32_bits():
+    """Pages beyond 2^32 bytes of the pool (and 2^31 elements) are written, read back and attended."""
+    hk, page, d, pool = 8, 256, 128, 8400                              # 2.2e9 elements each
+    pages = [torch.empty(pool, hk, page, d, dtype=BF, device="cuda") for _ in "kv"]
+    n, m = 3, 600
+    g = torch.Generator().manual_seed(14)
+    table = torch.tensor([[8399, 8398, 8250]], dtype=torch.int32, device="cuda")
+    x = [torch.randn(m, hk, d, generator=g).to(BF).cuda() for _ in "kv"]
+    lens = torch.tensor([m], dtype=torch.int32, device="cuda")
+    api.cache_append(*x, *pages, table, lens, torch.tensor([0, m], dtype=torch.int32, device="cuda"))
+    back = api.cache_gather(*pages, table, lens, torch.tensor([0, m], dtype=torch.int32, device="cuda"), m)
+    assert torch.equal(back[0], x[0]) and torch.equal(back[1], x[1])
+    s = dict(new=[n], lens=[m], window=-1, h=16, hk=hk, q=torch.randn(n, 16, d, generator=g).to(BF).cuda(), pages=pages,
+             scales=[None, None], table=table, seqlens=lens, cu=torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+             values=[[t.double().cpu()] for t in x])
+    o, lse = attend(s)
+    assert api.get_status() == 0
+    check(s, o, lse)
