@@ -50,6 +50,11 @@ CASES = [
     ([1] * 70, list(range(1, 71)), 1, 64, 256, torch.bfloat16, True),
     ([300, 400], [300, 1000], 16, 64, 16, torch.bfloat16, False),
     ([2000] + [1] * 40, [2000] + [3000] * 40, 2, 128, 64, torch.float16, True),
+    # thousands of rows: several per warp, of sequences that begin and end among them
+    ([0, 5001, 0, 0, 1, 2, 3, 0] + [3] * 700 + [6], [4, 5001, 7, 0, 900, 2, 33, 1] + [40] * 700 + [6], 2, 64, 16,
+     torch.float16, True),
+    ([12001, 1] + [7] * 1200, [12001, 3] + [7] * 1200, 1, 64, 32, torch.bfloat16, True),
+    ([9001, 1, 0, 3000], [9100, 3, 9, 3001], 3, 128, 64, torch.bfloat16, False),
 ]
 
 

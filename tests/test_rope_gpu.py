@@ -49,6 +49,10 @@ CASES = [
     ((2, 300), 6, 2, 128, 128, torch.bfloat16, False, 1.0, 0),
     ((3, 1200), 16, 16, 128, 96, torch.bfloat16, True, 1.0, 8000),
     ((20,), 1, 1, 1024, 1024, torch.bfloat16, False, 1.0, 3),
+    ((20003,), 1, 0, 64, 32, torch.float16, False, 1.0, 11),            # 16 tokens to a block
+    ((9000, 1), 3, 1, 64, 64, torch.bfloat16, True, 1.0, 5),            # one token per batch row
+    ((1700, 7), 5, 0, 128, 64, torch.float16, False, 1.0, 0),
+    ((5000, 3), 2, 1, 75, 46, torch.bfloat16, False, 1.0, 4),
 ]
 
 
