@@ -29,6 +29,12 @@
 
 namespace fa {
 
+// fp16 weights are 2^(x - m + 7): the largest, 2^kTau over the reference maximum m, still fits below
+// 65504, and the smallest, 2^-24, is 2^-31 of the reference weight, so that a hundred thousand keys of
+// little weight each keep their sum.  bf16 has the range without it.
+template <Elem W>
+constexpr float kWeightShift = W == Elem::kF16 ? 7.0f : 0.0f;
+
 // Bounded waits, smaller than mbar_wait: these kernels have many and their code has to stay in
 // the instruction cache.  A wait that runs out (2 s) leaves its site in the CTA's abort flag,
 // which ends every other wait; the flag is reported once, when the CTA ends (pg_report).
@@ -372,14 +378,21 @@ __device__ __forceinline__ void pg_load_tile(const PgArgs& a, const PgSeg& g, Pg
     // four keys per lane, which lie in one page; keys that the unit does not see are left out
     const int key = (j << 7) + lane * 4;
     const int pg = pages.get(a, g, p0, (lane * 4) >> a.page_shift, lane);
-    if (key + 3 >= g.keys.lo && key < g.keys.hi && pg >= 0 && pg < a.P) {
+    const bool seen = key + 3 >= g.keys.lo && key < g.keys.hi, good = pg >= 0 && pg < a.P;
+    if (seen && good) {
       const int64_t at = (static_cast<int64_t>(pg) * a.H_kv + g.kvh) * a.page + (key & (a.page - 1));
       if (FA_IN_BOUNDS(at >= 0 && at + 4 <= static_cast<int64_t>(a.P) * a.H_kv * a.page, a.status, 513)) {
         cp_async4(scales + lane * 4, a.k_scales + at);
         cp_async4(scales + 128 + lane * 4, a.v_scales + at);
       }
     }
-    cp_async_arrive(scales_full);
+    if (seen && !good) {  // the zeros of a bad page number have scale 1; a plain arrival publishes plain stores
+      *reinterpret_cast<uint32_t*>(scales + lane * 4) = 0x7f7f7f7fu;
+      *reinterpret_cast<uint32_t*>(scales + 128 + lane * 4) = 0x7f7f7f7fu;
+      mbar_arrive(scales_full);
+    } else {
+      cp_async_arrive(scales_full);
+    }
   }
   __syncwarp();
 }

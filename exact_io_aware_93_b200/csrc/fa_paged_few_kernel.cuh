@@ -46,7 +46,7 @@ namespace fa {
 // before m is raised, and weights are 2^(x - m + 13) <= 2^15: they are cut off at e5m2's 2^-16,
 // 2^-29 of the reference weight, far below what a long tail of small weights adds up to.
 constexpr float kTauCodes = 2.0f;
-constexpr float kPShift = 13.0f;
+constexpr float kCodesShift = 13.0f;
 
 template <int D, Elem E, bool Q8, int RW>
 struct PfCfg {
@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(384, 1)
   constexpr int NB = Cfg::kSBufs;
   constexpr unsigned kFull = 0xffffffffu;
   constexpr float kRaise = Q8 ? kTauCodes : kTau;
+  constexpr float kPShift = Q8 ? kCodesShift : kWeightShift<E>;
   extern __shared__ uint8_t smem_raw[];
   // aligned by an offset and not through an integer: the compiler keeps seeing shared memory
   PfSmem<D, E, Q8, RW>& sm = *reinterpret_cast<PfSmem<D, E, Q8, RW>*>(smem_raw + (1024u - (smem_u32(smem_raw) & 1023u)) % 1024u);
@@ -605,7 +606,7 @@ __global__ void __launch_bounds__(384, 1)
           const uint32_t unit = (me >> 3) & 7;
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
-            const float p = ex2_approx(x[r] - (ref[r] == -INFINITY ? 0.f : ref[r]));
+            const float p = ex2_approx(x[r] - (ref[r] == -INFINITY ? 0.f : ref[r]) + kPShift);
             const T v = ElemOps<E>::one(p);
             l[r] += p;
             // bf16: the rounded weights normalise O, as in softmax_row
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         if constexpr (Q8) lr[r] = l[r];
         if (lane == 0) sm.sums[grp][wq][r] = make_float2(l[r], lr[r]);
-        if (wq == 0 && lane == 0) sm.ref[grp][r] = Q8 ? ref[r] - kPShift : ref[r];
+        if (wq == 0 && lane == 0) sm.ref[grp][r] = ref[r] - kPShift;
       }
       // the group's last product (none: passes at once)
       ok = pg_wait(&sm.p_empty[grp], (mine & 1) ^ 1, wc);

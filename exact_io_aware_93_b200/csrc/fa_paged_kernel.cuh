@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
   constexpr int NSC = Cfg::kScaleRing;
   constexpr int NSEG = Cfg::kSegRing;
   constexpr unsigned kFull = 0xffffffffu;
+  constexpr float kShift = kWeightShift<Q8 ? Elem::kF16 : E>;
   extern __shared__ uint8_t smem_raw[];
   // aligned by an offset and not through an integer: the compiler keeps seeing shared memory
   PgSmem<D, E, Q8>& sm = *reinterpret_cast<PgSmem<D, E, Q8>*>(smem_raw + (1024u - (smem_u32(smem_raw) & 1023u)) % 1024u);
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
                 }
                 tmem_wait_st();
               }
-              m_use = m_ref == -INFINITY ? 0.f : m_ref;
+              m_use = (m_ref == -INFINITY ? 0.f : m_ref) - kShift;
             } else {
               uint32_t p[32];
               softmax_row<Q8 ? Elem::kF16 : E, 64>(s, p, c_tile, m_use, l, lr);
@@ -752,16 +753,16 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
       constexpr int kUnits = SC / 4;  // 16-byte units of a staged row; unit u sits at u ^ key(row)
       auto key = [](int r) { return (r >> 1) & (kUnits - 1); };
       if (!pair) {
-        if (real) sm.stat[grp][rc] = make_float3(m_ref, l, lr);
+        if (real) sm.stat[grp][rc] = make_float3(m_ref - kShift, l, lr);
         ok = sync_groups();
         if (!ok) break;
       }
-      float mm = m_ref, ls = l, lrs = lr, wgt = 1.f;
+      float mm = m_ref - kShift, ls = l, lrs = lr, wgt = 1.f;
       if (!pair && real) {
         const float3 st = sm.stat[grp ^ 1][rc];
-        mm = fmaxf(m_ref, st.x);
+        mm = fmaxf(m_ref - kShift, st.x);
         const float ref = mm == -INFINITY ? 0.f : mm;
-        const float mine = ex2_approx(m_ref - ref), other = ex2_approx(st.x - ref);
+        const float mine = ex2_approx(m_ref - kShift - ref), other = ex2_approx(st.x - ref);
         // the same order in both groups
         ls = grp == 0 ? mine * l + other * st.y : other * st.y + mine * l;
         lrs = grp == 0 ? mine * lr + other * st.z : other * st.z + mine * lr;

@@ -92,32 +92,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
-// One warp waits for several barriers at once: every lane polls its own (null: none), so that
-// barriers that are ready cost one round trip to shared memory together instead of one each.
-__device__ __forceinline__ bool mbar_wait_lanes(uint64_t* bar, uint32_t parity, const WaitCtx& w,
-                                                uint64_t timeout_ns = FA_WAIT_TIMEOUT_NS) {
-  const uint32_t a = bar ? smem_u32(bar) : 0;
-  bool done = bar == nullptr || mbar_test(a, parity);
-  if (__all_sync(0xffffffffu, done)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  uint32_t spins = 0;
-  while (true) {
-    if (!done) done = mbar_test(a, parity);
-    if (__all_sync(0xffffffffu, done)) return true;
-    if (++spins >= 32) {
-      spins = 0;
-      bool stop = *w.abort_flag != 0;
-      if (!stop && globaltimer_ns() - t0 > timeout_ns) {
-        stop = true;
-        *w.abort_flag = 1;
-        atomicCAS(w.status, 0, 6 /* FA_ERR_TIMEOUT */);
-        atomicCAS(w.status + 1, 0, w.site);
-      }
-      if (__any_sync(0xffffffffu, stop)) return false;
-    }
-  }
-}
-
 // ---------------------------------------------------------------- checking build
 // Compiled with -DFA_CHECKS, every TMA coordinate and every global index a kernel computes is
 // compared with the extent of the tensor it addresses before the access.  A violation records

@@ -59,7 +59,8 @@ typedef enum {
                              range; the access was skipped (reported by fa_get_status) */
 } fa_status;
 
-/* Library ABI version (this header: 6; 6 added fa_get_status_site). */
+/* Library ABI version (this header: 6; 6 added fa_get_status_site; fa_rope, fa_cache_append, fa_cache_gather
+ * and fa_paged came later and change nothing that was there). */
 int fa_abi_version(void);
 
 /*
@@ -440,7 +441,7 @@ size_t fa_paged_workspace_size(const fa_paged_problem* problem);
  * pages that hold only such positions too; key and value rows that some new token sees are
  * expected to be finite (a NaN or infinity there reaches the rows that see it, and may reach
  * others of the same sequence).  A chunk longer than max_q is cut to it, a length is cut to the
- * table's capacity, a page number outside [0, P) reads as zeros: each records FA_ERR_PLAN.
+ * table's capacity, a page number outside [0, P) reads as zeros (with scale 1): each records FA_ERR_PLAN.
  * Deterministic for fixed inputs and device.  All device-side values are read by the kernels:
  * a captured graph can be replayed as they change, within B, T and max_q.
  * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_ALIGNMENT, FA_ERR_DEVICE,

@@ -363,6 +363,90 @@ def test_long_tail_of_small_weights(dtype, quant, rows):
     assert (lse.double() - math.log1p((m - 1) * math.exp(-c))).abs().max().item() <= 2.0 ** -14
 
 
+@pytest.mark.parametrize("dtype,quant,rows", [(FP, False, 1), (FP, False, 40), (FP, True, 40), (BF, True, 40)])
+def test_little_weights_of_a_long_cache_keep_their_sum(dtype, quant, rows):
+    """A key of weight 1 in each of the first two tiles and thousands of 2^-26.6 each behind them, every
+    key/value head in one run of an SM: with values 0 for the two and 1 for the others O is the others'
+    share, 2^-14.6.  A weight is kept to 2^-25 / 2^7 = 2^-32 of the reference: 2^-5.4 of itself; the
+    output to fp16's smallest half step, 2^-25, or 2^-9 of itself."""
+    m, c = 8192, 26.6 * math.log(2.0)
+    hk = torch.cuda.get_device_properties(0).multi_processor_count
+    page = 256
+    table = torch.arange(m // page, dtype=torch.int32, device="cuda")[None]
+    kind = torch.float8_e4m3fn if quant else dtype
+    pages = [torch.zeros(m // page, hk, page, 64, dtype=kind, device="cuda") for _ in "kv"]
+    scales = [torch.full((m // page, hk, page), 127, dtype=torch.uint8, device="cuda") if quant else None for _ in "kv"]
+    k = torch.zeros(m, 1, 64, dtype=dtype, device="cuda")
+    k[:, 0, 0] = -1.0
+    k[[3, 131]] = 0.0
+    v = torch.ones(m, 1, 64, dtype=dtype, device="cuda")
+    v[[3, 131]] = 0.0
+    lens, cu = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([m], [0, m]))
+    api.cache_append(k.expand(m, hk, 64), v.expand(m, hk, 64), *pages, table, lens, cu, k_scales=scales[0],
+                     v_scales=scales[1])
+    q = torch.zeros(1, hk * rows, 64, dtype=dtype, device="cuda")
+    q[:, :, 0] = 16.0
+    o, lse = api.paged_attention(q, *pages, table, lens, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), 1,
+                                 scale=c / 16.0, k_scales=scales[0], v_scales=scales[1])
+    assert api.get_status() == 0
+    tail = (m - 2) * math.exp(-c)
+    share = tail / (2.0 + tail)
+    tol = share * 2.0 ** -5.4 * (1 + 2.0 ** -10) + max(2.0 ** -25, share * torch.finfo(dtype).eps / 2)
+    assert (o.double() - share).abs().max().item() <= tol
+    assert (lse.double() - math.log(2.0 + tail)).abs().max().item() <= 2.0 ** -14
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("new,lens", KINDS)
+def test_bad_page_numbers_of_an_e4m3_cache_read_as_zeros(new, lens, dtype):
+    """What a page of zero codes with scale 1 gives, bit for bit."""
+    s = build(new, lens, 8, 2, 128, 32, dtype, True, seed=15)
+    at = s["table"][-1, 0].item() if lens[-1] < 200 else s["table"][-1, 3].item()
+    col = 0 if lens[-1] < 200 else 3
+    for x, e in zip(s["pages"], s["scales"]):
+        x.view(torch.uint8)[at] = 0
+        e.view(torch.uint8)[at] = 127
+    want, want_l = attend(s)
+    assert api.get_status() == 0
+    for x, e in zip(s["pages"], s["scales"]):     # what must not be read
+        x.view(torch.uint8)[at] = 0x7F
+        e.view(torch.uint8)[at] = 255
+    for bad in (-1, s["pages"][0].shape[0]):
+        s["table"][-1, col] = bad
+        o, lse = attend(s)
+        assert api.get_status_site() == (9, 44)
+        assert torch.equal(o, want) and torch.equal(lse, want_l)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("new,lens", KINDS)
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_non_finite_queries_stay_in_their_row(new, lens, quant, value):
+    """A query that is not finite changes no bit of another's row; a NaN makes its own NaN."""
+    s = build(new, lens, 8, 2, 128, 32, BF, quant, seed=16)
+    want, want_l = attend(s)
+    s["q"] = s["q"].clone()
+    s["q"][0, 1, 5] = value
+    s["q"][-1, 7, 0] = value
+    o, lse = attend(s)
+    assert api.get_status() == 0
+    hit = torch.zeros(o.shape[:2], dtype=torch.bool, device="cuda")
+    hit[0, 1] = hit[-1, 7] = True
+    if math.isnan(value):
+        assert torch.all(torch.isnan(o[hit])) and torch.all(torch.isnan(lse.t()[hit]))
+    assert torch.equal(o[~hit], want[~hit]) and torch.equal(lse.t()[~hit], want_l.t()[~hit])
+
+
+def test_outputs_apart_from_what_is_read():
+    s = build([2, 1], [50, 20], 4, 2, 64, 16, BF, False, seed=17)
+    flat = s["pages"][0].view(-1)
+    for kw in (dict(out=s["q"]), dict(out=flat[:3 * 4 * 64].view(3, 4, 64)), dict(lse=flat[:24].view(torch.float32).view(4, 3)),
+               dict(workspace=s["q"])):
+        with pytest.raises(ValueError):
+            attend(s, **kw)
+    assert api.get_status() == 0
+
+
 def test_bad_plans_are_reported_and_skip_their_access():
     """Offsets, lengths and page numbers out of range: recorded, and everything else computed."""
     s = build([1, 1, 1], [500, 400, 300], 8, 2, 128, 32, BF, False, seed=12)
