@@ -371,17 +371,28 @@ def _check_heads(name: str, t: torch.Tensor, like: torch.Tensor | None = None) -
     strides), of ``like``'s type and device."""
     if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4):
         raise ValueError(f"{name} must be [tokens, heads, d] or [batch, seq_len, heads, d]")
-    if t.dtype not in _SIXTEEN or (like is not None and t.dtype != like.dtype):
-        raise TypeError(f"{name} must be bfloat16 or float16, one type for all, got {t.dtype}")
+    dtype = t.dtype
+    if dtype not in _SIXTEEN or (like is not None and dtype != like.dtype):
+        raise TypeError(f"{name} must be bfloat16 or float16, one type for all, got {dtype}")
     if not t.is_cuda or (like is not None and t.get_device() != like.get_device()):
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path), one device for all")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
+    if t.stride()[-1] != 1 and t.shape[-1] != 1:
         raise ValueError(f"{name} must have contiguous columns")
 
 
 def _span(t: torch.Tensor) -> tuple[int, int]:
     last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
     return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _check_apart(name: str, out: torch.Tensor, *others: torch.Tensor | None) -> None:
+    """A caller's output that the call would write while it still reads, or writes, one of the others."""
+    lo, hi = _span(out)
+    for t in others:
+        if t is not None and t.numel() and out.numel():
+            first, end = _span(t)
+            if lo < end and first < hi:
+                raise ValueError(f"{name} must not overlap the call's other tensors")
 
 
 def _check_rope_out(name: str, out: torch.Tensor, x: torch.Tensor, *others: torch.Tensor) -> None:
@@ -409,25 +420,31 @@ def _empty_like(t: torch.Tensor) -> torch.Tensor:
 
 
 def _strides3(t: torch.Tensor):
-    return (t.stride(0) if t.dim() == 4 else 0, t.stride(-3), t.stride(-2))
+    s = t.stride()
+    return s[:3] if len(s) == 4 else (0, s[0], s[1])
+
+
+_NO_STRIDES = (0, 0, 0)
 
 
 def _rope(q, k, positions, inv_freq, interleaved, factor, q_out, k_out, inverse):
     _check_heads("q", q)
+    shape, device = q.shape, q.get_device()
     if k is not None:
         _check_heads("k", k, q)
-        if k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
-            raise ValueError(f"k {tuple(k.shape)} does not fit q {tuple(q.shape)}")
+        k_shape = k.shape
+        if len(k_shape) != len(shape) or k_shape[:-2] != shape[:-2] or k_shape[-1] != shape[-1]:
+            raise ValueError(f"k {tuple(k_shape)} does not fit q {tuple(shape)}")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    lead = q.shape[:-2]
+    lead, d = shape[:-2], shape[-1]
     if (not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64)
-            or positions.device != q.device or (positions.shape != lead and positions.shape != lead[-1:])):
+            or positions.get_device() != device or positions.shape not in (lead, lead[-1:])):
         raise ValueError(f"positions must be int32 or int64 of shape {tuple(lead)} or {tuple(lead[-1:])} on {q.device}")
     if (not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1
-            or inv_freq.device != q.device or not inv_freq.is_contiguous()
-            or not 1 <= inv_freq.numel() <= q.shape[-1] // 2):
-        raise ValueError(f"inv_freq must be a contiguous float64 vector of 1 to {q.shape[-1] // 2} entries on {q.device}")
+            or inv_freq.get_device() != device or not inv_freq.is_contiguous()
+            or not 1 <= inv_freq.numel() <= d // 2):
+        raise ValueError(f"inv_freq must be a contiguous float64 vector of 1 to {d // 2} entries on {q.device}")
     given = (q_out, k_out)
     q_out = _empty_like(q) if q_out is None else q_out
     if k is not None and k_out is None:
@@ -438,17 +455,20 @@ def _rope(q, k, positions, inv_freq, interleaved, factor, q_out, k_out, inverse)
         _check_rope_out("k_out", k_out, k, q)
     if q.numel() == 0 and (k is None or k.numel() == 0):
         return q_out, k_out
-    B, N = (1, q.shape[0]) if q.dim() == 3 else (q.shape[0], q.shape[1])
-    none = (0, 0, 0)
-    p = _pack_rope(B, N, q.shape[-2], 0 if k is None else k.shape[-2], q.shape[-1], 2 * inv_freq.numel(),
-                   int(bool(interleaved)), int(inverse), float(factor), FA_DTYPE[q.dtype],
-                      int(positions.dtype == torch.int64), *_strides3(q), *(none if k is None else _strides3(k)),
-                      *_strides3(q_out), *(none if k is None else _strides3(k_out)),
-                      positions.stride(0) if positions.dim() == 2 else 0, positions.stride(-1))
+    B, N = (1, shape[0]) if len(shape) == 3 else (shape[0], shape[1])
+    pos_stride = positions.stride()
+    if k is None:
+        k_heads, k_strides, k_out_strides, k_ptr, k_out_ptr = 0, _NO_STRIDES, _NO_STRIDES, None, None
+    else:
+        k_heads, k_strides, k_out_strides = k_shape[-2], _strides3(k), _strides3(k_out)
+        k_ptr, k_out_ptr = k.data_ptr(), k_out.data_ptr()
+    p = _pack_rope(B, N, shape[-2], k_heads, d, 2 * inv_freq.numel(), 1 if interleaved else 0, 1 if inverse else 0,
+                   float(factor), FA_DTYPE[q.dtype], 1 if positions.dtype == torch.int64 else 0, *_strides3(q),
+                   *k_strides, *_strides3(q_out), *k_out_strides, pos_stride[0] if len(pos_stride) == 2 else 0,
+                   pos_stride[-1])
     with _on(q):
-        st = lib().fa_rope(p, q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
-                           None if k is None else k_out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
-                           _stream_ptr(q))
+        st = lib().fa_rope(p, q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr, positions.data_ptr(),
+                           inv_freq.data_ptr(), _stream_ptr(q))
     if st != 0:
         raise FAError(st, "fa_rope")
     return q_out, k_out
@@ -478,31 +498,50 @@ def rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, positions: torch.Tensor,
 
 
 _SCALE_TYPES = (torch.float8_e8m0fnu, torch.uint8)
+_INT32 = (torch.int32,)
+
+
+def _is(t, shape, dtypes, device: int) -> bool:
+    """A contiguous tensor of this shape, one of these types, on this device."""
+    return (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.get_device() == device
+            and t.is_contiguous())
 
 
 def _check_pages(k_pages, v_pages, page_table, seqlens, k_scales, v_scales, dtype) -> bool:
     """The tensors of a paged cache read or written as ``dtype``; True for an e4m3 pool."""
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
         if (not isinstance(t, torch.Tensor) or t.dim() != 4 or not t.is_cuda or not t.is_contiguous()
-                or 0 in t.shape):
+                or t.numel() == 0):
             raise ValueError(f"{name} must be a contiguous CUDA tensor [pages, kv_heads, page, d], none of them 0")
-    if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or k_pages.device != v_pages.device:
+    shape, kind, device = k_pages.shape, k_pages.dtype, k_pages.get_device()
+    if v_pages.shape != shape or v_pages.dtype != kind or v_pages.get_device() != device:
         raise ValueError("k_pages and v_pages must have one shape, dtype and device")
-    quant = k_pages.dtype == torch.float8_e4m3fn
-    if not quant and k_pages.dtype != dtype:
-        raise TypeError(f"pages of {k_pages.dtype} do not fit {dtype} (pages are of that type, or float8_e4m3fn)")
-    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        if not quant and t is not None:
-            raise ValueError(f"{name} given for 16-bit pages")
-        if quant and (not isinstance(t, torch.Tensor) or t.dtype not in _SCALE_TYPES or t.device != k_pages.device
-                      or t.shape != k_pages.shape[:3] or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous float8_e8m0fnu tensor of shape {tuple(k_pages.shape[:3])} "
-                             f"on {k_pages.device}")
+    quant = kind == torch.float8_e4m3fn
+    if not quant:
+        if kind != dtype:
+            raise TypeError(f"pages of {kind} do not fit {dtype} (pages are of that type, or float8_e4m3fn)")
+        if k_scales is not None or v_scales is not None:
+            raise ValueError("scales given for 16-bit pages")
+    elif not (_is(k_scales, shape[:3], _SCALE_TYPES, device) and _is(v_scales, shape[:3], _SCALE_TYPES, device)):
+        raise ValueError(f"k_scales and v_scales must be contiguous float8_e8m0fnu tensors of shape {tuple(shape[:3])} "
+                         f"on {k_pages.device}")
     if (not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.dtype != torch.int32
-            or page_table.device != k_pages.device or not page_table.is_contiguous()):
+            or page_table.get_device() != device or not page_table.is_contiguous()):
         raise ValueError(f"page_table must be a contiguous int32 [sequences, pages] tensor on {k_pages.device}")
-    check_buffer("seqlens", seqlens, (page_table.shape[0],), torch.int32, k_pages.device)
+    if not _is(seqlens, page_table.shape[:1], _INT32, device):
+        check_buffer("seqlens", seqlens, (page_table.shape[0],), torch.int32, k_pages.device)
     return quant
+
+
+def _check_pools(a: torch.Tensor, b: torch.Tensor, *rows: torch.Tensor) -> None:
+    """Pools that are written: apart from each other and from the rows written to them."""
+    nbytes, pa, pb = a.numel() * a.element_size(), a.data_ptr(), b.data_ptr()
+    if abs(pa - pb) < nbytes:
+        raise ValueError("the pools of keys and values must not overlap")
+    for t in rows:
+        at = t.data_ptr()
+        if pa <= at < pa + nbytes or pb <= at < pb + nbytes:
+            raise ValueError("new keys and values must not lie in the pools")
 
 
 def _ptr(t: torch.Tensor | None):
@@ -527,13 +566,18 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     quant = _check_pages(k_pages, v_pages, page_table, seqlens, k_scales, v_scales, k.dtype)
     P, H_kv, page, d = k_pages.shape
     B, max_pages = page_table.shape
-    if k.device != k_pages.device or k.shape[1:] != (H_kv, d):
+    T, heads, width = k.shape
+    if k.get_device() != k_pages.get_device() or heads != H_kv or width != d:
         raise ValueError(f"k {tuple(k.shape)} does not fit pages {tuple(k_pages.shape)} on {k_pages.device}")
-    check_buffer("cu_q", cu_q, (B + 1,), torch.int32, k.device)
-    if k.shape[0] == 0:
+    if not _is(cu_q, (B + 1,), _INT32, k.get_device()):
+        check_buffer("cu_q", cu_q, (B + 1,), torch.int32, k.device)
+    _check_pools(k_pages, v_pages, k, v)
+    if quant:
+        _check_pools(k_scales, v_scales, k, v)
+    if T == 0:
         return
-    p = _pack_cache(B, k.shape[0], H_kv, d, P, max_pages, page, FA_DTYPE[k.dtype], int(quant),
-                       k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+    p = _pack_cache(B, T, H_kv, d, P, max_pages, page, FA_DTYPE[k.dtype], 1 if quant else 0, *k.stride()[:2],
+                    *v.stride()[:2])
     with _on(k):
         st = lib().fa_cache_append(p, k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                                    _ptr(k_scales), _ptr(v_scales), page_table.data_ptr(), seqlens.data_ptr(),
@@ -562,17 +606,21 @@ def cache_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch
     total = int(total)
     if total < 0:
         raise ValueError(f"total must not be negative, got {total}")
-    check_buffer("cu_k", cu_k, (B + 1,), torch.int32, k_pages.device)
-    if starts is not None:
+    device = k_pages.get_device()
+    if not _is(cu_k, (B + 1,), _INT32, device):
+        check_buffer("cu_k", cu_k, (B + 1,), torch.int32, k_pages.device)
+    if starts is not None and not _is(starts, (B,), _INT32, device):
         check_buffer("starts", starts, (B,), torch.int32, k_pages.device)
-    shape = (total, H_kv, d)
-    k_out = torch.empty(shape, dtype=dtype, device=k_pages.device) if k_out is None else k_out
-    v_out = torch.empty(shape, dtype=dtype, device=k_pages.device) if v_out is None else v_out
-    check_buffer("k_out", k_out, shape, dtype, k_pages.device)
-    check_buffer("v_out", v_out, shape, dtype, k_pages.device)
+    shape, given = (total, H_kv, d), (k_out, v_out)
+    k_out = k_pages.new_empty(shape, dtype=dtype) if k_out is None else k_out
+    v_out = k_pages.new_empty(shape, dtype=dtype) if v_out is None else v_out
+    for name, out, other in (("k_out", given[0], v_out), ("v_out", given[1], k_out)):
+        if out is not None:
+            check_buffer(name, out, shape, dtype, k_pages.device)
+            _check_apart(name, out, other, k_pages, v_pages, k_scales, v_scales)
     if total == 0:
         return k_out, v_out
-    p = _pack_cache(B, total, H_kv, d, P, max_pages, page, FA_DTYPE[dtype], int(quant), 0, 0, 0, 0)
+    p = _pack_cache(B, total, H_kv, d, P, max_pages, page, FA_DTYPE[dtype], 1 if quant else 0, 0, 0, 0, 0)
     with _on(k_pages):
         st = lib().fa_cache_gather(p, k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
                                    _ptr(v_scales), page_table.data_ptr(), seqlens.data_ptr(), cu_k.data_ptr(),
@@ -586,10 +634,10 @@ def _paged_problem(q, k_pages, page_table, max_q, causal, scale, window, quant) 
     T, H, d = q.shape
     P, H_kv, page, _ = k_pages.shape
     B, max_pages = page_table.shape
+    stride = q.stride()
     return _pack_paged(B, T, H, H_kv, int(max_q), P, max_pages, page, d,
-                          1.0 / math.sqrt(d) if scale is None else float(scale), int(bool(causal)),
-                          -1 if window is None else int(window), FA_DTYPE[q.dtype], int(quant),
-                          q.stride(0), q.stride(1))
+                       1.0 / math.sqrt(d) if scale is None else float(scale), 1 if causal else 0,
+                       -1 if window is None else int(window), FA_DTYPE[q.dtype], 1 if quant else 0, stride[0], stride[1])
 
 
 def paged_workspace_size(q: torch.Tensor, k_pages: torch.Tensor, page_table: torch.Tensor, max_q: int) -> int:
@@ -618,27 +666,32 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
         raise ValueError("q must be [tokens, heads, d]")
     quant = _check_pages(k_pages, v_pages, page_table, seqlens, k_scales, v_scales, q.dtype)
     T, H, d = q.shape
-    if q.device != k_pages.device or d != k_pages.shape[3] or H % k_pages.shape[1] != 0:
+    device = q.get_device()
+    if device != k_pages.get_device() or d != k_pages.shape[3] or H % k_pages.shape[1] != 0:
         raise ValueError(f"q {tuple(q.shape)} does not fit pages {tuple(k_pages.shape)} on {k_pages.device} "
                          "(key/value heads must divide the query heads)")
-    check_buffer("cu_q", cu_q, (page_table.shape[0] + 1,), torch.int32, q.device)
+    if not _is(cu_q, (page_table.shape[0] + 1,), _INT32, device):
+        check_buffer("cu_q", cu_q, (page_table.shape[0] + 1,), torch.int32, q.device)
     if out is None:
         out = _empty_like(q)
     else:
         check_buffer("out", out, q.shape, q.dtype, q.device)
+        _check_apart("out", out, q, k_pages, v_pages, k_scales, v_scales)
     if lse is None:
-        lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((H, T), dtype=torch.float32)
     else:
         check_buffer("lse", lse, (H, T), torch.float32, q.device)
+        _check_apart("lse", lse, out, q, k_pages, v_pages, k_scales, v_scales)
     if T == 0:
         return out, lse
     p = _paged_problem(q, k_pages, page_table, max_q, causal, scale, window, quant)
     with _on(q):
         if workspace is None:
             need = int(lib().fa_paged_workspace_size(p))
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty(max(need, 1), dtype=torch.uint8)
         else:
             check_scratch("workspace", workspace, q.device)
+            _check_apart("workspace", workspace, q, out, lse)
         st = lib().fa_paged(p, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
                             _ptr(v_scales), page_table.data_ptr(), seqlens.data_ptr(), cu_q.data_ptr(),
                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),

@@ -221,3 +221,16 @@ def test_cache_refusals():
     three = [torch.zeros(4, 2, 48, 64, dtype=torch.bfloat16, device="cuda") for _ in "kv"]    # pages of 48
     with pytest.raises(api.FAError):
         api.cache_gather(*three, s["table"], s["seqlens"], s["cu"], 2)
+
+
+def test_cache_buffers_that_overlap():
+    s = build([2], [20], 2, 64, 16, torch.bfloat16, True, seed=12)
+    for kw in (dict(v_pages=s["pages"][0]), dict(v_scales=s["scales"][0])):
+        with pytest.raises(ValueError):
+            append(s, **kw)
+    out = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    for k_out, v_out in ((out[:2], out[1:]), (out[:2], out[:2])):
+        with pytest.raises(ValueError):
+            api.cache_gather(*s["pages"], s["table"], s["seqlens"], s["cu"], 2, k_scales=s["scales"][0],
+                             v_scales=s["scales"][1], k_out=k_out, v_out=v_out)
+    assert api.get_status() == 0

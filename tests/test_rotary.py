@@ -96,3 +96,16 @@ def test_rope_output_apart_from_its_inputs(monkeypatch):
         api._check_rope_out("q_out", buf[1:9, :4], q, k)        # shifted by a token
     with pytest.raises(ValueError):
         api._check_rope_out("k_out", q, q[:, :4], q)            # another input too
+
+
+def test_buffers_that_overlap():
+    buf = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    k, v = buf[:2], buf[2:]
+    rows = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    api._check_pools(k, v, rows, rows)                          # two halves of one pool
+    for a, b, r in ((k, k, rows), (buf[:3], buf[1:], rows), (k, v, v[0, 0, :3])):
+        with pytest.raises(ValueError):
+            api._check_pools(a, b, r)
+    api._check_apart("out", k, v, None, rows, rows[:0])
+    with pytest.raises(ValueError):
+        api._check_apart("out", k, rows, buf[1:3])
