@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) fa_rope_kernel(const RopeArgs
         const int w = h0 + in.h >= a.H;
         const T* x = static_cast<const T*>(a.x[w]) + in.offset(a, a.xs, h0 + in.h, w);
         if (FA_IN_BOUNDS(t0 + in.tk < static_cast<int64_t>(a.B) * a.N && c1 + 8 <= a.d, a.status, 401)) {
-          v0[u] = *reinterpret_cast<const uint4*>(x + c0);  // plain loads: y may be x
-          v1[u] = *reinterpret_cast<const uint4*>(x + c1);
+          v0[u] = __ldcs(reinterpret_cast<const uint4*>(x + c0));  // coherent: y may be x
+          v1[u] = __ldcs(reinterpret_cast<const uint4*>(x + c1));
         }
         in.next(nh);
       }
@@ -182,8 +182,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) fa_rope_kernel(const RopeArgs
       const int w = h0 + out.h >= a.H;
       T* y = static_cast<T*>(a.y[w]) + out.offset(a, a.ys, h0 + out.h, w);
       if (FA_IN_BOUNDS(t0 + tk < static_cast<int64_t>(a.B) * a.N && c1 + 8 <= a.d, a.status, 402)) {
-        *reinterpret_cast<uint4*>(y + c0) = v0[u];
-        *reinterpret_cast<uint4*>(y + c1) = v1[u];
+        __stcs(reinterpret_cast<uint4*>(y + c0), v0[u]);
+        __stcs(reinterpret_cast<uint4*>(y + c1), v1[u]);
       }
       out.next(nh);
     }

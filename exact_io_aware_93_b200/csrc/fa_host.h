@@ -25,7 +25,7 @@ struct DeviceInfo {
   bool fwd_attr[3][2][2] = {};  // [element type][d==128][causal]
   bool bwd_attr[2][2][2] = {};
   bool dec_attr[2][2][4] = {};  // [fp16][d==128][M = 128; M = 64 with 1, 2, 4 row copies]
-  bool paged_attr[2][2][2][4] = {};  // [fp16][e4m3 pages][d==128][tiles; 8, 16, 32 rows]
+  bool paged_attr[2][2][2][3] = {};  // [fp16][e4m3 pages][d==128][tiles; 8, 16 rows]
 };
 
 // Defined in fa_api.cu.

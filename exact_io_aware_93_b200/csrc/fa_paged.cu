@@ -26,9 +26,9 @@ fa_status check_paged(const fa_paged_problem& p) {
   const long long cap = static_cast<long long>(p.max_pages) * p.page;
   const long long planes = static_cast<long long>(p.P) * p.H_kv;
   if (cap > INT_MAX - 1024 || planes >= INT_MAX || p.H_kv > 65535 || p.T > INT_MAX / 4) return FA_ERR_INVALID_ARG;
-  // the work list is counted in 32 bits, up to 3 units of cost per key tile
+  // the work list is counted in 32 bits, up to 3 units of cost per key tile and 8 per unit
   const int tq = 128 / (p.H / p.H_kv);
-  const long double cost = 3.0L * fa::paged_units(p, p.max_q, tq) * p.H_kv * ((cap + 127) / 128);
+  const long double cost = fa::paged_units(p, p.max_q, tq) * (3.0L * ((cap + 127) / 128) + 8.0L) * p.H_kv;
   if (cost > static_cast<long double>(INT_MAX / 2)) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }

@@ -10,7 +10,7 @@
 // Work list.  A unit visits T = hi - lo tiles of 128 keys, those that some row of it sees
 // (causal: up to its last token; window: from its first token's first key).  The key tiles of
 // all units are laid end to end (sequence, key/value head, unit), each as long as it takes
-// (Cfg::kPairCost, kSplitCost), and CTA c of the persistent grid takes the tiles that start in
+// (Cfg::kPairCost, kSplitCost, and kUnitCost once per unit: its epilogue), and CTA c of the persistent grid takes the tiles that start in
 // [c L, (c+1) L), L = total / grid: every SM gets the same work whatever the mix of chunks,
 // single tokens and lengths.  A CTA's run falls into SEGMENTS, each inside one unit; a segment
 // that is not a whole unit leaves a partial result (O normalised, log-sums) that
@@ -23,6 +23,8 @@
 // of the unit sees are not fetched, and value rows outside the unit's keys are zeroed in shared
 // memory: stale slots, and pages a sliding window has left behind, may hold anything.
 #pragma once
+
+#include <type_traits>
 
 #include "fa_cache_kernels.cuh"
 #include "fa_fwd_kernel.cuh"
@@ -102,6 +104,7 @@ struct PgArgs {
   int B, T, H, H_kv, max_q, TQ, max_pages, page, page_shift, P, window, causal;
   float scale_log2;
   long long slots;        // 2 per CTA
+  int behind;             // launched behind the few-rows kernel of the same call
   int* status;
 };
 
@@ -151,14 +154,19 @@ __device__ __forceinline__ bool pg_is_pair(const PgArgs& a, const PgSeq& s, int 
   return s.n - u * 2 * a.TQ > a.TQ;
 }
 
+// Cost of a unit: its end (kUnitCost, which lies before its first tile in the list), then its tiles.
+template <typename Cfg>
+__device__ __forceinline__ int pg_unit_cost(const PgArgs& a, const PgSeq& s, int u) {
+  const PgKeys k = pg_unit_keys(a, s, u);
+  const int tiles = k.t1 - k.t0;
+  return tiles > 0 ? Cfg::kUnitCost + tiles * (pg_is_pair(a, s, u) ? Cfg::kPairCost : Cfg::kSplitCost) : 0;
+}
+
 // Cost of a sequence's units for one key/value head.
 template <typename Cfg>
 __device__ __forceinline__ int pg_seq_cost(const PgArgs& a, const PgSeq& s) {
   int w = 0;
-  for (int u = 0; u < s.units; ++u) {
-    const PgKeys k = pg_unit_keys(a, s, u);
-    w += (k.t1 - k.t0) * (pg_is_pair(a, s, u) ? Cfg::kPairCost : Cfg::kSplitCost);
-  }
+  for (int u = 0; u < s.units; ++u) w += pg_unit_cost<Cfg>(a, s, u);
   return w;
 }
 
@@ -202,8 +210,7 @@ __device__ __forceinline__ void pg_plan(const PgArgs& a, int lane, PgPlan* out) 
         p.kvh = (p.t0 - excl) / w;
         p.start = excl + p.kvh * w;
         while (true) {
-          const PgKeys k = pg_unit_keys(a, s, p.u);
-          const int c = (k.t1 - k.t0) * (pg_is_pair(a, s, p.u) ? Cfg::kPairCost : Cfg::kSplitCost);
+          const int c = pg_unit_cost<Cfg>(a, s, p.u);
           if (p.t0 < p.start + c) break;
           p.start += c;
           ++p.u;
@@ -273,11 +280,11 @@ struct PgWalk {
       const int cost = pair ? Cfg::kPairCost : Cfg::kSplitCost;
       const int T = k.t1 - k.t0;
       // the tiles that start in [t0, t1)
-      const int first = t0 > start ? (t0 - start + cost - 1) / cost : 0;
-      const int last = min(T, (t1 - start + cost - 1) / cost);
+      const int begin = start + Cfg::kUnitCost;
+      const int first = t0 > begin ? (t0 - begin + cost - 1) / cost : 0;
+      const int last = t1 > begin ? min(T, (t1 - begin + cost - 1) / cost) : 0;
       const int tok0 = u * 2 * a.TQ;
-      const int begin = start;
-      start += T * cost;
+      if (T > 0) start = begin + T * cost;
       ++u;
       if (first >= last) continue;
       g.b = b;
@@ -512,14 +519,15 @@ __device__ __forceinline__ void pg_clean(const PgSeg& g, int j, uint8_t* tile, i
 // Every query row is scaled by a power of two, 2^e the smallest with max|row| <= 448 * 2^e, and
 //   kPieces   cut into that many e4m3 pieces, each the rounding of what the ones before it left:
 //             two hold a bf16, three an fp16, exactly, down to 2^-18 of the row's largest
-//   0         written as fp16: exact for both types, down to 2^-33 of the row's largest
-// Piece i of (token, head) lies at out[((i T + token) H + head) D], fp16 rows likewise; factors
+//   kHalf     written as fp16: exact for both types, down to 2^-33 of the row's largest
+// Piece i of (token, head) lies at pieces[((i T + token) H + head) D], fp16 rows likewise at half; factors
 // 2^e at q_scale[token H + head].  D / 16 lanes per row.
-template <int D, Elem E, int kPieces>
+template <int D, Elem E, int kPieces, bool kHalf>
 __global__ void __launch_bounds__(256) fa_paged_scale_q_kernel(const void* q, int64_t token_stride, int64_t head_stride,
-                                                               uint8_t* out, float* q_scale, int T, int H,
-                                                               int* status) {
+                                                               uint8_t* pieces, uint8_t* half, float* q_scale, int T,
+                                                               int H, int* status) {
   constexpr int L = D / 16;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the kernel before it may still run
   const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / L;
   const int item = threadIdx.x % L;
   const bool live = row < static_cast<int64_t>(T) * H;
@@ -551,29 +559,28 @@ __global__ void __launch_bounds__(256) fa_paged_scale_q_kernel(const void* q, in
   if (!live || !FA_IN_BOUNDS(token < T && h < H && item * 16 + 16 <= D, status, 510)) return;
 #pragma unroll
   for (int i = 0; i < 16; ++i) f[i] *= inv;
-  if constexpr (kPieces > 0) {
-#pragma unroll
-    for (int p = 0; p < kPieces; ++p) {
-      uint32_t c[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[i] = pack_e4m3x4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-        const float2 a = e4m3x2_to_float2(c[i]), b = e4m3x2_to_float2(c[i] >> 16);
-        f[4 * i] -= a.x;
-        f[4 * i + 1] -= a.y;
-        f[4 * i + 2] -= b.x;
-        f[4 * i + 3] -= b.y;
-      }
-      *reinterpret_cast<uint4*>(out + ((static_cast<int64_t>(p) * T + token) * H + h) * D + item * 16) =
-          make_uint4(c[0], c[1], c[2], c[3]);
-    }
-  } else {
+  if constexpr (kHalf) {
     uint32_t c[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = pack_f16x2(f[2 * i], f[2 * i + 1]);
-    uint4* dst = reinterpret_cast<uint4*>(out + (row * D + item * 16) * 2);
+    uint4* dst = reinterpret_cast<uint4*>(half + (row * D + item * 16) * 2);
     dst[0] = make_uint4(c[0], c[1], c[2], c[3]);
     dst[1] = make_uint4(c[4], c[5], c[6], c[7]);
+  }
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = pack_e4m3x4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+      const float2 a = e4m3x2_to_float2(c[i]), b = e4m3x2_to_float2(c[i] >> 16);
+      f[4 * i] -= a.x;
+      f[4 * i + 1] -= a.y;
+      f[4 * i + 2] -= b.x;
+      f[4 * i + 3] -= b.y;
+    }
+    *reinterpret_cast<uint4*>(pieces + ((static_cast<int64_t>(p) * T + token) * H + h) * D + item * 16) =
+        make_uint4(c[0], c[1], c[2], c[3]);
   }
   if (item == 0) q_scale[row] = __int_as_float((127 + e) << 23);
 }
@@ -582,7 +589,8 @@ __global__ void __launch_bounds__(256) fa_paged_scale_q_kernel(const void* q, in
 // Per row: LSE = log sum_s exp(lse_s) and O = sum_s exp(lr_s - LR) O_s with LR = log sum_s
 // exp(lr_s), the convex combination one CTA would have formed.  Blocks (c, y) with c < `ctas` take
 // the unit that CTA c began and did not finish; further blocks c = ctas + b give the rows of
-// sequence b's units without keys O = 0, LSE = -inf.  All other rows were written by their CTA.
+// sequence b's units without keys O = 0, LSE = -inf.  All other rows were written by their CTA.  A mixed
+// batch is joined by one launch, y below `many_y` the tiles' part, the others the few rows'.
 //
 // A warp takes 32 / L rows at a time: L lanes form the weights of a row's next L partial results,
 // then all 32 lanes share each row's columns.  Tiles of 128 leave many rows of two or three partial
@@ -590,23 +598,21 @@ __global__ void __launch_bounds__(256) fa_paged_scale_q_kernel(const void* q, in
 // with 2048 tokens at 32K 1042 / 1044 / 1098 us, one of 24 sequences of 30 rows 70.5 / 68.0 / 66.6).
 // Few rows leave up to a hundred partial results: L = 32, and W warps share a row's.
 template <int D, Elem E, typename Cfg, int L, int W, int kThreads>
-__global__ void __launch_bounds__(kThreads) fa_paged_merge_kernel(const PgArgs a, int ctas) {
+__device__ __forceinline__ void pg_merge(const PgArgs& a, int ctas, int by, int ny, float (*acc_sh)[D]) {
   using T = typename ElemOps<E>::T;
   constexpr unsigned kFull = 0xffffffffu;
   constexpr int V = D / 32;       // columns per lane
   constexpr int R = 32 / L;       // rows per warp
   constexpr int kRowsAtOnce = kThreads / 32 / W * R;
   static_assert(W == 1 || (R == 1 && kThreads == 32 * W), "warps that share a row are a block");
-  __shared__ float acc_sh[W][D];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int G = a.H / a.H_kv;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results are there
   if (static_cast<int>(blockIdx.x) >= ctas) {
     const int b = static_cast<int>(blockIdx.x) - ctas;
     const PgSeq s = pg_seq(a, b);
     // a token at a position >= 0 sees itself
-    if (blockIdx.y > 0 || (s.len > 0 && (!a.causal || s.len >= s.n))) return;
+    if (by > 0 || (s.len > 0 && (!a.causal || s.len >= s.n))) return;
     for (int u = 0; u < s.units; ++u) {
       const PgKeys k = pg_unit_keys(a, s, u);
       if (k.t1 > k.t0) continue;
@@ -635,7 +641,7 @@ __global__ void __launch_bounds__(kThreads) fa_paged_merge_kernel(const PgArgs a
   auto part = [&](int i) -> int64_t {
     return static_cast<int64_t>(2 * (static_cast<int>(blockIdx.x) + i) + (i == 0)) * (Cfg::kSubs * Cfg::kRows);
   };
-  for (int row0 = blockIdx.y * kRowsAtOnce + (W > 1 ? 0 : warp * R); row0 < rows; row0 += gridDim.y * kRowsAtOnce) {
+  for (int row0 = by * kRowsAtOnce + (W > 1 ? 0 : warp * R); row0 < rows; row0 += ny * kRowsAtOnce) {
     // this lane's row and partial results sl, sl + L, ..; behind the last row the last again, not stored
     const int mine_at = in_part(min(row0 + lane / L, rows - 1)), sl = lane % L;
     const float* po[R];
@@ -734,6 +740,23 @@ __global__ void __launch_bounds__(kThreads) fa_paged_merge_kernel(const PgArgs a
       }
     }
   }
+}
+
+// FewCfg, ManyCfg: the kernels of the call, void for one that it does not take.
+template <int D, Elem E, typename FewCfg, typename ManyCfg, int kThreads>
+__global__ void __launch_bounds__(kThreads) fa_paged_merge_kernel(const PgArgs few, const PgArgs many, int ctas, int many_y) {
+  constexpr int W = kThreads / 32;
+  __shared__ float acc_sh[W][D];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results are there
+  const int y = static_cast<int>(blockIdx.y);
+  if constexpr (!std::is_void_v<ManyCfg>) {
+    if (y < many_y) {
+      pg_merge<D, E, ManyCfg, 16, 1, kThreads>(many, ctas, y, many_y, nullptr);
+      return;
+    }
+  }
+  if constexpr (!std::is_void_v<FewCfg>)
+    pg_merge<D, E, FewCfg, 32, W, kThreads>(few, ctas, y - many_y, static_cast<int>(gridDim.y) - many_y, acc_sh);
 }
 
 }  // namespace fa

@@ -1,5 +1,5 @@
 // fa_paged_few_kernel.cuh -- exact attention over a paged cache for few query rows per key/value
-// head (up to 32: single tokens, drafted tokens), for sm_100a.  The work list, the page loads and
+// head (up to 16: single tokens, drafted tokens), for sm_100a.  The work list, the page loads and
 // the join of partial results are in fa_paged_common.cuh.
 //
 // The cache is a stream: nothing but its bytes should cost time, so the KEYS take the 128 rows of
@@ -54,8 +54,11 @@ struct PfCfg {
   static constexpr int kPPieces = E == Elem::kF16 ? 4 : 3;  // e5m2 pieces of a weight
   static constexpr int kRows = RW;      // rows of a tile and of a partial result
   static constexpr int kSubs = 1;
-  static constexpr int kPairCost = 1;   // units are single tiles
-  static constexpr int kSplitCost = 1;
+  static constexpr int kPairCost = 2;   // units are single tiles
+  static constexpr int kSplitCost = 2;
+  // the end of a unit, as long as 2 key tiles of 16-bit pages and 4 of e4m3 (without: 24 sequences of
+  // 512 tokens 20.5 us, with 16.9; e4m3 24.8 and 21.6)
+  static constexpr int kUnitCost = Q8 ? 8 : 4;
   static constexpr int kThreads = 384;
   static constexpr int kAhead = 3;      // key tiles whose scores run ahead of their values
   static constexpr int kSBufs = 4;
@@ -73,7 +76,7 @@ struct PfCfg {
   static constexpr int kPChunks = Q8 ? 1 : 2;         // 128 keys of a row in 128-byte chunks
   static constexpr int kPChunkBytes = kNO * 128;
   static constexpr int kPBytes = kPChunks * kPChunkBytes;
-  static constexpr int kStages = (Q8 ? (RW == 32 ? 10 : (RW == 16 && E == Elem::kF16 ? 11 : 12)) : 6) * (128 / D);
+  static constexpr int kStages = (Q8 ? (RW == 16 && E == Elem::kF16 ? 11 : 12) : 6) * (128 / D);
   static constexpr int kScaleRing = 8;  // key tiles
   static constexpr int kSegRing = 4;
   static constexpr int kSegReaders = 10;  // warps
@@ -196,6 +199,10 @@ __global__ void __launch_bounds__(384, 1)
     tmem_alloc(&sm.tmem_base, Cfg::kTmemCols);
     tmem_relinquish();
   }
+  // Launched while the kernel before it may still run: what that one writes is read from here on.
+  // (e4m3 pages: it is the scaling of the queries, which has waited for the kernel before it and
+  // writes nothing that the plan reads.)
+  if constexpr (!Q8) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 8) {
     if (lane == 0) {
       tma_prefetch_desc(&tm_q);
@@ -208,7 +215,6 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
-  // launched while the kernel that scales the queries may still run
   if constexpr (Q8) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 

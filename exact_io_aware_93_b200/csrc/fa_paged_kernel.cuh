@@ -49,6 +49,10 @@ struct PgCfg {
   // time of a key tile, in the work list's units: of a pair, and of a single tile
   static constexpr int kPairCost = 3;
   static constexpr int kSplitCost = 2;
+  // the end of a unit, 5.5 us.  (Without it CTAs of several short units ended 18 us after the mean: 24
+  // sequences of 700 to 16384 tokens, 5 new ones each, window 4096, 64.6 us; 4 / 6 / 8 / 12: 56.3 / 52.6 /
+  // 51.6 / 51.3.)
+  static constexpr int kUnitCost = 8;
   static constexpr int kChunks = D / 64;              // 128-byte chunks of a 16-bit row
   static constexpr int kChunkBytes = 128 * 128;
   static constexpr int kTileBytes = kChunks * kChunkBytes;
@@ -175,6 +179,12 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
     tmem_alloc(&sm.tmem_base, Cfg::kTmemCols);
     tmem_relinquish();
   }
+  // Launched while the kernel before it may still run: what that one writes is read from here on.
+  // (e4m3 pages: it is the scaling of the queries, which has waited for the kernel before it and
+  // writes nothing that the plan reads.)  Behind the few-rows kernel (a mixed batch), which has waited
+  // before it let this one start, nothing is left to wait for: its end is waited for at this one's.
+  if constexpr (!Q8)
+    if (!a.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 8) {
     if (lane == 0) {
       tma_prefetch_desc(&tm_q);
@@ -187,8 +197,8 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
-  // launched while the kernel that scales the queries may still run
-  if constexpr (Q8) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (Q8)
+    if (!a.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Readers of the segment ring: the next segment, or null at the end or after an abort; a
@@ -819,6 +829,8 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
     tmem_dealloc(tbase, Cfg::kTmemCols);
   }
   if (threadIdx.x == 0) pg_report(&sm.abort_flag, status);
+  // the join waits for this kernel and reads both kernels' partial results
+  if (a.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace fa

@@ -28,28 +28,27 @@ struct PagedCall {
 // With e4m3 pages, the e4m3 pieces of a query in the few-rows kernel: all bits of a bf16 (8), or of
 // an fp16 (11), four to a piece.
 constexpr int paged_q_pieces(bool f16) { return f16 ? 3 : 2; }
-// Most rows of the few-rows kernel; 32 of fp16 with e4m3 pages would not fit into tensor memory.
-constexpr int paged_most_rows(bool quant, bool f16) { return quant && !f16 ? 32 : 16; }
+// Most rows of a key/value head in the few-rows kernel.  (20 rows, tiles of 128 against an instance for
+// 32 rows: 16-bit pages, 16 sequences of 16-32K tokens, 262 / 270 us; e4m3 pages, 24 of 4096, 84 / 112 us,
+// 24 of 16384, 210 / 231 us.)
+constexpr int kPagedMostRows = 16;
 
 // Which kernels a call takes.  A key/value head's rows, (H / H_kv) * n for n new tokens, choose
 // per sequence: up to `rows` of them the few-rows kernel (n <= few_q), more the tiles of 128.
-//   all sequences few (max_q says so): that kernel alone, at the smallest of 8, 16 and, bf16 with
-//     e4m3 pages, 32 rows.  (16 sequences of 16-32K tokens, 20 rows: 16-bit pages 270 us there and 262 us
-//     in tiles of 128; e4m3 pages 322 and 386 us.)
+//   all sequences few (max_q says so): that kernel alone, at the smaller of 8 and 16 rows
 //   all sequences max_q tokens long (T = B max_q): the tiles alone
-//   a mixture: both, one after the other, single tokens in the first at the smallest size
+//   a mixture: both, one behind the other, single tokens in the first at the smaller size
 struct PagedKernels {
-  int rows;   // 8, 16, 32, or 0: the few-rows kernel is not used
+  int rows;   // 8, 16, or 0: the few-rows kernel is not used
   int few_q;  // its most tokens per sequence
   bool many;
 };
 inline PagedKernels paged_kernels(const fa_paged_problem& p) {
   const int G = p.H / p.H_kv;
   const long long rows = static_cast<long long>(G) * p.max_q;
-  const int most = paged_most_rows(p.quant, p.dtype == FA_DTYPE_F16);
-  if (rows <= most) return {rows <= 8 ? 8 : (rows <= 16 ? 16 : 32), p.max_q, false};
-  if (G > most || static_cast<long long>(p.B) * p.max_q == p.T) return {0, 0, true};
-  const int r = G <= 8 ? 8 : (G <= 16 ? 16 : 32);
+  if (rows <= kPagedMostRows) return {rows <= 8 ? 8 : 16, p.max_q, false};
+  if (G > kPagedMostRows || static_cast<long long>(p.B) * p.max_q == p.T) return {0, 0, true};
+  const int r = G <= 8 ? 8 : 16;
   return {r, r / G, true};
 }
 // At most this many units (pairs of tiles of TQ tokens) per key/value head among sequences of up

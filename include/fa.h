@@ -420,8 +420,8 @@ typedef struct fa_paged_problem {
 
 /*
  * Bytes of device workspace fa_paged needs on the CURRENT device: per kernel that the call may
- * take (one for up to 32 rows of a key/value head, one for more) a plan, two partial results per
- * SM (of 8, 16 or 32 rows, or 256) of 4 * d + 8 bytes per row and, with e4m3 pages, 2 * d bytes
+ * take (one for up to 16 rows of a key/value head, one for more) a plan, two partial results per
+ * SM (of 8 or 16 rows, or 256) of 4 * d + 8 bytes per row and, with e4m3 pages, 2 * d bytes
  * (fp16: up to 3 * d) per query row; with e4m3 pages 4 more per query row.
  * 0 for an invalid or unsupported problem or without an sm_100 device.
  */
