@@ -625,70 +625,90 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
           float c_tile = c_row;
           if constexpr (Q8) c_tile *= sm.scales[grp][ss].k;
           const bool masked = k0 + kBN - 1 > all_hi || k0 < all_lo;
-          // A row is taken in halves, first for its maximum and then for its weights.  With e4m3 pages
-          // in one rolled loop: the roles' code together has to stay in the instruction cache
-          // (unrolled, with the conversion beside it, every warp ran two to three times slower).  P
-          // lies over the second half of S, which is read last before it is overwritten.
-          float mx = -INFINITY, m_use = 0.f;
-          uint32_t s[64];
-#pragma unroll(Q8 ? 1 : 4)
-          for (int pass = 0; pass < 4; ++pass) {
-            const int half = pass == 1 || pass == 2;
-            if (Q8 || pass != 2) {  // unrolled, the second half is still at hand
+          // Raises the reference maximum and brings O to it; `e`: with e4m3 pages the exponent of O from here
+          // on (O is held in units of 2^e_ref).  The subtrahend of the weights' exponents.
+          auto reference = [&](float m_new, int e) -> float {
+            const bool raise = m_new > m_ref + kTau;
+            bool grown = false;
+            float alpha = raise ? ex2_approx(m_ref - m_new) : 1.0f;
+            if (raise) {
+              l *= alpha;
+              lr *= alpha;
+              m_ref = m_new;
+            }
+            if constexpr (Q8) {
+              grown = j > j0 && e > e_ref;
+              if (grown) alpha = e - e_ref > 126 ? 0.f : alpha * __int_as_float((127 + e_ref - e) << 23);
+              e_ref = e;
+            }
+            if ((__any_sync(kFull, raise) || grown) && j > j0) {
+              // the commit that signalled this S covers the group's previous P.V
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tO + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                tmem_st32(tO + c, o);
+              }
+              tmem_wait_st();
+            }
+            return (m_ref == -INFINITY ? 0.f : m_ref) - kShift;
+          };
+          // the largest of n scores
+          auto largest = [&](const auto& s) -> float {
+            constexpr int n = sizeof(s) / 4;
+            float mx8[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) mx8[x] = fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 8]));
+#pragma unroll
+            for (int c = 16; c < n; c += 16)
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                mx8[x] = fmax3(mx8[x], __uint_as_float(s[c + x]), __uint_as_float(s[c + 8 + x]));
+            return fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+          };
+          auto mask = [&](auto& s, int base) {
+            constexpr int n = sizeof(s) / 4;
+            const int lim = vis_hi - k0 - base, first = vis_lo - k0 - base;
+#pragma unroll
+            for (int c = 0; c < n; ++c)
+              if (c > lim || c < first) s[c] = __float_as_uint(-INFINITY);
+          };
+          if constexpr (!Q8) {
+            // the whole row in registers
+            uint32_t s[kBN], p[kBN / 2];
+#pragma unroll
+            for (int c = 0; c < kBN; c += 32) tmem_ld32(tS + c, s + c);
+            tmem_wait_ld();
+            if (masked) mask(s, 0);
+            const float m_use = reference(largest(s) * c_tile, 0);
+            softmax_row<E, kBN>(s, p, c_tile, m_use, l, lr);
+            tmem_st32(tS + 64, p);
+            tmem_st32(tS + 96, p + 32);
+          } else {
+            // A row is taken in halves, first for its maximum and then for its weights, in one rolled loop:
+            // the roles' code together has to stay in the instruction cache (unrolled, with the conversion
+            // beside it, every warp ran two to three times slower).  P lies over the second half of S,
+            // which is read last before it is overwritten.
+            float mx = -INFINITY, m_use = 0.f;
+#pragma unroll 1
+            for (int pass = 0; pass < 4; ++pass) {
+              const int half = pass == 1 || pass == 2;
+              uint32_t s[64];
               tmem_ld32(tS + half * 64, s);
               tmem_ld32(tS + half * 64 + 32, s + 32);
               tmem_wait_ld();
-            }
-            if (masked && (Q8 || pass != 2)) {
-              const int lim = vis_hi - k0 - half * 64, first = vis_lo - k0 - half * 64;
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (c > lim || c < first) s[c] = __float_as_uint(-INFINITY);
-            }
-            if (pass < 2) {
-              float mx8[8];
-#pragma unroll
-              for (int x = 0; x < 8; ++x) mx8[x] = fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 8]));
-#pragma unroll
-              for (int c = 16; c < 64; c += 16)
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                  mx8[x] = fmax3(mx8[x], __uint_as_float(s[c + x]), __uint_as_float(s[c + 8 + x]));
-              mx = fmaxf(mx, fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-              if (pass == 0) continue;
-              const float m_new = mx * c_tile;
-              const bool raise = m_new > m_ref + kTau;
-              bool grown = false;  // the value exponent grew: O is held in units of 2^e_ref
-              float alpha = raise ? ex2_approx(m_ref - m_new) : 1.0f;
-              if (raise) {
-                l *= alpha;
-                lr *= alpha;
-                m_ref = m_new;
+              if (masked) mask(s, half * 64);
+              if (pass < 2) {
+                mx = fmaxf(mx, largest(s));
+                if (pass == 1) m_use = reference(mx * c_tile, sm.scales[grp][ss].e);
+              } else {
+                uint32_t p[32];
+                softmax_row<Elem::kF16, 64>(s, p, c_tile, m_use, l, lr);
+                tmem_st32(tS + 64 + half * 32, p);
               }
-              if constexpr (Q8) {
-                const int e = sm.scales[grp][ss].e;
-                grown = j > j0 && e > e_ref;
-                if (grown) alpha = e - e_ref > 126 ? 0.f : alpha * __int_as_float((127 + e_ref - e) << 23);
-                e_ref = e;
-              }
-              if ((__any_sync(kFull, raise) || grown) && j > j0) {
-                // the commit that signalled this S covers the group's previous P.V
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                  uint32_t o[32];
-                  tmem_ld32(tO + c, o);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-                  tmem_st32(tO + c, o);
-                }
-                tmem_wait_st();
-              }
-              m_use = (m_ref == -INFINITY ? 0.f : m_ref) - kShift;
-            } else {
-              uint32_t p[32];
-              softmax_row<Q8 ? Elem::kF16 : E, 64>(s, p, c_tile, m_use, l, lr);
-              tmem_st32(tS + 64 + half * 32, p);
             }
           }
           tmem_wait_st();
