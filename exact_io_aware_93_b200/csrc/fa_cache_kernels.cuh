@@ -103,6 +103,9 @@ struct RopeRow {
   }
 };
 
+// 16384 tokens of 32 heads of 128 rotated, 268 MB moved: 46.5 us (5.8 TB/s); plain instead of evict-first
+// loads and stores: 48.
+//
 // Rows of whole 16-element items (R and d multiples of 16, 16-byte aligned rows): a thread
 // owns one item of a head for several rows, 32 bytes in and out per row, and issues four
 // rows' loads before it needs the first.  The block's cos/sin are computed once per token and
@@ -313,6 +316,9 @@ __device__ __forceinline__ int e4m3_exponent(float amax) {
   return E == Elem::kF16 ? min(max(e, -15), 8) : min(max(e, -126), 119);
 }
 
+// 32768 tokens of 8 heads of 128, 16-bit pages, 268 MB moved by each: append and gather 45 us (6.0 TB/s).
+// (Evict-first loads and stores, or loads alone: 1 to 2 us slower.)
+//
 // Appends rows of the new keys and values at their positions: the last position of a sequence is
 // seqlens[b] - 1.  A warp takes 2^lg rows (a lane finds where one lies) and its lanes 16 elements of
 // a head each, the rows of one head side by side: their slots, and the scales, are neighbours in a
