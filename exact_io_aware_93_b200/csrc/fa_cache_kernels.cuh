@@ -46,13 +46,27 @@ constexpr int kRopeThreads = 256;
 constexpr double kInv2Pi = 0.15915494309189535;     // 1 / (2 pi) to 53 bits, and the rest
 constexpr double kInv2PiLo = -9.839338337591243e-18;
 
-// cos and sin of every pair of the block's tokens: tab[0][token][j], tab[1][token][j].
-__device__ __forceinline__ void rope_table(const RopeArgs& a, int64_t t0, int nt, float* tab) {
+// Batch row and place in it of token `add` after (b, n).
+struct RopeToken {
+  int b;
+  unsigned n;
+  __device__ __forceinline__ RopeToken(const RopeArgs& a, int b0, int n0, int add)
+      : b(b0), n(static_cast<unsigned>(n0) + add) {
+    if (n >= static_cast<unsigned>(a.N)) {
+      b += static_cast<int>(n / a.N);
+      n %= a.N;
+    }
+  }
+};
+
+// cos and sin of every pair of the block's tokens, (b, n) the first: tab[0][token][j], tab[1][token][j].
+__device__ __forceinline__ void rope_table(const RopeArgs& a, int b, int n, int nt, float* tab) {
   const int half = a.rd >> 1;
   for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
-    const int64_t t = t0 + i / half;
-    const int j = i % half;
-    const int64_t at = (t / a.N) * a.ps[0] + (t % a.N) * a.ps[1];
+    const int tk = i / half;
+    const int j = i - tk * half;
+    const RopeToken t(a, b, n, tk);
+    const int64_t at = t.b * a.ps[0] + t.n * a.ps[1];
     const double p = a.pos64 ? static_cast<double>(static_cast<const long long*>(a.pos)[at])
                              : static_cast<double>(static_cast<const int*>(a.pos)[at]);
     // p * f / (2 pi) modulo 1 with the roundings of both products carried along: at p = 2^31
@@ -81,7 +95,7 @@ struct RopeRow {
   int tk, h;  // this row's token, from that one on, and head among the block's
   int dt, dh; // what a step adds
   __device__ __forceinline__ RopeRow(const RopeArgs& a, int64_t t0, int nh, int row, int step)
-      : b(static_cast<int>(t0 / a.N)), n(static_cast<int>(t0 - static_cast<int64_t>(b) * a.N)), tk(row / nh),
+      : b(a.B == 1 ? 0 : static_cast<int>(t0 / a.N)), n(static_cast<int>(t0 - static_cast<int64_t>(b) * a.N)), tk(row / nh),
         h(row - tk * nh), dt(step / nh), dh(step - dt * nh) {}
   __device__ __forceinline__ void next(int nh) {
     tk += dt;
@@ -93,18 +107,13 @@ struct RopeRow {
   }
   // Element offset of head `head` of all (q's, then k's); w says which.
   __device__ __forceinline__ int64_t offset(const RopeArgs& a, const int64_t (&st)[2][3], int head, int w) const {
-    int bb = b;
-    unsigned nn = static_cast<unsigned>(n) + tk;
-    if (nn >= static_cast<unsigned>(a.N)) {
-      bb += static_cast<int>(nn / a.N);
-      nn %= a.N;
-    }
-    return bb * st[w][0] + nn * st[w][1] + (head - (w ? a.H : 0)) * st[w][2];
+    const RopeToken t(a, b, n, tk);
+    return t.b * st[w][0] + t.n * st[w][1] + (head - (w ? a.H : 0)) * st[w][2];
   }
 };
 
-// 16384 tokens of 32 heads of 128 rotated, 268 MB moved: 46.5 us (5.8 TB/s); plain instead of evict-first
-// loads and stores: 48.
+// 16384 tokens of 32 heads of 128 rotated, 268 MB moved: 45.3 us (5.9 TB/s); plain instead of evict-first
+// loads and stores: 47.
 //
 // Rows of whole 16-element items (R and d multiples of 16, 16-byte aligned rows): a thread
 // owns one item of a head for several rows, 32 bytes in and out per row, and issues four
@@ -147,7 +156,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) fa_rope_kernel(const RopeArgs
     }
   };
   load(r0);  // in flight while the table is computed
-  rope_table(a, t0, nt, tab);
+  rope_table(a, in.b, in.n, nt, tab);
   __syncthreads();
   for (int base = r0; r0 < step && base < rows; base += U * step) {
     if (base != r0) load(base);
@@ -204,11 +213,11 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_any_kernel(const RopeArg
   const int nt = left < a.tokens_per_block ? static_cast<int>(left) : a.tokens_per_block;
   const int h0 = blockIdx.y * a.heads_per_block;
   const int nh = min(a.heads_per_block, a.H + a.Hk - h0);
-  rope_table(a, t0, nt, tab);
+  RopeRow at(a, t0, nh, 0, 1);
+  rope_table(a, at.b, at.n, nt, tab);
   __syncthreads();
   const int per = a.d - half;  // pairs, then copied columns
   const int rows = nt * nh;
-  RopeRow at(a, t0, nh, 0, 1);
   for (int i = threadIdx.x; i < rows * per; i += kRopeThreads) {
     const int row = i / per;
     const int e = i - row * per;
