@@ -168,7 +168,7 @@ def _stream_ptr(t: torch.Tensor) -> int:
 def _on(t: torch.Tensor):
     """Make t's device current for a library call: the library takes its SM count, kernel
     set-up and status word from the current device, and launches on that device's stream."""
-    return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+    return _HERE if t.get_device() == torch._C._cuda_getDevice() else torch.cuda.device(t.device)
 
 
 def validate_inputs(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor) -> None:
@@ -433,13 +433,13 @@ def _rope(q, k, positions, inv_freq, interleaved, factor, q_out, k_out, inverse)
     if k is not None:
         _check_heads("k", k, q)
         k_shape = k.shape
-        if len(k_shape) != len(shape) or k_shape[:-2] != shape[:-2] or k_shape[-1] != shape[-1]:
+        if len(k_shape) != len(shape) or (*k_shape[:-2], shape[-2], k_shape[-1]) != shape:
             raise ValueError(f"k {tuple(k_shape)} does not fit q {tuple(shape)}")
     elif k_out is not None:
         raise ValueError("k_out without k")
     lead, d = shape[:-2], shape[-1]
-    if (not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64)
-            or positions.get_device() != device or positions.shape not in (lead, lead[-1:])):
+    if (not isinstance(positions, torch.Tensor) or positions.dtype not in _INTS
+            or positions.get_device() != device or (positions.shape != lead and positions.shape != lead[-1:])):
         raise ValueError(f"positions must be int32 or int64 of shape {tuple(lead)} or {tuple(lead[-1:])} on {q.device}")
     if (not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1
             or inv_freq.get_device() != device or not inv_freq.is_contiguous()
@@ -499,6 +499,7 @@ def rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, positions: torch.Tensor,
 
 _SCALE_TYPES = (torch.float8_e8m0fnu, torch.uint8)
 _INT32 = (torch.int32,)
+_INTS = (torch.int32, torch.int64)
 
 
 def _is(t, shape, dtypes, device: int) -> bool:

@@ -306,6 +306,49 @@ def test_captured_graph_replayed_as_the_batch_changes(quant):
         assert torch.equal(out[0], out[1]) and torch.equal(lse[0], lse[1])
 
 
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("new,lens", KINDS)
+def test_captured_behind_copies_and_other_streams(new, lens, quant):
+    """In a graph behind a memory copy, behind a kernel, and where two streams join: the call waits
+    for what it reads each time."""
+    s = build(new, lens, 8, 2, 128, 32, BF, quant, seed=18)
+    want, want_l = attend(s)
+    torch.cuda.synchronize()
+    live = dict(s, q=torch.zeros_like(s["q"]), seqlens=torch.zeros_like(s["seqlens"]))
+    side = torch.cuda.Stream()
+    big = torch.empty(1 << 26, device="cuda")
+    graphs = []
+    for before in ("copy", "kernel", "join"):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            main = torch.cuda.current_stream()
+            if before == "join":
+                side.wait_stream(main)
+                with torch.cuda.stream(side):
+                    big.add_(1.0)
+                    live["seqlens"].copy_(s["seqlens"])
+            big.mul_(0.5)                                    # long enough to be still running
+            if before != "join":
+                live["seqlens"].copy_(s["seqlens"])
+            if before == "copy":
+                live["q"].copy_(s["q"])
+            else:
+                torch.add(s["q"], 0.0, out=live["q"])
+            if before == "join":
+                main.wait_stream(side)
+            out = attend(live)
+            live["q"].zero_()
+            live["seqlens"].zero_()
+        graphs.append((g, out))
+    for _ in range(2):
+        for g, (o, lse) in graphs:
+            o.fill_(-1.0)
+            g.replay()
+            torch.cuda.synchronize()
+            assert api.get_status_site() == (0, 0)
+            assert torch.equal(o, want) and torch.equal(lse, want_l)
+
+
 def test_two_streams_at_once():
     """Calls in flight on two streams, and on one that is not the tensors' own, each with its own
     workspace."""
