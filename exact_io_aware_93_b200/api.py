@@ -559,7 +559,8 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     lies in page page_table[b, p // page] (int32 [B, max_pages]) at slot p % page of the pools
     [P, H_kv, page, d].  Pools of float8_e4m3fn take codes with one power-of-two scale per row in
     ``k_scales`` / ``v_scales`` (float8_e8m0fnu [P, H_kv, page]).  Everything but the shapes is read
-    on the device; bad positions and page numbers skip their row and set the status word."""
+    on the device; bad positions and page numbers skip their row and set the status word.  The pools
+    overlap neither each other nor the new rows."""
     for name, t in (("k", k), ("v", v)):
         _check_heads(name, t, k)
         if t.dim() != 3 or t.shape != k.shape:
@@ -595,7 +596,8 @@ def cache_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch
     """(k, v) [total, H_kv, d] read back from a paged cache via ``fa_cache_gather``: row cu_k[b] + i is
     position starts[b] + i of sequence b (``starts`` None: from 0).  Rows whose position is at or past
     seqlens[b], and rows behind cu_k[B], are left as they were.  ``dtype`` is the type of the values
-    read from e4m3 pages (bfloat16 when not given); 16-bit pages are read as they are."""
+    read from e4m3 pages (bfloat16 when not given); 16-bit pages are read as they are.  Given outputs
+    overlap neither each other nor the pools."""
     if dtype is None:
         is8 = isinstance(k_pages, torch.Tensor) and k_pages.dtype == torch.float8_e4m3fn
         dtype = torch.bfloat16 if is8 or not isinstance(k_pages, torch.Tensor) else k_pages.dtype
@@ -661,7 +663,9 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     contiguous columns): one token (decoding), a few (drafted tokens) or a chunk of a prompt, mixed
     freely.  With ``causal`` its token i stands at position seqlens[b] - n_b + i and sees the keys at
     or before it, with ``window`` no more than that many back; without, all seqlens[b] keys.  A token
-    that sees no key gets O = 0 and LSE = -inf; rows behind cu_q[B] are left as they were."""
+    that sees no key gets O = 0 and LSE = -inf; rows behind cu_q[B] are left as they were.  Given
+    outputs and a given workspace (``paged_workspace_size`` bytes, for calls that do not overlap in time)
+    lie apart from what the call reads and from each other."""
     _check_heads("q", q)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, d]")
