@@ -9,7 +9,9 @@ A model used past the length it was trained on scales them:
   bands   by the turns r a pair makes over ``trained`` positions: kept for r >= high, divided by
           ``scale`` for r <= low, blended linearly in r between
   yarn    the same idea blended linearly in the pair's index, between the indices that make
-          ``high`` and ``low`` turns, with the amplitude factor 0.1 ln(scale) + 1
+          ``high`` and ``low`` turns (rounded outwards, kept within 0 and rotary_dim - 1: the end
+          may lie behind the last pair), with the amplitude factor 0.1 ln(scale) + 1
+          (YaRN: Efficient Context Window Extension of Large Language Models, 2023)
 """
 from __future__ import annotations
 
@@ -53,7 +55,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | None
         def index(turns):  # the (fractional) pair that makes this many turns over `trained`
             return rotary_dim * math.log(trained / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
         first = max(math.floor(index(high)), 0)
-        last = min(math.ceil(index(low)), rotary_dim // 2 - 1)
+        last = min(math.ceil(index(low)), rotary_dim - 1)
         ramp = ((j - first) / max(last - first, 0.001)).clamp(0.0, 1.0)
         freq = (1.0 - ramp) * freq + ramp * freq / scale
         factor = 0.1 * math.log(scale) + 1.0

@@ -51,6 +51,26 @@ def test_yarn_ends_and_factor():
     assert torch.all(freq[1:] < freq[:-1])
 
 
+@pytest.mark.parametrize("dim,base,scale,trained,low,high", [
+    (128, 1e4, 16.0, 4096, 1.0, 32.0),                          # the slowest pair makes less than `low` turns
+    (128, 1e4, 4.0, 65536, 1.0, 32.0), (64, 1e4, 4.0, 65536, 1.0, 32.0),
+    (128, 1e4, 4.0, 131072, 1.0, 32.0), (64, 1e4, 4.0, 131072, 0.5, 64.0),   # and where it makes more
+    (64, 100.0, 2.0, 65536, 1.0, 32.0), (2, 1e4, 2.0, 65536, 1.0, 32.0)])    # the end's limit, rotary_dim - 1
+def test_yarn_blends_every_pair_by_the_definition(dim, base, scale, trained, low, high):
+    """Pair x makes `turns` turns over `trained` positions where trained base^(-2x / dim) = 2 pi turns;
+    the blend is linear in x from floor(x(high)) to ceil(x(low)), wherever the last pair is."""
+    freq, _ = f(dim, base=base, scaling="yarn", scale=scale, trained=trained, low=low, high=high)
+
+    def at(turns):
+        return dim / 2 * math.log(trained / (2 * math.pi * turns)) / math.log(base)
+    first, last = max(math.floor(at(high)), 0), min(math.ceil(at(low)), dim - 1)
+    for x in range(dim // 2):
+        part = min(max((x - first) / (last - first), 0.0), 1.0) if last > first else float(x > first)
+        plain = base ** (-2.0 * x / dim)
+        want = plain * (1.0 - part) + plain / scale * part
+        assert freq[x].item() == pytest.approx(want, rel=1e-12), x
+
+
 @pytest.mark.parametrize("kw", [
     dict(rotary_dim=63), dict(rotary_dim=0), dict(rotary_dim=64, base=1.0), dict(rotary_dim=64, scale=0.5),
     dict(rotary_dim=64, scaling="other"), dict(rotary_dim=64, scaling="yarn", scale=2.0),
