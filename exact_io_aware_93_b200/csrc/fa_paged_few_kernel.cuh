@@ -600,8 +600,10 @@ __global__ void __launch_bounds__(384, 1)
               w[y] = p * vf;
             }
             // fp16, with three pieces rounded to 9 significant bits; its upper byte is the e5m2
-            // truncation, and each remainder is exact in fp16
-            uint32_t v = pack_f16x2(w[0], w[1]) + (Cfg::kPPieces == 3 ? 0x00020002u : 0u);
+            // truncation, and each remainder is exact in fp16.  The sum saturates at 0x7fff, which is
+            // what a NaN packs to.
+            uint32_t v = pack_f16x2(w[0], w[1]);
+            if constexpr (Cfg::kPPieces == 3) v = __vaddss2(v, 0x00020002u);
 #pragma unroll
             for (int piece = 0; piece < Cfg::kPPieces; ++piece) {
 #pragma unroll

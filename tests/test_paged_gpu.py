@@ -560,3 +560,26 @@ def test_offsets_past_32_bits():
     o, lse = attend(s)
     assert api.get_status() == 0
     check(s, o, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("new,lens", KINDS)
+@pytest.mark.parametrize("which", [0, 1])
+def test_nan_scales_reach_the_rows_that_see_them(new, lens, dtype, which):
+    """A scale byte of 255 makes its row NaN: every token of the sequence sees it, and other sequences
+    keep their bits.  A NaN value changes no log-sum."""
+    s = build(new, lens, 8, 2, 128, 32, dtype, True, seed=19)
+    want, want_l = attend(s)
+    hit = torch.zeros(sum(new), dtype=torch.bool, device="cuda")
+    for b in range(2 if new[1] > 1 else 1):
+        pg, slot = s["table"][b, 0].item(), 5 + b
+        s["scales"][which].view(torch.uint8)[pg, :, slot] = 255
+        hit[s["cu"][b]:s["cu"][b + 1]] = True
+    o, lse = attend(s)
+    assert api.get_status() == 0
+    assert torch.all(torch.isnan(o[hit])) and torch.equal(o[~hit], want[~hit])
+    assert torch.equal(lse[:, ~hit], want_l[:, ~hit])
+    if which == 0:
+        assert torch.all(torch.isnan(lse[:, hit]))
+    else:
+        assert torch.equal(lse, want_l)
