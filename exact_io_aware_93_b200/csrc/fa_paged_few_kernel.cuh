@@ -22,10 +22,9 @@
 //   Q   e4m3 pieces per row (fa_paged_scale_q_kernel), two of a bf16 and three of an fp16 row, as
 //       rows r, RW + r, .. of the tile: the score columns are added by the key's thread
 //   P   the weight, an fp16 value, is the sum of e5m2 pieces (e5m2 is the upper byte of an fp16):
-//       three hold 9 bits, one more than bf16, and four all 11, for fp16 outputs.  e5m2 and not
-//       e4m3 for its range: a long tail of small weights beside a large one keeps its mass.  The
-//       pieces are rows of P^T, their products columns of O^T,
-//       added at the end.
+//       three hold the 9 bits that it is rounded to, one more than bf16, and four all 11, for fp16
+//       outputs.  e5m2 and not e4m3 for its range: a long tail of small weights beside a large one
+//       keeps its mass.  The pieces are rows of P^T, their products columns of O^T, added at the end.
 //   scales  a key's 2^ek and 2^(ev - E) are one number each for its thread; E is the largest
 //       value exponent of the group's tiles so far (O^T is rescaled when it grows).  The bytes
 //       come with the K tile, into a ring of their own that the softmax groups free.
@@ -598,12 +597,14 @@ __global__ void __launch_bounds__(384, 1)
               const float p = ex2_approx(x[r + y] - (ref[r + y] == -INFINITY ? 0.f : ref[r + y]) + kPShift);
               l[r + y] += p;
               w[y] = p * vf;
+              // Three pieces hold 9 significant bits: rounded to the nearest, here, since l sums the
+              // weights before it (the pieces of an fp16 as they fall cut it off, by 3.2e-4 in the mean,
+              // up to 2.6e-3).  w + 2^15 w rounds at 2^-8 of w's power of two, and what is left of it
+              // without 2^15 w is exact.
+              if constexpr (Cfg::kPPieces == 3) w[y] = fmaf(w[y], -32768.f, fmaf(w[y], 32768.f, w[y]));
             }
-            // fp16, with three pieces rounded to 9 significant bits; its upper byte is the e5m2
-            // truncation, and each remainder is exact in fp16.  The sum saturates at 0x7fff, which is
-            // what a NaN packs to.
+            // fp16: its upper byte is the e5m2 truncation, and each remainder is exact in fp16
             uint32_t v = pack_f16x2(w[0], w[1]);
-            if constexpr (Cfg::kPPieces == 3) v = __vaddss2(v, 0x00020002u);
 #pragma unroll
             for (int piece = 0; piece < Cfg::kPPieces; ++piece) {
 #pragma unroll

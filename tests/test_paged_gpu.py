@@ -583,3 +583,29 @@ def test_nan_scales_reach_the_rows_that_see_them(new, lens, dtype, which):
         assert torch.all(torch.isnan(lse[:, hit]))
     else:
         assert torch.equal(lse, want_l)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("new,lens,h,hk", [
+    ([1] * 64, [300 + 9 * i for i in range(64)], 8, 1), ([2] * 32, [900 + 17 * i for i in range(32)], 8, 1),
+    ([5] * 8, [700 + 90 * i for i in range(8)], 32, 4)])
+def test_outputs_are_no_longer_or_shorter_than_they_should_be(new, lens, h, hk, dtype, quant):
+    """The factor c for which c times the fp64 result is nearest to O is 1: roundings of weights and
+    outputs are as often up as down.  Each of the 32768 or more elements is off by up to 2 2^-9 of
+    sqrt(mean O^2) (a weight's rounding to 9 bits and the output's to 8, both at most 2^-9; sums of many
+    values grow as O does), so that the mean of independent ones stays below 2^-12, 11 of its standard
+    deviations of at most 2^-8 / sqrt(32768)."""
+    d = 128
+    s = build(new, lens, h, hk, d, 64, dtype, quant, seed=20)
+    o, _ = attend(s, causal=False)
+    assert api.get_status() == 0
+    along, square, at = 0.0, 0.0, 0
+    for b, n in enumerate(new):
+        k, v = (s["values"][i][b].cuda().transpose(0, 1).repeat_interleave(h // hk, 0) for i in range(2))
+        x = s["q"][at:at + n].double().transpose(0, 1) @ k.transpose(1, 2) * d ** -0.5
+        want = torch.softmax(x, -1) @ v
+        along += ((o[at:at + n].double().transpose(0, 1) - want) * want).sum().item()
+        square += (want * want).sum().item()
+        at += n
+    assert abs(along / square) <= 2.0 ** -12
