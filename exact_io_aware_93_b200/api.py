@@ -13,6 +13,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import operator
 import os
 import struct
 
@@ -381,8 +382,28 @@ def _check_heads(name: str, t: torch.Tensor, like: torch.Tensor | None = None) -
 
 
 def _span(t: torch.Tensor) -> tuple[int, int]:
-    last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
+    shape, stride = t.shape, t.stride()
+    last = sum(map(operator.mul, shape, stride)) - sum(stride)
     return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _interleaved(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two tensors whose spans overlap have no element in common all the same, as slices of one
+    buffer do: then all of a and all of b lie in two parts of one period, a stride of a, once the
+    strides that are multiples of the period are left out."""
+    size = a.element_size()
+    gap = b.data_ptr() - a.data_ptr()
+    if b.element_size() != size or gap % size:
+        return False
+    gap //= size
+    dims = [list(zip(t.shape, t.stride())) for t in (a, b)]
+    for period in a.stride()[:-1]:
+        if period > 0:
+            room, more = [sum([(n - 1) * st for n, st in d if st % period], 1) for d in dims]
+            at = gap % period
+            if room <= at and at + more <= period:
+                return True
+    return False
 
 
 def _check_apart(name: str, out: torch.Tensor, *others: torch.Tensor | None) -> None:
@@ -395,24 +416,27 @@ def _check_apart(name: str, out: torch.Tensor, *others: torch.Tensor | None) -> 
                 raise ValueError(f"{name} must not overlap the call's other tensors")
 
 
-def _check_rope_out(name: str, out: torch.Tensor, x: torch.Tensor, *others: torch.Tensor) -> None:
-    """An output of rope: x's shape, no element twice, and either x itself or apart from it (a
-    partial overlap would be read after it is written)."""
+def _check_rope_out(name: str, out: torch.Tensor, x: torch.Tensor, *others: torch.Tensor | None) -> None:
+    """An output of rope: x's shape, no element twice, x itself or apart from it (a partial overlap
+    would be read after it is written), and apart from the others."""
     _check_heads(name, out, x)
-    if out.shape != x.shape:
-        raise ValueError(f"{name} must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
+    shape, stride = out.shape, out.stride()
+    if shape != x.shape:
+        raise ValueError(f"{name} must have shape {tuple(x.shape)}, got {tuple(shape)}")
     reach = 1
-    for st, n in sorted((st, n) for n, st in zip(out.shape, out.stride()) if n > 1):
+    for st, n in sorted((st, n) for n, st in zip(shape, stride) if n > 1):
         if st < reach:
             raise ValueError(f"{name} must not overlap itself")
         reach = st * (n - 1) + reach
-    if out.data_ptr() == x.data_ptr() and out.stride() == x.stride():
-        if any(t.data_ptr() == x.data_ptr() for t in others if t is not None):
-            raise ValueError(f"{name} must not be another input too")
-        return
-    for t in (x, *others):
-        if t is not None and _span(out)[0] < _span(t)[1] and _span(t)[0] < _span(out)[1]:
-            raise ValueError(f"{name} must be its input itself or lie apart from the inputs")
+    lo = out.data_ptr()
+    hi = lo + reach * out.element_size()
+    if out is not x and (lo != x.data_ptr() or stride != x.stride()):
+        others = (x, *others)
+    for t in others:
+        if t is not None and t.numel() and out.numel():
+            first, end = _span(t)
+            if lo < end and first < hi and not _interleaved(out, t):
+                raise ValueError(f"{name} must be its input itself or lie apart from the inputs and the other output")
 
 
 def _empty_like(t: torch.Tensor) -> torch.Tensor:
@@ -450,9 +474,9 @@ def _rope(q, k, positions, inv_freq, interleaved, factor, q_out, k_out, inverse)
     if k is not None and k_out is None:
         k_out = _empty_like(k)
     if given[0] is not None:
-        _check_rope_out("q_out", q_out, q, k)
+        _check_rope_out("q_out", q_out, q, k, None if k_out is k else k_out)
     if given[1] is not None:
-        _check_rope_out("k_out", k_out, k, q)
+        _check_rope_out("k_out", k_out, k, None if q_out is q else q)
     if q.numel() == 0 and (k is None or k.numel() == 0):
         return q_out, k_out
     B, N = (1, shape[0]) if len(shape) == 3 else (shape[0], shape[1])
@@ -485,7 +509,9 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_f
     q is [T, H, d] or [B, N, H, d] and k the same with its own heads (or None), bfloat16 or
     float16, with any strides but contiguous columns (slices of a fused projection).
     ``positions`` is int32 or int64 of the leading shape, or [N] for every batch row;
-    ``inv_freq`` is float64 (``rotary.rope_frequencies``).  Outputs may be the inputs themselves."""
+    ``inv_freq`` is float64 (``rotary.rope_frequencies``).  An output may be its input itself; apart
+    from that, given outputs share no element with each other or with q and k (slices of one buffer
+    may interleave)."""
     return _rope(q, k, positions, inv_freq, interleaved, factor, q_out, k_out, False)
 
 

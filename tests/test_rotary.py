@@ -1,6 +1,9 @@
 """Rotary frequencies (host side): closed forms, limits of the scalings, refusals; and the
 binding's refusals, which come before any device work."""
+import contextlib
+import itertools
 import math
+import random
 
 import pytest
 import torch
@@ -129,3 +132,66 @@ def test_buffers_that_overlap():
     api._check_apart("out", k, v, None, rows, rows[:0])
     with pytest.raises(ValueError):
         api._check_apart("out", k, rows, buf[1:3])
+
+
+class _Reached(Exception):
+    """The library would have been called."""
+
+
+def _no_device(monkeypatch):
+    """The binding's checks on CPU tensors: only where a tensor lies is overlooked."""
+    def reached():
+        raise _Reached
+    monkeypatch.setattr(api, "_check_heads", lambda *a: None)
+    monkeypatch.setattr(api, "_on", lambda t: contextlib.nullcontext())
+    monkeypatch.setattr(api, "_stream_ptr", lambda t: 0)
+    monkeypatch.setattr(api, "lib", reached)
+
+
+def _rotate(q, k, q_out=None, k_out=None):
+    api.rope(q, k, torch.arange(q.shape[-3]), f(64)[0], q_out=q_out, k_out=k_out)
+
+
+def test_rope_outputs_that_overlap_each_other_or_an_input(monkeypatch):
+    _no_device(monkeypatch)
+    x = torch.zeros(8, 8, 64, dtype=torch.bfloat16)
+    fused, other = x.clone(), torch.zeros(8, 8, 64, dtype=torch.bfloat16)
+    q, k = fused[:, :4], fused[:, 4:8]
+    heads = torch.zeros(2, 6, 8, 64, dtype=torch.bfloat16).transpose(1, 2)          # [B, N, H, d] of [B, H, N, d]
+    for q_, k_, qo, ko in (
+            (q, k, q, k), (q, k, None, None), (q, k, q, None), (q, k, None, k),    # in place, whole or in part
+            (q, k, other[:, :4], other[:, 4:]), (q, k, other[:, 4:], other[:, :4]), (q, k, other[:, :4], k),
+            (x[:4], x[4:], x[:4], x[4:]), (x[:1, :3], x[:1, 3:6], x[:1, :3], x[:1, 3:6]),
+            (heads[:, :, :4], heads[:, :, 4:], heads[:, :, :4], heads[:, :, 4:]),
+            (x.view(2, 4, 8, 64)[:, :, :5], x.view(2, 4, 8, 64)[:, :, 5:], x.view(2, 4, 8, 64)[:, :, :5], None),
+            (x[:, 1:1], x[:, :2], None, x[:, :2]), (x[:, :2], x[:, 1:1], x[:, :2], x[:, 1:1]), (q, None, q, None)):
+        with pytest.raises(_Reached):
+            _rotate(q_, k_, qo, ko)
+    for q_, k_, qo, ko in (
+            (q, k, other[:, :4], other[:, :4]),                                     # one buffer for both
+            (q, k, other[:, :4], other[:, 2:6]), (q, k, q, q), (q, k, k, None),
+            (x[:, :4], x[:, 2:6], x[:, :4], x[:, 2:6]),                             # inputs that share heads, in place
+            (x[:, :4], x[:, 2:6], x[:, :4], None), (x[:, :4], x[:, 2:6], None, x[:, 2:6]),
+            (x[:, :4], x[:, 3:], x[:, :4], other[:, 3:]),
+            (x[:4, :4], x[3:7, :4], x[:4, :4], other[:4, :4]),                      # or a token
+            (heads[:, :, :4], heads[:, :, 3:6], heads[:, :, :4], None)):
+        with pytest.raises(ValueError):
+            _rotate(q_, k_, qo, ko)
+
+
+def test_interleaved_slices_have_no_element_in_common():
+    """Whatever the strides: where slices are taken for interleaved, no offset is in both."""
+    rng = random.Random(7)
+    buf, found = torch.zeros(4096, dtype=torch.bfloat16), 0
+    strides = [0, 1, 2, 3, 4, 6, 8, 12, 24, 48, 96, 7]
+    for _ in range(20000):
+        pair = []
+        for _ in range(2):
+            shape = [rng.randint(1, 4) for _ in range(3)] + [rng.randint(1, 6)]
+            pair.append(torch.as_strided(buf, shape, [rng.choice(strides) for _ in range(3)] + [1], rng.randint(0, 120)))
+        if api._interleaved(*pair):
+            found += 1
+            at = [{t.storage_offset() + sum(i * s for i, s in zip(ix, t.stride()))
+                   for ix in itertools.product(*map(range, t.shape))} for t in pair]
+            assert not at[0] & at[1], [(t.shape, t.stride(), t.storage_offset()) for t in pair]
+    assert found > 500
