@@ -566,8 +566,8 @@ def _check_pools(a: torch.Tensor, b: torch.Tensor, *rows: torch.Tensor) -> None:
     if abs(pa - pb) < nbytes:
         raise ValueError("the pools of keys and values must not overlap")
     for t in rows:
-        at = t.data_ptr()
-        if pa <= at < pa + nbytes or pb <= at < pb + nbytes:
+        lo, hi = _span(t)
+        if t.numel() and (lo < pa + nbytes and pa < hi or lo < pb + nbytes and pb < hi):
             raise ValueError("new keys and values must not lie in the pools")
 
 

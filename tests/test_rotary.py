@@ -195,3 +195,19 @@ def test_interleaved_slices_have_no_element_in_common():
                    for ix in itertools.product(*map(range, t.shape))} for t in pair]
             assert not at[0] & at[1], [(t.shape, t.stride(), t.storage_offset()) for t in pair]
     assert found > 500
+
+
+def test_new_rows_that_run_into_a_pool():
+    flat = torch.zeros(8192, dtype=torch.bfloat16)
+    a, b = flat[2048:4096].view(2, 1, 16, 64), flat[6144:].view(2, 1, 16, 64)
+    for first, t, apart in ((0, 16, True), (0, 17, False), (1920, 1, True), (1984, 1, False), (2048, 1, False),
+                            (3968, 1, False), (4032, 1, True), (4096, 16, True), (4096, 17, False)):
+        rows = torch.as_strided(flat, (t, 1, 64), (128, 64, 1), first + 64)     # the second half of each 128
+        if apart:
+            api._check_pools(a, b, flat[:64].view(1, 1, 64), rows)
+        else:
+            with pytest.raises(ValueError):
+                api._check_pools(a, b, flat[:64].view(1, 1, 64), rows)
+            with pytest.raises(ValueError):
+                api._check_pools(b, a, rows)
+    api._check_pools(a, b, flat[2112:2112].view(0, 1, 64))
