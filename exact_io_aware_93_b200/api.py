@@ -382,9 +382,11 @@ def _check_heads(name: str, t: torch.Tensor, like: torch.Tensor | None = None) -
 
 
 def _span(t: torch.Tensor) -> tuple[int, int]:
+    at = t.data_ptr()
+    if t.is_contiguous():
+        return at, at + t.numel() * t.element_size()
     shape, stride = t.shape, t.stride()
-    last = sum(map(operator.mul, shape, stride)) - sum(stride)
-    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+    return at, at + (sum(map(operator.mul, shape, stride)) - sum(stride) + 1) * t.element_size()
 
 
 def _interleaved(a: torch.Tensor, b: torch.Tensor) -> bool:
@@ -406,14 +408,20 @@ def _interleaved(a: torch.Tensor, b: torch.Tensor) -> bool:
     return False
 
 
-def _check_apart(name: str, out: torch.Tensor, *others: torch.Tensor | None) -> None:
+def _spans(*tensors: torch.Tensor | None) -> list[tuple[int, int]]:
+    return [_span(t) for t in tensors if t is not None and t.numel()]
+
+
+def _check_spans(name: str, out: torch.Tensor, spans: list[tuple[int, int]]) -> None:
     """A caller's output that the call would write while it still reads, or writes, one of the others."""
     lo, hi = _span(out)
-    for t in others:
-        if t is not None and t.numel() and out.numel():
-            first, end = _span(t)
-            if lo < end and first < hi:
-                raise ValueError(f"{name} must not overlap the call's other tensors")
+    for first, end in spans:
+        if lo < end and first < hi and out.numel():
+            raise ValueError(f"{name} must not overlap the call's other tensors")
+
+
+def _check_apart(name: str, out: torch.Tensor, *others: torch.Tensor | None) -> None:
+    _check_spans(name, out, _spans(*others))
 
 
 def _check_rope_out(name: str, out: torch.Tensor, x: torch.Tensor, *others: torch.Tensor | None) -> None:
@@ -623,7 +631,7 @@ def cache_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch
     position starts[b] + i of sequence b (``starts`` None: from 0).  Rows whose position is at or past
     seqlens[b], and rows behind cu_k[B], are left as they were.  ``dtype`` is the type of the values
     read from e4m3 pages (bfloat16 when not given); 16-bit pages are read as they are.  Given outputs
-    overlap neither each other nor the pools."""
+    overlap neither each other nor what the call reads."""
     if dtype is None:
         is8 = isinstance(k_pages, torch.Tensor) and k_pages.dtype == torch.float8_e4m3fn
         dtype = torch.bfloat16 if is8 or not isinstance(k_pages, torch.Tensor) else k_pages.dtype
@@ -646,7 +654,7 @@ def cache_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch
     for name, out, other in (("k_out", given[0], v_out), ("v_out", given[1], k_out)):
         if out is not None:
             check_buffer(name, out, shape, dtype, k_pages.device)
-            _check_apart(name, out, other, k_pages, v_pages, k_scales, v_scales)
+            _check_apart(name, out, other, k_pages, v_pages, k_scales, v_scales, page_table, seqlens, cu_k, starts)
     if total == 0:
         return k_out, v_out
     p = _pack_cache(B, total, H_kv, d, P, max_pages, page, FA_DTYPE[dtype], 1 if quant else 0, 0, 0, 0, 0)
@@ -703,16 +711,19 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
                          "(key/value heads must divide the query heads)")
     if not _is(cu_q, (page_table.shape[0] + 1,), _INT32, device):
         check_buffer("cu_q", cu_q, (page_table.shape[0] + 1,), torch.int32, q.device)
+    spans = None
+    if out is not None or lse is not None or workspace is not None:
+        spans = _spans(q, k_pages, v_pages, k_scales, v_scales, page_table, seqlens, cu_q)
     if out is None:
         out = _empty_like(q)
     else:
         check_buffer("out", out, q.shape, q.dtype, q.device)
-        _check_apart("out", out, q, k_pages, v_pages, k_scales, v_scales)
+        _check_spans("out", out, spans)
     if lse is None:
         lse = q.new_empty((H, T), dtype=torch.float32)
     else:
         check_buffer("lse", lse, (H, T), torch.float32, q.device)
-        _check_apart("lse", lse, out, q, k_pages, v_pages, k_scales, v_scales)
+        _check_spans("lse", lse, spans + [_span(out)])
     if T == 0:
         return out, lse
     p = _paged_problem(q, k_pages, page_table, max_q, causal, scale, window, quant)
@@ -722,7 +733,7 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
             workspace = q.new_empty(max(need, 1), dtype=torch.uint8)
         else:
             check_scratch("workspace", workspace, q.device)
-            _check_apart("workspace", workspace, q, out, lse)
+            _check_spans("workspace", workspace, spans + [_span(out), _span(lse)])
         st = lib().fa_paged(p, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
                             _ptr(v_scales), page_table.data_ptr(), seqlens.data_ptr(), cu_q.data_ptr(),
                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
