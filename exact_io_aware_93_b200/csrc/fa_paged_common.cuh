@@ -128,6 +128,11 @@ __device__ __forceinline__ bool pg_seq_ok(const PgArgs& a, int b) {
   return c0 >= 0 && c1 >= c0 && c1 <= a.T && c1 - c0 <= a.max_q && len >= 0 && len <= a.max_pages * a.page;
 }
 
+// The first key that the window leaves a token at position `pos` (negative: before the sequence's first).
+__device__ __forceinline__ int pg_first_key(const PgArgs& a, int pos) {
+  return a.window >= 0 && pos > a.window ? pos - a.window : 0;
+}
+
 // Keys [lo, hi) that the tokens at positions p0 .. p1 of a sequence of `len` keys see, and the
 // key tiles that hold them.
 struct PgKeys {
@@ -136,7 +141,7 @@ struct PgKeys {
 __device__ __forceinline__ PgKeys pg_keys(const PgArgs& a, int len, int p0, int p1) {
   PgKeys k;
   k.hi = a.causal ? min(p1 + 1, len) : len;
-  k.lo = a.window >= 0 ? max(0, p0 - a.window) : 0;
+  k.lo = pg_first_key(a, p0);
   if (k.hi <= k.lo) k.hi = k.lo = 0;
   k.t0 = k.lo >> 7;
   k.t1 = (k.hi + 127) >> 7;

@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(384, 1)
       const int nt = g.nt, kt0 = g.kt0;
       // every row sees the keys from all_lo to all_hi
       const int all_hi = a.causal ? g.pos0 : g.len - 1;
-      const int all_lo = a.window >= 0 ? g.pos0 + g.ntok - 1 - a.window : 0;
+      const int all_lo = pg_first_key(a, g.pos0 + g.ntok - 1);
       float ref[RW], l[RW], lr[RW], c_row[Q8 ? RW : 1];
 #pragma unroll
       for (int r = 0; r < RW; ++r) {
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int r = 0; r < RW; ++r) {
             const int pos = g.pos0 + i;
             const int hi = a.causal ? min(pos, g.len - 1) : g.len - 1;
-            const int lo = a.window >= 0 ? pos - a.window : 0;
+            const int lo = pg_first_key(a, pos);
             if (key > hi || key < lo) x[r] = -INFINITY;
             if (++h == G) h = 0, ++i;
           }

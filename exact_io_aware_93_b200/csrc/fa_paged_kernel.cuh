@@ -609,10 +609,10 @@ __global__ void __launch_bounds__(PgCfg<D, E, Q8>::kThreads, 1)
         const int iq = rc < M ? rc / G : 0;
         const int qpos = g.pos0 + tok + iq;
         vis_hi = rc < M ? (a.causal ? min(qpos, g.len - 1) : g.len - 1) : -1;
-        vis_lo = a.window >= 0 ? qpos - a.window : 0;
+        vis_lo = pg_first_key(a, qpos);
         // every row of the tile sees the keys from all_lo to all_hi
         all_hi = a.causal ? g.pos0 + tok : g.len - 1;
-        all_lo = a.window >= 0 ? g.pos0 + tok + M / G - 1 - a.window : 0;
+        all_lo = pg_first_key(a, g.pos0 + tok + M / G - 1);
         if constexpr (Q8) {
           if (rc < M && FA_IN_BOUNDS(g.q0 + tok + iq < a.T, status, 512))
             c_row *= __ldg(a.q_scale + (static_cast<int64_t>(g.q0) + tok + iq) * a.H + g.kvh * G + rc - iq * G);

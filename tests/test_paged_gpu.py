@@ -609,3 +609,17 @@ def test_outputs_are_no_longer_or_shorter_than_they_should_be(new, lens, h, hk, 
         square += (want * want).sum().item()
         at += n
     assert abs(along / square) <= 2.0 ** -12
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("new,lens", [([5, 2, 1], [2, 900, 0]), ([400, 90], [300, 20]), ([300, 1, 64], [250, 900, 3])])
+def test_the_widest_window_is_none(new, lens, quant):
+    """More new tokens than keys, so that some stand before the first position; a window that reaches
+    past any cache hides nothing."""
+    s = build(new, lens, 8, 2, 64, 32, BF, quant, seed=22)
+    want, want_l = attend(s)
+    check(s, want, want_l)
+    for window in (2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 301, 10 ** 6):
+        o, lse = attend(s, window=window)
+        assert api.get_status() == 0
+        assert torch.equal(o, want) and torch.equal(lse, want_l), window
