@@ -195,7 +195,8 @@ struct BwdPtrs {
 template <fa::Elem E>
 fa_status dispatch_bwd(DeviceInfo& di, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                        const CUtensorMap& mdo, const BwdPtrs& x, const fa_problem& p, cudaStream_t s) {
-  const int B = p.B, H = p.H, H_kv = p.H_kv, N = p.N, w = p.window;
+  const int B = p.B, H = p.H, H_kv = p.H_kv, N = p.N;
+  const int w = p.window < N ? p.window : N;  // wider hides nothing, and key + window stays in range
   if (p.d == 128)
     return p.causal ? launch_bwd<128, true, E>(di, mq, mk, mv, mdo, x.o, x.dO, x.lse, x.dq, x.dk, x.dv, x.ws, B, H,
                                                H_kv, N, w, p.scale, s)

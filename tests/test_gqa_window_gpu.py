@@ -56,3 +56,21 @@ def test_ex_argument_checks():
     with pytest.raises(api.FAError) as e:
         api.fwd(q, q, q, causal=False, window=8)  # a window needs causal masking
     assert e.value.status == 1
+
+
+@pytest.mark.parametrize("N", [100, 300])
+def test_the_widest_window_is_none(N):
+    """Windows up to 2^31 - 1 give what no window gives, bit for bit (dQ, whose key blocks are added in
+    any order, where there is one)."""
+    inp = make_inputs(1, 4, N, 64, seed=9300 + N, with_do=True, H_kv=2)
+    q, k, v, do = (inp[n].cuda() for n in ("q", "k", "v", "do"))
+    o, lse = api.fwd(q, k, v, causal=True)
+    want = api.bwd(q, k, v, o, do, lse, causal=True)
+    for window in (N - 1, N, 2 ** 31 - 300, 2 ** 31 - 1):
+        o2, l2 = api.fwd(q, k, v, causal=True, window=window)
+        got = api.bwd(q, k, v, o, do, lse, causal=True, window=window)
+        torch.cuda.synchronize()
+        assert api.get_status() == 0
+        assert torch.equal(o2, o) and torch.equal(l2, lse)
+        for i in (0, 1, 2) if N <= 128 else (1, 2):
+            assert torch.equal(got[i], want[i]), (window, i)
