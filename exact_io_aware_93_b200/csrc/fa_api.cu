@@ -280,7 +280,7 @@ fa_status launch_decode(DeviceInfo& di, const CUtensorMap& mq, const CUtensorMap
   a.H_kv = p.H_kv;
   a.N_q = p.N_q;
   a.N_kv = p.N_kv;
-  a.window = p.window;
+  a.window = p.window < p.N_kv ? p.window : p.N_kv;  // wider hides nothing, and position - window stays in range
   a.causal = p.causal;
   a.R = R;
   a.scale_log2 = p.scale * 1.4426950408889634f;

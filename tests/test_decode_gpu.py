@@ -114,3 +114,16 @@ def test_decode_workload_sampled(name):
     pairs += [(0, 0), (w.B - 1, w.H - 1)]
     eo, el = decode_errors(inp, o, lse, w.scale, w.causal, w.window, heads=pairs)
     assert eo <= O_TOL and el <= LSE_TOL, (eo, el)
+
+
+def test_the_widest_window_is_none():
+    """Windows up to 2^31 - 1 give what none gives, bit for bit, also for sequences with fewer cached
+    positions than new queries."""
+    inp = make_decode_inputs(4, 8, 2, 5, 700, 64, seed=77, lengths=[700, 2, 0, 5], tail_nan=True)
+    q, k, v, sl = (inp[n].cuda() for n in ("q", "k", "v", "seqlens"))
+    want, want_l = api.decode(q, k, v, sl)
+    for window in (700, 10 ** 6, 2 ** 31 - 3, 2 ** 31 - 1):
+        o, lse = api.decode(q, k, v, sl, window=window)
+        torch.cuda.synchronize()
+        assert api.get_status() == 0
+        assert torch.equal(o, want) and torch.equal(lse, want_l), window
