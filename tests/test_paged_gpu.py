@@ -623,3 +623,58 @@ def test_the_widest_window_is_none(new, lens, quant):
         o, lse = attend(s, window=window)
         assert api.get_status() == 0
         assert torch.equal(o, want) and torch.equal(lse, want_l), window
+
+
+def _many(kind):
+    if kind == "tiles":                                                       # 160 rows and fewer, none
+        new = [20 - i % 7 * 3 if i % 11 else 0 for i in range(140)]
+        return new, [n + 37 * (i % 23) for i, n in enumerate(new)]
+    if kind == "chunks apart":                                                # behind 32, 64, .. others and beside them
+        new = [150] + [1] * 31 + [40] + [1] * 70 + [0] * 40 + [60, 1, 33] + [2] * 200 + [90]
+    else:                                                                     # none at the ends
+        new = [0] * 33 + [1] * 64 + [25] * 3 + [0] + [1] * 32 + [50] + [1] * 31 + [0] * 70
+    return new, [n + (29 * i) % 400 for i, n in enumerate(new)]
+
+
+@pytest.mark.parametrize("dtype,quant", [(BF, False), (BF, True), (FP, True)])
+@pytest.mark.parametrize("kind", ["tiles", "chunks apart", "chunks inside"])
+def test_hundreds_of_sequences(kind, dtype, quant):
+    new, lens = _many(kind)
+    s = build(new, lens, 8, 1 if kind == "tiles" else 2, 64, 16, dtype, quant, seed=23)
+    o, lse = attend(s)
+    torch.cuda.synchronize()
+    assert api.get_status_site() == (0, 0)
+    check(s, o, lse)
+
+
+def test_single_tokens_between_chunks_cost_what_they_cost_behind_them():
+    """2048 sequences of one token between two chunks, and the same behind both: the same work, so the
+    shortest of 20 runs in turn differ by noise, far below the quarter allowed (stepping over the
+    sequences between two of a CTA's chunks one at a time added half)."""
+    hk, page, d, n = 8, 64, 64, 2048
+    runs = []
+    for order in ([0] + [2] * n + [1], [0, 1] + [2] * n):
+        new, lens = ([(500, 500, 1)[i] for i in order], [(900, 900, 64)[i] for i in order])
+        need = torch.tensor([-(-m // page) for m in lens])
+        first = need.cumsum(0) - need
+        table = (first[:, None] + torch.arange(int(need.max()))).to(torch.int32).cuda()     # past a length: anyone's
+        pages = [torch.ones(int(need.sum()), hk, page, d, dtype=BF, device="cuda") for _ in "kv"]
+        q = torch.ones(sum(new), 4 * hk, d, dtype=BF, device="cuda")
+        args = (q, *pages, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), offsets(new).cuda(), max(new))
+        api.paged_attention(*args)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = api.paged_attention(*args)
+        runs.append((g, args, out, []))
+    for _ in range(20):
+        for g, _, _, times in runs:
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            g.replay()
+            end.record()
+            torch.cuda.synchronize()
+            times.append(start.elapsed_time(end))
+    assert api.get_status() == 0
+    for _, _, (o, _), _ in runs:
+        assert torch.all(o == 1.0)
+    assert min(runs[0][3]) <= 1.25 * min(runs[1][3]), [min(r[3]) for r in runs]
