@@ -48,7 +48,8 @@ namespace fa {
 
 // Over e4m3 pages a score may exceed its row's reference maximum m by 2^2 (16-bit pages: kTau, 2^8)
 // before m is raised, and weights are 2^(x - m + 13) <= 2^15: they are cut off at e5m2's 2^-16,
-// 2^-29 of the reference weight, far below what a long tail of small weights adds up to.
+// 2^-29 of the reference weight, far below what a long tail of small weights adds up to.  The weight
+// carries its key's value scale, 2^(ev - E): a row that far below the largest is cut off that much earlier.
 constexpr float kTauCodes = 2.0f;
 constexpr float kCodesShift = 13.0f;
 

@@ -320,9 +320,9 @@ typedef struct fa_rope_problem {
 
 /*
  *   q, k         : in,  [B, N, H, d] and [B, N, H_k, d] with the given strides
- *   q_out, k_out : out, the same shapes; each may be its input (same pointer and strides),
- *                  any other overlap is not supported
- *   positions    : in,  DEVICE int32 / int64, any sign
+ *   q_out, k_out : out, the same shapes; each may be its input (same pointer and strides); any
+ *                  other element in common, of the two outputs too, is not supported
+ *   positions    : in,  DEVICE int32 / int64, any sign, below 2^53 in size
  *   inv_freq     : in,  DEVICE fp64 [rotary_dim / 2], radians per position
  * Pointers need the alignment of their element; rows that are 16-byte aligned with d and
  * rotary_dim multiples of 16 take the fast path.  Errors: FA_ERR_INVALID_ARG,
@@ -440,7 +440,12 @@ size_t fa_paged_workspace_size(const fa_paged_problem* problem);
  * token of the sequence sees through the window, may hold anything, and page_table entries of
  * pages that hold only such positions too; key and value rows that some new token sees are
  * expected to be finite (a NaN or infinity there reaches the rows that see it, and may reach
- * others of the same sequence).  A chunk longer than max_q is cut to it, a length is cut to the
+ * others of the same sequence; so does a scale byte of 255).  Over e4m3 pages the rows that one SM
+ * works through for a sequence share a unit 2^E, the largest value scale met so far.  A value row of
+ * scale 2^e is held exactly down to e = E - 15 in tiles of 128 query rows, to 8 bits of its largest down to
+ * E - 24, and counts as zero below; with up to 16 query rows its weight is cut off at 2^(E - e - 29) of
+ * the row's reference weight, which is at most the largest.  Keys in tiles of 128 are held likewise
+ * against the largest key scale of their 128.  A chunk longer than max_q is cut to it, a length is cut to the
  * table's capacity, a page number outside [0, P) reads as zeros (with scale 1): each records FA_ERR_PLAN.
  * Deterministic for fixed inputs and device.  All device-side values are read by the kernels:
  * a captured graph can be replayed as they change, within B, T and max_q.
@@ -475,8 +480,9 @@ fa_status fa_selftest_bounds(void* stream);
 /*
  * Synchronises `stream`, then returns and clears the device status word of the
  * current device: FA_OK, FA_ERR_TIMEOUT if a kernel gave up a bounded wait since the
- * last call, or (checking build) FA_ERR_BOUNDS if a bounds check failed.  Returns FA_ERR_DEVICE if the stream or device reports a
- * CUDA error.
+ * last call, FA_ERR_PLAN if a paged call met a length, offset or page number out of range, or
+ * (checking build) FA_ERR_BOUNDS if a bounds check failed.  Returns FA_ERR_DEVICE if the stream
+ * or device reports a CUDA error.
  */
 fa_status fa_get_status(void* stream);
 
