@@ -427,10 +427,11 @@ def _check_apart(name: str, out: torch.Tensor, *others: torch.Tensor | None) -> 
 def _check_rope_out(name: str, out: torch.Tensor, x: torch.Tensor, *others: torch.Tensor | None) -> None:
     """An output of rope: x's shape, no element twice, x itself or apart from it (a partial overlap
     would be read after it is written), and apart from the others."""
-    _check_heads(name, out, x)
+    if out is not x:
+        _check_heads(name, out, x)
+        if out.shape != x.shape:
+            raise ValueError(f"{name} must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
     shape, stride = out.shape, out.stride()
-    if shape != x.shape:
-        raise ValueError(f"{name} must have shape {tuple(x.shape)}, got {tuple(shape)}")
     reach = 1
     for st, n in sorted((st, n) for n, st in zip(shape, stride) if n > 1):
         if st < reach:
@@ -568,14 +569,15 @@ def _check_pages(k_pages, v_pages, page_table, seqlens, k_scales, v_scales, dtyp
     return quant
 
 
-def _check_pools(a: torch.Tensor, b: torch.Tensor, *rows: torch.Tensor) -> None:
-    """Pools that are written: apart from each other and from the rows written to them."""
+def _check_pools(a: torch.Tensor, b: torch.Tensor, *rows) -> None:
+    """Pools that are written: apart from each other and from the rows written to them (tensors, or
+    spans known already)."""
     nbytes, pa, pb = a.numel() * a.element_size(), a.data_ptr(), b.data_ptr()
     if abs(pa - pb) < nbytes:
         raise ValueError("the pools of keys and values must not overlap")
     for t in rows:
-        lo, hi = _span(t)
-        if t.numel() and (lo < pa + nbytes and pa < hi or lo < pb + nbytes and pb < hi):
+        lo, hi = t if type(t) is tuple else _span(t)
+        if lo < hi and (lo < pa + nbytes and pa < hi or lo < pb + nbytes and pb < hi):
             raise ValueError("new keys and values must not lie in the pools")
 
 
@@ -586,7 +588,8 @@ def _ptr(t: torch.Tensor | None):
 def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                  page_table: torch.Tensor, seqlens: torch.Tensor, cu_q: torch.Tensor,
                  k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None) -> None:
-    """Write new keys and values [T, H_kv, d] into a paged cache via ``fa_cache_append``.
+    """Write new keys and values [T, H_kv, d] (any strides but contiguous columns and rows aligned to 16
+    bytes) into a paged cache via ``fa_cache_append``.
 
     Sequence b owns rows cu_q[b] .. cu_q[b + 1] (int32 [B + 1]), the last of its seqlens[b]
     positions (int32 [B], the new rows included); rows behind cu_q[B] are not written.  Position p
@@ -607,15 +610,17 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
         raise ValueError(f"k {tuple(k.shape)} does not fit pages {tuple(k_pages.shape)} on {k_pages.device}")
     if not _is(cu_q, (B + 1,), _INT32, k.get_device()):
         check_buffer("cu_q", cu_q, (B + 1,), torch.int32, k.device)
-    _check_pools(k_pages, v_pages, k, v)
-    if quant:
-        _check_pools(k_scales, v_scales, k, v)
     if T == 0:
         return
-    p = _pack_cache(B, T, H_kv, d, P, max_pages, page, FA_DTYPE[k.dtype], 1 if quant else 0, *k.stride()[:2],
-                    *v.stride()[:2])
+    (k_tok, k_head, _), (v_tok, v_head, _), kp, vp = k.stride(), v.stride(), k.data_ptr(), v.data_ptr()
+    rows = ((kp, kp + 2 * ((T - 1) * k_tok + (H_kv - 1) * k_head + d)),
+            (vp, vp + 2 * ((T - 1) * v_tok + (H_kv - 1) * v_head + d)))
+    _check_pools(k_pages, v_pages, *rows)
+    if quant:
+        _check_pools(k_scales, v_scales, *rows)
+    p = _pack_cache(B, T, H_kv, d, P, max_pages, page, FA_DTYPE[k.dtype], 1 if quant else 0, k_tok, k_head, v_tok, v_head)
     with _on(k):
-        st = lib().fa_cache_append(p, k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        st = lib().fa_cache_append(p, kp, vp, k_pages.data_ptr(), v_pages.data_ptr(),
                                    _ptr(k_scales), _ptr(v_scales), page_table.data_ptr(), seqlens.data_ptr(),
                                    cu_q.data_ptr(), _stream_ptr(k))
     if st != 0:
@@ -694,8 +699,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     paged caches (``cache_append``'s layout), via ``fa_paged``.
 
     Sequence b owns tokens cu_q[b] .. cu_q[b + 1] of q [T, H, d] (at most ``max_q``, any strides but
-    contiguous columns): one token (decoding), a few (drafted tokens) or a chunk of a prompt, mixed
-    freely.  With ``causal`` its token i stands at position seqlens[b] - n_b + i and sees the keys at
+    contiguous columns and rows aligned to 16 bytes): one token (decoding), a few (drafted tokens) or a
+    chunk of a prompt, mixed freely.  With ``causal`` its token i stands at position seqlens[b] - n_b + i and sees the keys at
     or before it, with ``window`` no more than that many back; without, all seqlens[b] keys.  A token
     that sees no key gets O = 0 and LSE = -inf; rows behind cu_q[B] are left as they were.  Given
     outputs and a given workspace (``paged_workspace_size`` bytes, for calls that do not overlap in time)
