@@ -32,7 +32,7 @@
 // its softmax and its products in turn.)
 //
 // Bound by device memory: 16 sequences of 16-32K tokens, 32 heads sharing 8, d 128, one new token each:
-// 230 us over 16-bit pages (6.5 TB/s), 135 us over e4m3 pages (5.6 TB/s).  Pages of 16 e4m3 slots are boxes
+// 230 us over 16-bit pages (6.5 TB/s), 132 us over e4m3 pages (5.7 TB/s).  Pages of 16 e4m3 slots are boxes
 // of 2 KB and stream at three quarters of that.  What does not grow with the cache, 17 us: launch and plan
 // 3, the first tile 4, a segment's end 2.5, the join 5.
 //

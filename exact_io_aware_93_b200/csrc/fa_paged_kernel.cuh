@@ -24,9 +24,9 @@
 // warps 12-15 the conversion.
 //
 // Bound by the chain scores, softmax, weights, products of a tile, as the forward kernel: 2048 new tokens
-// at 32K, 32 heads sharing 8, d 128, 16-bit pages 1016 us (1048 TFLOP/s) in a short run, 1.15 to 1.19 ms
-// under the power cap; with 2 key/value heads, whose pages stay in L2, 1109 TFLOP/s.  e4m3 pages: 1217 us
-// (875 TFLOP/s), bound by the conversion and the three converted tiles that fit.
+// at 32K, 32 heads sharing 8, d 128, 16-bit pages 1.15 to 1.19 ms under the power cap (895 to 925 TFLOP/s),
+// 1016 us (1048) in a short run; there, with 2 key/value heads, whose pages stay in L2, 1109 TFLOP/s, and
+// over e4m3 pages 1217 us (875), bound by the conversion and the three converted tiles that fit.
 //
 // Tensor memory: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [256+D,256+2D); P
 // overwrites the second half of S.
